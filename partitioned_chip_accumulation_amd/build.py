@@ -8,6 +8,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -15,16 +17,16 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libpca_hist.so")
 SOURCES = ["hist_api.hip", "hist_bench.hip", "hist_tune.hip", "hist_static.hip",
-           "hist_model.hip"]
+           "hist_model.hip", "experts_group.hip", "experts_combine.hip", "experts_matmul.hip"]
+JOBS = 6  # compilers at one time
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Wall",
-    # packed fp32 instructions stay off (the kernels are integer-only anyway)
+    # packed fp32 instructions stay off
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
 
@@ -34,10 +36,7 @@ def hipcc() -> str:
     return os.path.join(rocm, "bin", "hipcc")
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIBRARY + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC,
-           *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp]
+def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -47,6 +46,17 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("hipcc failed:\n" + "\n".join(errors))
     if verbose and errors:
         print("\n".join(errors), file=sys.stderr)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every source (several at a time) and link the library."""
+    tmp = LIBRARY + ".tmp"
+    with tempfile.TemporaryDirectory() as d, ThreadPoolExecutor(JOBS) as pool:
+        objects = [os.path.join(d, s + ".o") for s in SOURCES]
+        list(pool.map(lambda so: _run(
+            [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c",
+             os.path.join(CSRC, so[0]), "-o", so[1]], verbose), zip(SOURCES, objects)))
+        _run([hipcc(), "--offload-arch=gfx950", "-shared", *objects, "-o", tmp], verbose)
     os.replace(tmp, LIBRARY)
     return LIBRARY
 

@@ -1,0 +1,263 @@
+// experts_tile.hpp -- one tile of a matrix product on the matrix cores: staging
+// of its operands in LDS, the fragments read from there, and the tile's place
+// in the ragged list of the experts' rows.
+//
+// A tile is D[m][n] = sum_r A[m][r] B[n][r]. An operand lies in memory either
+// along the reduction (kAlong: a row of memory is one m or n, its elements
+// consecutive r) or across it (kAcross: a row of memory is one r, its
+// elements consecutive m or n). Both are staged in steps of 128 bytes of
+// reduction (64 16-bit elements, 128 8-bit ones):
+//
+//   kAlong   [rows][128 bytes]; a lane's fragment is one 16-byte read.
+//   kAcross  [64][columns]; a lane's fragment is two transposing 8-byte reads.
+//
+// The fragments go to the matrix instruction with B first, so that a lane
+// holds four consecutive columns n of one row m of the result.
+#pragma once
+
+#include "experts_common.hpp"
+
+namespace pca_experts {
+
+constexpr uint32_t kStepBytes = 128;
+
+// What one matrix instruction takes and gives, by element type.
+template <class T> struct Mma;
+template <> struct Mma<__bf16> {
+    typedef bf16x8 Frag;
+    typedef f32x4 Acc;
+    static __device__ __forceinline__ Acc run(Frag a, Frag b, Acc c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <> struct Mma<_Float16> {
+    typedef f16x8 Frag;
+    typedef f32x4 Acc;
+    static __device__ __forceinline__ Acc run(Frag a, Frag b, Acc c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+};
+template <> struct Mma<int8_t> {
+    typedef s32x4 Frag;
+    typedef s32x4 Acc;
+    static __device__ __forceinline__ Acc run(Frag a, Frag b, Acc c)
+    {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+    }
+};
+
+// 16 bytes at p, of which only the first `left` belong to the row; the others
+// read 0. Any alignment of T.
+template <class T>
+__device__ __forceinline__ u32x4 load16(const char *p, int left)
+{
+    if (left >= 16) return load_any<u32x4>(p);
+    u32x4 v = {0, 0, 0, 0};
+    constexpr int kEach = 16 / sizeof(T);
+    constexpr uint32_t kMask = sizeof(T) == 1 ? 0xffu : 0xffffu;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        if (i * (int)sizeof(T) < left) {
+            uint32_t e;
+            if constexpr (sizeof(T) == 1) e = *(const uint8_t *)(p + i);
+            else e = load_any<uint16_t>(p + i * 2);
+            v[i * sizeof(T) / 4] |= (e & kMask) << (i * sizeof(T) * 8 % 32);
+        }
+    }
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// Staging. A thread moves kLoads 16-byte pieces of the operand per step; piece
+// i * THREADS + thread goes to that place in LDS, and the place in the row
+// that it comes from is permuted so that the fragments' reads meet no bank
+// twice.
+
+// Along the reduction: ROWS rows of 128 bytes. Eight pieces a row, piece s of
+// row r holding the row's bytes 16 * (s ^ (r >> 1) % 8).
+template <class T, int ROWS, int THREADS>
+struct Along {
+    static constexpr bool kAcross = false;
+    static constexpr int kLoads = ROWS * 8 / THREADS;
+    static constexpr uint32_t kBytes = ROWS * kStepBytes;
+    static_assert(ROWS * 8 % THREADS == 0 && THREADS / 8 % 16 == 0, "pieces of one permutation");
+    const char *row[kLoads];
+    uint32_t at;  // this thread's byte within a row's step
+    u32x4 v[kLoads];
+
+    // row_of(r): the address of row r's first element, for r < ROWS.
+    template <class F>
+    __device__ __forceinline__ void init(F row_of)
+    {
+        const uint32_t r = threadIdx.x / 8;
+        at = ((threadIdx.x % 8) ^ ((r >> 1) & 7)) * 16;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) row[i] = row_of(i * (THREADS / 8) + r);
+    }
+    __device__ __forceinline__ void fetch(uint32_t step, uint32_t bytes)
+    {
+        const uint32_t from = step * kStepBytes + at;
+        const int left = (int)bytes - (int)from;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) v[i] = load16<T>(row[i] + from, left);
+    }
+    __device__ __forceinline__ void store(char *lds) const
+    {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            *(u32x4 *)(lds + (i * THREADS + threadIdx.x) * 16) = v[i];
+    }
+    // Fragment of rows [first, first + 16), reduction part kk (64 bytes).
+    static __device__ __forceinline__ typename Mma<T>::Frag frag(const char *lds, uint32_t first,
+                                                                 uint32_t kk)
+    {
+        const uint32_t lane = threadIdx.x % 64, r = first + lane % 16;
+        const uint32_t piece = (lane / 16 + 4 * kk) ^ ((r >> 1) & 7);
+        return *(const typename Mma<T>::Frag *)(lds + r * kStepBytes + piece * 16);
+    }
+};
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// Across the reduction: 64 rows of COLS 16-bit elements. The 32-byte parts of
+// row r are permuted by part ^ h(r), h(r) = r % 4 + 4 * (r / 8 % 2): the 16 lanes of
+// a transposing read take 32 bytes from each of four rows, and the eight rows
+// that half a wave takes then lie in eight different bank groups.
+template <class T, int COLS, int THREADS>
+struct Across {
+    static constexpr bool kAcross = true;
+    static constexpr int kRows = kStepBytes / 2;
+    static constexpr int kPieces = COLS / 8;  // of one row
+    static constexpr int kLoads = kRows * kPieces / THREADS;
+    static constexpr int kRowsEach = THREADS / kPieces;  // rows between a thread's pieces
+    static constexpr uint32_t kBytes = kRows * COLS * 2;
+    static_assert(kRowsEach % 16 == 0 && COLS % 128 == 0, "pieces of one permutation");
+    int left;      // bytes of the row from this thread's column on
+    uint32_t col;  // byte offset of this thread's column
+    u32x4 v[kLoads];
+
+    static __device__ __forceinline__ uint32_t mix(uint32_t r)
+    {
+        return (r & 3) | ((r >> 1) & 4);
+    }
+    static __device__ __forceinline__ uint32_t row_of(int i)
+    {
+        return i * kRowsEach + threadIdx.x / kPieces;
+    }
+    // cols: columns of the operand that are left from the tile's first one.
+    __device__ __forceinline__ void init(int cols)
+    {
+        const uint32_t r = threadIdx.x / kPieces;
+        col = ((threadIdx.x % kPieces) ^ (mix(r) << 1)) * 16;
+        left = cols * 2 - (int)col;
+    }
+    // address(r): the tile's first column in row r of this step, or nullptr
+    // for a row past the end (which reads 0).
+    template <class F>
+    __device__ __forceinline__ void fetch(F address)
+    {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const char *p = address(row_of(i));
+            v[i] = load16<T>(p + col, p ? left : 0);
+        }
+    }
+    __device__ __forceinline__ void store(char *lds) const
+    {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            *(u32x4 *)(lds + (i * THREADS + threadIdx.x) * 16) = v[i];
+    }
+    static __device__ __forceinline__ typename Mma<T>::Frag frag(const char *lds, uint32_t first,
+                                                                 uint32_t kk)
+    {
+        const uint32_t lane = threadIdx.x % 64, i = lane % 16;
+        const uint32_t r = kk * 32 + lane / 16 * 8 + i / 4;  // mix(r) == mix(r + 4)
+        const char *p = lds + r * (COLS * 2) + ((first / 16) ^ mix(r)) * 32 + i % 4 * 8;
+        union {
+            s16x4 half[2];
+            typename Mma<T>::Frag whole;
+        } f;
+        f.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+        f.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * COLS * 2));
+        return f.whole;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// The list of tiles. Group g of the sorted rows is expert g's, g = experts the
+// rows past the last kept one (their results are zero). The tiles of one
+// group come together, its row tiles within 8 of them fastest, so that tiles
+// that run at one time share rows and weights in the L2.
+struct Tile {
+    uint32_t group;  // > experts: no such tile
+    uint32_t begin;  // the group's rows are [begin, end)
+    uint32_t end;
+    uint32_t m;      // row tile within the group
+    uint32_t n;      // column tile
+};
+
+// Workgroups go to the 8 XCDs in turn: `span` consecutive tiles go to one.
+__device__ __forceinline__ uint32_t tile_of_block(uint32_t block, uint32_t span)
+{
+    const uint32_t xcd = block % 8, i = block / 8;
+    return (i / span * 8 + xcd) * span + i % span;
+}
+
+// offsets == nullptr: one group of all rows. Every wave finds the tile by
+// itself: 64 groups at a time, the scan of their row tiles, and a ballot.
+__device__ __forceinline__ Tile find_tile(uint32_t tile, const int32_t *__restrict__ offsets,
+                                          uint32_t experts, uint32_t rows, uint32_t rows_log2,
+                                          uint32_t n_tiles)
+{
+    Tile t;
+    uint32_t m_tiles = 0, before = 0;
+    const uint32_t want = tile / n_tiles;  // row tiles before, over all groups
+    if (!offsets) {
+        t.group = 0;
+        t.begin = 0;
+        t.end = rows;
+        m_tiles = (rows + (1u << rows_log2) - 1) >> rows_log2;
+        if (want >= m_tiles) t.group = experts + 1;
+    } else {
+        const uint32_t lane = threadIdx.x % 64;
+        t.group = experts + 1;
+        t.begin = t.end = 0;
+        for (uint32_t g0 = 0; g0 <= experts; g0 += 64) {
+            const uint32_t g = g0 + lane;
+            uint32_t b = 0, e = 0;
+            if (g <= experts) {
+                b = (uint32_t)offsets[g];
+                e = g < experts ? (uint32_t)offsets[g + 1] : rows;
+                e = e > rows ? rows : e;
+                b = b > e ? e : b;
+            }
+            const uint32_t mine = (e - b + (1u << rows_log2) - 1) >> rows_log2;
+            const uint32_t upto = pca::wave_inclusive_scan(mine);
+            const uint64_t past = __ballot(before + upto > want);
+            if (past) {
+                const int at = __builtin_ctzll(past);
+                t.group = g0 + at;
+                t.begin = __builtin_amdgcn_readlane(b, at);
+                t.end = __builtin_amdgcn_readlane(e, at);
+                m_tiles = __builtin_amdgcn_readlane(mine, at);
+                before += __builtin_amdgcn_readlane(upto, at) - m_tiles;
+                break;
+            }
+            before += __builtin_amdgcn_readlane(upto, 63);
+        }
+    }
+    if (t.group <= experts) {
+        const uint32_t i = tile - before * n_tiles;
+        const uint32_t eight = i / (8 * n_tiles), r = i - eight * 8 * n_tiles;
+        const uint32_t high = m_tiles - eight * 8 < 8 ? m_tiles - eight * 8 : 8;
+        t.m = eight * 8 + r % high;
+        t.n = r / high;
+    }
+    return t;
+}
+
+}  // namespace pca_experts
