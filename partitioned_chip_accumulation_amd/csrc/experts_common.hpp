@@ -6,13 +6,11 @@
 #include <stdint.h>
 
 #include "experts.h"
-#include "hist_common.hpp"
 #include "hist_host.hpp"
 
 namespace pca_experts {
 
-using pca::u32x4;
-
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t s32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -62,6 +60,25 @@ __device__ __forceinline__ void store8(T *p, typename Vec8<T>::type v, int left)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < left) p[i] = v[i];
+}
+
+__device__ __forceinline__ void lds_add(uint32_t *lds, uint32_t slot, uint32_t v)
+{
+    __hip_atomic_fetch_add(lds + slot, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+
+// Inclusive sum over the wave's lanes, all of them active: within rows of 16
+// lanes by row shifts, then lane 15 of each row into the next and lane 31 into
+// the upper half (DPP, no LDS round trip).
+__device__ __forceinline__ uint32_t wave_inclusive_scan(uint32_t v)
+{
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, true);   // row_shr:1
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, true);   // row_shr:2
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, true);   // row_shr:4
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, true);   // row_shr:8
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false);  // row_bcast:15
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false);  // row_bcast:31
+    return v;
 }
 
 __device__ __forceinline__ float wave_sum_f(float v)

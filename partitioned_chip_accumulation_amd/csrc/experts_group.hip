@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) k_group_count(const I *__restrict__ 
         const uint32_t i = blockIdx.x * chunk + r + threadIdx.x;
         if (i < pairs) {
             const uint32_t e = expert_of(ids, i, experts);
-            if (e < experts) pca::lds_add(hist, e, 1u);
+            if (e < experts) lds_add(hist, e, 1u);
         }
     }
     __syncthreads();
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads)
         const uint32_t i = first + r + lane;
         if (i < pairs) {
             const uint32_t e = expert_of(ids, i, experts);
-            if (e < experts) pca::lds_add(mine, e, 1u);
+            if (e < experts) lds_add(mine, e, 1u);
         }
     }
     __syncthreads();
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads)
             for (uint32_t w = 0; w < kWaves; ++w) total += wave_at[w * experts + e];
         }
     }
-    const uint32_t inclusive = pca::wave_inclusive_scan(total);
+    const uint32_t inclusive = wave_inclusive_scan(total);
     if (lane == 63) wave_total[wave] = inclusive;
     __syncthreads();
     uint32_t start = inclusive - total, kept = 0;

@@ -236,7 +236,7 @@ __device__ __forceinline__ Tile find_tile(uint32_t tile, const int32_t *__restri
                 b = b > e ? e : b;
             }
             const uint32_t mine = (e - b + (1u << rows_log2) - 1) >> rows_log2;
-            const uint32_t upto = pca::wave_inclusive_scan(mine);
+            const uint32_t upto = wave_inclusive_scan(mine);
             const uint64_t past = __ballot(before + upto > want);
             if (past) {
                 const int at = __builtin_ctzll(past);

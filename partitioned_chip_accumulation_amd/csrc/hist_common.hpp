@@ -1,5 +1,6 @@
 // hist_common.hpp -- shared pieces of the gfx950 kernels of the partitioned LDS
-// histogram: the input view, wave and LDS helpers and the wave hot slot. Part of libpca_hist.so (see hist_kernels.hpp for the
+// histogram: the input view, wave and LDS helpers, the wave hot slot, and the
+// zero-fill kernel. Part of libpca_hist.so (see hist_kernels.hpp for the
 // overview).
 #pragma once
 
@@ -176,6 +177,15 @@ __device__ __forceinline__ void zero_lds(uint32_t *lds, uint32_t len)
     u32x4 *l4 = reinterpret_cast<u32x4 *>(lds);
     const uint32_t len4 = (len + 3) >> 2;
     for (uint32_t i = threadIdx.x; i < len4; i += WG) l4[i] = u32x4{0u, 0u, 0u, 0u};
+}
+
+// ---------------------------------------------------------------------------
+// Fill counts with zeros (n == 0).
+__global__ void k_fill_zero(uint32_t *__restrict__ dst, uint64_t len)
+{
+    for (uint64_t i = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; i < len;
+         i += (uint64_t)gridDim.x * blockDim.x)
+        dst[i] = 0u;
 }
 
 }  // namespace pca

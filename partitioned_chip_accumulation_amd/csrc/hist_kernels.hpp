@@ -38,15 +38,3 @@
 #include "hist_sweep.hpp"
 #include "hist_scatter.hpp"
 #include "hist_stream.hpp"
-
-namespace pca {
-
-// Fill counts with zeros (n == 0).
-__global__ void k_fill_zero(uint32_t *__restrict__ dst, uint64_t len)
-{
-    for (uint64_t i = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; i < len;
-         i += (uint64_t)gridDim.x * blockDim.x)
-        dst[i] = 0u;
-}
-
-}  // namespace pca
