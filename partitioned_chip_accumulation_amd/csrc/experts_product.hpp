@@ -1,0 +1,751 @@
+// experts_product.hpp -- the kernels of the expert layer's matrix products and how
+// they are launched. Part of libpca_hist.so.
+#pragma once
+
+#include "experts_tile.hpp"
+
+#include <type_traits>
+
+namespace pca_experts {
+
+// The tile: 128 x 128 results by four waves of 64 x 64 each.
+constexpr int kTile = 128;
+constexpr int kThreads = 256;
+constexpr int kPart = 64;         // rows and columns of one wave
+constexpr int kFrags = kPart / 16;
+
+struct RowsArgs {
+    char *out;
+    const char *a;
+    const char *b;
+    int64_t ldo, lda, ldb, b_stride;  // bytes
+    const int32_t *offsets;           // nullptr: one group
+    const int32_t *order;             // nullptr: row p of a belongs to row p
+    const float *sa, *sb;             // 8-bit operands' scales
+    uint32_t rows, a_rows, experts;
+    uint32_t cols;   // of the result
+    uint32_t bytes;  // of the reduction
+    uint32_t n_tiles, span;
+    Divide divide;  // by top_k
+};
+
+// The row of a that sorted row p reads; a bad index reads row 0 (the row's
+// place in the result is still its own).
+__device__ __forceinline__ uint32_t source_row(const RowsArgs &g, uint32_t p)
+{
+    if (!g.order) return p;
+    const uint32_t t = g.divide((uint32_t)g.order[p]);
+    return t < g.a_rows ? t : 0;
+}
+
+// A wave's fragments, FM x FN of 16 x 16 results, to memory: through LDS, so that
+// whole rows of the wave's part leave together, 16 bytes a lane (stored as they
+// lie in registers, 8 bytes a lane, a store touched 16 pieces of 32 bytes).
+// value(i, j): the four results of fragment (i, j) in this lane, columns lane / 16 * 4
+// + 0..3 of row lane % 16. out: the part's first element, `high` rows and `wide`
+// columns of it exist. lds: the wave's own FM * FN * 512 bytes.
+template <class O, int FM, int FN, class F>
+__device__ __forceinline__ void store_part(char *lds, O *out, int64_t ld_bytes, int high, int wide,
+                                           F value)
+{
+    typedef O O4 __attribute__((ext_vector_type(4)));
+    constexpr uint32_t kRow = FN * 32, kPieces = FN * 2;  // bytes and 16-byte pieces of a row
+    const uint32_t lane = threadIdx.x % 64;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const uint32_t r = i * 16 + lane % 16;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const f32x4 v = value(i, j);
+            const uint32_t c = j * 16 + lane / 16 * 4;
+            *(O4 *)(lds + r * kRow + ((c / 8) ^ (r % kPieces)) * 16 + c % 8 * 2) =
+                O4{(O)v[0], (O)v[1], (O)v[2], (O)v[3]};
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int s = 0; s < FM * 16 * (int)kPieces / 64; ++s) {
+        const uint32_t r = (s * 64 + lane) / kPieces, p = lane % kPieces;
+        const auto v = *(const typename Vec8<O>::type *)(lds + r * kRow + (p ^ (r % kPieces)) * 16);
+        const int left = wide - (int)p * 8;
+        if ((int)r < high && left > 0) store8((O *)((char *)out + r * ld_bytes) + p * 8, v, left);
+    }
+}
+
+// The part of a product of rows: `real` is false for rows past the last kept one.
+template <class T, class O, int FM, int FN, class Acc>
+__device__ __forceinline__ void store_rows(const RowsArgs &g, char *lds, const Tile &t,
+                                           const Acc (&acc)[FM][FN], bool real, uint32_t row,
+                                           uint32_t col, int high, int wide)
+{
+    O *out = (O *)(g.out + (int64_t)row * g.ldo) + col;
+    if constexpr (sizeof(T) == 1) {
+        const uint32_t lane = threadIdx.x % 64;
+        f32x4 sb[FN] = {};
+        float sa[FM] = {};
+        if (real) {
+            const float *from = g.sb + (uint64_t)t.group * g.cols + col;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int c = j * 16 + lane / 16 * 4 + q;
+                    sb[j][q] = c < wide ? from[c] : 0.f;
+                }
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int r = i * 16 + lane % 16;
+                sa[i] = r < high ? g.sa[source_row(g, row + r)] : 0.f;
+            }
+        }
+        store_part<O, FM, FN>(lds, out, g.ldo, high, wide, [&](int i, int j) {
+            f32x4 v;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = (float)acc[i][j][q] * sa[i] * sb[j][q];
+            return v;
+        });
+    } else {
+        store_part<O, FM, FN>(lds, out, g.ldo, high, wide, [&](int i, int j) { return acc[i][j]; });
+    }
+}
+
+// T: element of the operands; O: of the result; B: how the weights are staged.
+template <class T, class O, class B>
+__global__ void __launch_bounds__(kThreads) k_rows(RowsArgs g)
+{
+    typedef Along<T, kTile, kThreads> A;
+    typedef typename Mma<T>::Acc Acc;
+    __shared__ __align__(16) char lds[2][A::kBytes + B::kBytes];
+    const Tile t = find_tile(tile_of_block(blockIdx.x, g.span), g.offsets, g.experts, g.rows, 7,
+                             g.n_tiles);
+    if (t.group > g.experts) return;
+    const uint32_t m0 = t.begin + t.m * kTile, n0 = t.n * kTile;
+    const uint32_t high = t.end - m0 < kTile ? t.end - m0 : kTile;
+    const uint32_t wide = g.cols - n0 < kTile ? g.cols - n0 : kTile;
+    const uint32_t wave = threadIdx.x / 64;
+    const uint32_t wm = wave / 2 * kPart, wn = wave % 2 * kPart;
+    Acc acc[kFrags][kFrags] = {};
+
+    if (!g.offsets || t.group < g.experts) {
+        A a;
+        B b;
+        a.init([&](uint32_t r) {
+            return g.a + (int64_t)source_row(g, m0 + (r < high ? r : high - 1)) * g.lda;
+        });
+        const char *w = g.b + (int64_t)t.group * g.b_stride;
+        if constexpr (B::kAcross) b.init((int)wide);
+        else b.init([&](uint32_t r) { return w + (int64_t)(n0 + (r < wide ? r : wide - 1)) * g.ldb; });
+        const uint32_t steps = (g.bytes + kStepBytes - 1) / kStepBytes;
+        auto fetch = [&](uint32_t step) {
+            a.fetch(step, g.bytes);
+            if constexpr (B::kAcross)
+                b.fetch([&](uint32_t r) -> const char * {
+                    const uint32_t at = step * B::kRows + r;
+                    return at * 2 < g.bytes ? w + (int64_t)at * g.ldb + n0 * 2 : nullptr;
+                });
+            else b.fetch(step, g.bytes);
+        };
+        fetch(0);
+        for (uint32_t step = 0; step < steps; ++step) {
+            char *la = lds[step & 1], *lb = la + A::kBytes;
+            a.store(la);
+            b.store(lb);
+            __syncthreads();  // every wave is then past the other half's reads
+            if (step + 1 < steps) fetch(step + 1);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                typename Mma<T>::Frag fa[kFrags], fb[kFrags];
+#pragma unroll
+                for (int i = 0; i < kFrags; ++i) {
+                    fa[i] = A::frag(la, wm + i * 16, kk);
+                    fb[i] = B::frag(lb, wn + i * 16, kk);
+                }
+#pragma unroll
+                for (int i = 0; i < kFrags; ++i)
+#pragma unroll
+                    for (int j = 0; j < kFrags; ++j)
+                        acc[i][j] = Mma<T>::run(fb[j], fa[i], acc[i][j]);
+            }
+        }
+    }
+
+    __syncthreads();
+    store_rows<T, O>(g, lds[0] + wave * kPart * kPart * 2, t, acc,
+                     !g.offsets || t.group < g.experts, m0 + wm, n0 + wn, (int)high - (int)wm,
+                     (int)wide - (int)wn);
+}
+
+struct DwArgs {
+    char *out;
+    const char *dy;
+    const char *x;
+    int64_t lddy, ldx;  // bytes
+    const int32_t *offsets;
+    const int32_t *order;
+    uint32_t rows, x_rows, experts, n, k;
+    uint32_t n_tiles, k_tiles, span;
+    Divide divide;  // by top_k
+};
+
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_dw(DwArgs g)
+{
+    typedef Across<T, kTile, kThreads> A;
+    typedef typename Mma<T>::Acc Acc;
+    __shared__ __align__(16) char lds[2][2 * A::kBytes];
+    const uint32_t tile = tile_of_block(blockIdx.x, g.span);
+    const uint32_t each = g.n_tiles * g.k_tiles, e = tile / each;
+    if (e >= g.experts) return;
+    const uint32_t in = tile - e * each;
+    const uint32_t n0 = in % g.n_tiles * kTile, k0 = in / g.n_tiles * kTile;
+    const uint32_t high = g.n - n0 < kTile ? g.n - n0 : kTile;
+    const uint32_t wide = g.k - k0 < kTile ? g.k - k0 : kTile;
+    uint32_t end = __builtin_amdgcn_readfirstlane(g.offsets[e + 1]);
+    uint32_t begin = __builtin_amdgcn_readfirstlane(g.offsets[e]);
+    end = end > g.rows ? g.rows : end;
+    begin = begin > end ? end : begin;
+    const uint32_t wave = threadIdx.x / 64;
+    const uint32_t wm = wave / 2 * kPart, wn = wave % 2 * kPart;
+    Acc acc[kFrags][kFrags] = {};
+    A a, b;
+    a.init((int)high);
+    b.init((int)wide);
+    auto fetch = [&](uint32_t p0) {
+        a.fetch([&](uint32_t r) -> const char * {
+            const uint32_t p = p0 + r;
+            return p < end ? g.dy + (int64_t)p * g.lddy + n0 * 2 : nullptr;
+        });
+        b.fetch([&](uint32_t r) -> const char * {
+            const uint32_t p = p0 + r;
+            if (p >= end) return nullptr;
+            const uint32_t s = g.order ? g.divide((uint32_t)g.order[p]) : p;
+            return s < g.x_rows ? g.x + (int64_t)s * g.ldx + k0 * 2 : nullptr;
+        });
+    };
+    if (begin < end) fetch(begin);
+    uint32_t half = 0;
+    for (uint32_t p0 = begin; p0 < end; p0 += A::kRows, half ^= 1) {
+        char *la = lds[half], *lb = la + A::kBytes;
+        a.store(la);
+        b.store(lb);
+        __syncthreads();
+        if (p0 + A::kRows < end) fetch(p0 + A::kRows);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            typename Mma<T>::Frag fa[kFrags], fb[kFrags];
+#pragma unroll
+            for (int i = 0; i < kFrags; ++i) {
+                fa[i] = A::frag(la, wm + i * 16, kk);
+                fb[i] = A::frag(lb, wn + i * 16, kk);
+            }
+#pragma unroll
+            for (int i = 0; i < kFrags; ++i)
+#pragma unroll
+                for (int j = 0; j < kFrags; ++j)
+                    acc[i][j] = Mma<T>::run(fb[j], fa[i], acc[i][j]);
+        }
+    }
+    __syncthreads();
+    store_part<T, kFrags, kFrags>(lds[0] + wave * kPart * kPart * 2, (T *)g.out + ((int64_t)e * g.n + n0 + wm) * g.k + k0 + wn,
+                     (int64_t)g.k * 2, (int)high - (int)wm, (int)wide - (int)wn,
+                     [&](int i, int j) { return acc[i][j]; });
+}
+
+// ---------------------------------------------------------------------------
+// The pipelined products.
+
+// BM x BN results by WM x WN waves, PER_CU workgroups on a CU.
+template <int BM_, int BN_, int WM_, int WN_, int PER_CU_>
+struct Shape {
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+    static constexpr int THREADS = WM * WN * 64, PER_CU = PER_CU_;
+    static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // fragments of a wave
+    static constexpr int WAVES_PER_SIMD = THREADS / 256 * PER_CU;
+};
+
+extern __shared__ __align__(16) char pipe_lds[];
+
+// The loop over the steps. load(fast, step, lds, i) queues piece i of LOADS of a step
+// (fast: a whole one, of which there are `whole`), frag_a and frag_b read the fragments
+// of half a step, and ahead(step) may look up what the loads of that step need.
+//
+// A step is two halves. At its top the first half's fragments are in registers (or
+// on their way), and the next step's pieces are. While the first half is multiplied
+// the second half's fragments are read; then the stage is free, and while the second
+// half is multiplied the pieces of the step after the next go there, and the next step's
+// first fragments are read. So there is one barrier a step, loads have a step to
+// arrive, and all reads and loads are issued between products.
+template <class T, class S, int LOADS, uint32_t STAGE, class L, class FA, class FB, class H>
+__device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
+                                          typename Mma<T>::Acc (&acc)[S::FM][S::FN], L load,
+                                          FA frag_a, FB frag_b, H ahead)
+{
+    constexpr int FM = S::FM, FN = S::FN;
+    struct Frags {
+        typename Mma<T>::Frag a[FM], b[FN];
+    };
+    constexpr int kReads = FM + FN;
+    constexpr int kParts = FM * 3 / 4 > 0 ? FM * 3 / 4 : 1;
+    constexpr int kReadsEach = (kReads + kParts - 1) / kParts;
+    constexpr int kLoadsEach = (LOADS + FM - 1) / FM;
+    constexpr int kReadGap = FN / kReadsEach > 0 ? FN / kReadsEach : 1;
+    constexpr int kLoadGap = FN / kLoadsEach > 0 ? FN / kLoadsEach : 1;
+    static_assert(kReadsEach <= FN && kLoadsEach <= FN, "one of each after a product at most");
+    auto read = [&](const char *lds, Frags &f, int kk, int r) {
+        if (r < FN) f.b[r] = frag_b(lds, r, kk);
+        else f.a[r - FN] = frag_a(lds, r - FN, kk);
+    };
+    auto half = [&](auto with_loads, auto fast, const Frags &now, Frags &then, const char *lds,
+                    int kk, uint32_t step, uint32_t to) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                acc[i][j] = Mma<T>::run(now.b[j], now.a[i], acc[i][j]);
+                const int r = i * kReadsEach + j / kReadGap, p = i * kLoadsEach + j / kLoadGap;
+                if (j % kReadGap == 0 && j / kReadGap < kReadsEach && r < kReads)
+                    read(lds, then, kk, r);
+                if constexpr (decltype(with_loads)::value)
+                    if (j % kLoadGap == 0 && j / kLoadGap < kLoadsEach && p < LOADS)
+                        load(fast, step, to, p);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)pipe_lds;
+    Frags f[2];
+    auto step = [&](auto fast, auto stage, uint32_t k) {
+        constexpr uint32_t kHere = decltype(stage)::value * STAGE;
+        constexpr uint32_t kThere = STAGE - kHere;
+        ahead(k + 2);
+        half(std::false_type(), fast, f[0], f[1], pipe_lds + kHere, 1, 0, 0);
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave has left the stage
+        wait_loads<0>();
+        block_barrier();
+        half(std::true_type(), fast, f[1], f[0], pipe_lds + kThere, 0, k + 2, base + kHere);
+    };
+    typedef std::integral_constant<int, 0> Even;
+    typedef std::integral_constant<int, 1> Odd;
+    ahead(0);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) load(std::false_type(), 0, base, i);
+    ahead(1);
+    if (steps > 1) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load(std::false_type(), 1, base + STAGE, i);
+        wait_loads<LOADS>();
+    } else {
+        wait_loads<0>();
+    }
+    block_barrier();
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read(pipe_lds, f[0], 0, r);
+    uint32_t k = 0;
+    for (; k + 3 < whole; k += 2) {
+        step(std::true_type(), Even(), k);
+        step(std::true_type(), Odd(), k + 1);
+    }
+    for (; k < steps; k += 2) {
+        step(std::false_type(), Even(), k);
+        if (k + 1 < steps) step(std::false_type(), Odd(), k + 1);
+    }
+    block_barrier();
+}
+
+// The same where two sets of fragments do not fit beside the sums, as with two
+// operands across the reduction: a fragment of A takes the registers of the one that has just
+// been used up (those of B alternate), so the reads of the second half end with the first
+// half's products, and the barrier comes a few rows of products into the second.
+template <class T, class S, int LOADS, uint32_t STAGE, class L, class FA, class FB, class H>
+__device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole,
+                                          typename Mma<T>::Acc (&acc)[S::FM][S::FN], L load,
+                                          FA frag_a, FB frag_b, H ahead)
+{
+    constexpr int FM = S::FM, FN = S::FN;
+    constexpr int kWait = FM / 4;  // rows of the second half before the barrier
+    constexpr int kReads = (FM + FN + FM - kWait - 1) / (FM - kWait);
+    constexpr int kLoads = (LOADS + FM - kWait - 1) / (FM - kWait);
+    static_assert(kWait > 0 && FN <= FM, "rows to spread the reads over");
+    typename Mma<T>::Frag a[FM], b[2][FN];
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)pipe_lds;
+    auto products = [&](int i, const typename Mma<T>::Frag (&with)[FN]) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) Mma<T>::add(with[j], a[i], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto step = [&](auto fast, auto stage, uint32_t k) {
+        constexpr uint32_t kHere = decltype(stage)::value * STAGE;
+        constexpr uint32_t kThere = STAGE - kHere;
+        ahead(k + 2);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            products(i, b[0]);
+            if (i < FN) b[1][i] = frag_b(pipe_lds + kHere, i, 1);
+            a[i] = frag_a(pipe_lds + kHere, i, 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            products(i, b[1]);
+            if (i == kWait - 1) {
+                __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave has left the stage
+                wait_loads<0>();
+                block_barrier();
+            } else if (i >= kWait) {
+#pragma unroll
+                for (int r = (i - kWait) * kReads; r < (i - kWait + 1) * kReads; ++r) {
+                    if (r < FN) b[0][r] = frag_b(pipe_lds + kThere, r, 0);
+                    else if (r < FM + FN) a[r - FN] = frag_a(pipe_lds + kThere, r - FN, 0);
+                }
+#pragma unroll
+                for (int p = (i - kWait) * kLoads; p < (i - kWait + 1) * kLoads; ++p)
+                    if (p < LOADS) load(fast, k + 2, base + kHere, p);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    typedef std::integral_constant<int, 0> Even;
+    typedef std::integral_constant<int, 1> Odd;
+    ahead(0);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) load(std::false_type(), 0, base, i);
+    ahead(1);
+    if (steps > 1) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load(std::false_type(), 1, base + STAGE, i);
+        wait_loads<LOADS>();
+    } else {
+        wait_loads<0>();
+    }
+    block_barrier();
+#pragma unroll
+    for (int j = 0; j < FN; ++j) b[0][j] = frag_b(pipe_lds, j, 0);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) a[i] = frag_a(pipe_lds, i, 0);
+    uint32_t k = 0;
+    for (; k + 3 < whole; k += 2) {
+        step(std::true_type(), Even(), k);
+        step(std::true_type(), Odd(), k + 1);
+    }
+    for (; k < steps; k += 2) {
+        step(std::false_type(), Even(), k);
+        if (k + 1 < steps) step(std::false_type(), Odd(), k + 1);
+    }
+    sums_done(acc);
+    block_barrier();
+}
+
+// How the operands of a product of rows, and of the weights' gradient, are staged.
+template <class T, class S, bool ACROSS>
+struct RowsParts {
+    typedef PipeAlong<T, S::BM, S::THREADS> A;
+    typedef typename std::conditional<ACROSS, PipeAcross<T, S::BN, S::THREADS>,
+                                      PipeAlong<T, S::BN, S::THREADS>>::type B;
+    static constexpr uint32_t STAGE = A::kBytes + B::kBytes;
+};
+template <class T, class S>
+struct DwParts {
+    typedef PipeAcross<T, S::BM, S::THREADS> A;
+    typedef PipeAcross<T, S::BN, S::THREADS> B;
+    static constexpr uint32_t STAGE = A::kBytes + B::kBytes;
+};
+
+template <class T, class O, class S, bool ACROSS>
+__global__ void __launch_bounds__(S::THREADS)
+    __attribute__((amdgpu_waves_per_eu(S::WAVES_PER_SIMD, S::WAVES_PER_SIMD)))
+    k_rows_pipe(RowsArgs g)
+{
+    typedef RowsParts<T, S, ACROSS> P;
+    typedef typename P::A A;
+    typedef typename P::B B;
+    constexpr int kLog2 = __builtin_ctz(S::BM);
+    const Tile t = find_tile(tile_of_block(blockIdx.x, g.span), g.offsets, g.experts, g.rows, kLog2,
+                             g.n_tiles);
+    if (t.group > g.experts) return;
+    const uint32_t m0 = t.begin + t.m * S::BM, n0 = t.n * S::BN;
+    const uint32_t high = t.end - m0 < S::BM ? t.end - m0 : S::BM;
+    const uint32_t wide = g.cols - n0 < S::BN ? g.cols - n0 : S::BN;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const uint32_t wm = wave / S::WN * (S::BM / S::WM), wn = wave % S::WN * (S::BN / S::WN);
+    const bool real = !g.offsets || t.group < g.experts;
+    typename Mma<T>::Acc acc[S::FM][S::FN] = {};
+
+    if (real) {
+        A a;
+        const char *rows = g.order ? g.a : g.a + (int64_t)m0 * g.lda;
+        a.init([&](uint32_t r) {
+            r = r < high ? r : high - 1;
+            return (g.order ? source_row(g, m0 + r) : r) * (uint32_t)g.lda;
+        });
+        const char *w = g.b + (int64_t)t.group * g.b_stride;
+        const uint32_t steps = (g.bytes + kStepBytes - 1) / kStepBytes;
+        const uint32_t whole = g.bytes / kStepBytes, mine = wave * 1024;
+        auto fa = [&](const char *lds, int i, int kk) { return A::frag(lds, wm + i * 16, kk); };
+        auto fb = [&](const char *lds, int j, int kk) {
+            if constexpr (ACROSS) return B::frag(lds + A::kBytes, wn, j, kk);
+            else return B::frag(lds + A::kBytes, wn + j * 16, kk);
+        };
+        if constexpr (ACROSS) {
+            w += n0 * 2;
+            const uint32_t offset = B::row_of(0) * (uint32_t)g.ldb + B::byte_of(wide);
+            run_steps<T, S, A::kLoads + B::kLoads, P::STAGE>(
+                steps, whole, acc,
+                [&](auto fast, uint32_t step, uint32_t lds, int i) {
+                    if (!decltype(fast)::value && step >= steps) return;
+                    if (i < A::kLoads) {
+                        if constexpr (decltype(fast)::value) a.load(rows, step, lds + mine, i);
+                        else a.load_end(rows, step, g.bytes, lds + mine, i);
+                    } else {
+                        i -= A::kLoads;
+                        lds += A::kBytes + B::place_of(i, wave);
+                        const char *base =
+                            w + (int64_t)(step * B::kRows + i * B::kRowsEach) * g.ldb;
+                        if constexpr (decltype(fast)::value) load_to_lds(base, offset, lds);
+                        else
+                            load_to_lds((step * B::kRows + B::row_of(i)) * 2 < g.bytes
+                                            ? base + offset
+                                            : (const char *)&kZeros,
+                                        lds);
+                    }
+                },
+                fa, fb, [](uint32_t) {});
+        } else {
+            B b;
+            w += (int64_t)n0 * g.ldb;
+            b.init([&](uint32_t r) { return (r < wide ? r : wide - 1) * (uint32_t)g.ldb; });
+            run_steps<T, S, A::kLoads + B::kLoads, P::STAGE>(
+                steps, whole, acc,
+                [&](auto fast, uint32_t step, uint32_t lds, int i) {
+                    if (!decltype(fast)::value && step >= steps) return;
+                    lds += mine;
+                    if (i < A::kLoads) {
+                        if constexpr (decltype(fast)::value) a.load(rows, step, lds, i);
+                        else a.load_end(rows, step, g.bytes, lds, i);
+                    } else {
+                        i -= A::kLoads;
+                        lds += A::kBytes;
+                        if constexpr (decltype(fast)::value) b.load(w, step, lds, i);
+                        else b.load_end(w, step, g.bytes, lds, i);
+                    }
+                },
+                fa, fb, [](uint32_t) {});
+        }
+    }
+    store_rows<T, O>(g, pipe_lds + wave * (S::FM * S::FN * 512), t, acc, real, m0 + wm, n0 + wn,
+                     (int)high - (int)wm, (int)wide - (int)wn);
+}
+
+template <class T, class S>
+__global__ void __launch_bounds__(S::THREADS)
+    __attribute__((amdgpu_waves_per_eu(S::WAVES_PER_SIMD, S::WAVES_PER_SIMD)))
+    k_dw_pipe(DwArgs g)
+{
+    typedef DwParts<T, S> P;
+    typedef typename P::A A;
+    typedef typename P::B B;
+    const uint32_t tile = tile_of_block(blockIdx.x, g.span);
+    const uint32_t each = g.n_tiles * g.k_tiles, e = tile / each;
+    if (e >= g.experts) return;
+    const uint32_t in = tile - e * each;
+    const uint32_t n0 = in % g.n_tiles * S::BM, k0 = in / g.n_tiles * S::BN;
+    const uint32_t high = g.n - n0 < S::BM ? g.n - n0 : S::BM;
+    const uint32_t wide = g.k - k0 < S::BN ? g.k - k0 : S::BN;
+    uint32_t end = __builtin_amdgcn_readfirstlane(g.offsets[e + 1]);
+    uint32_t begin = __builtin_amdgcn_readfirstlane(g.offsets[e]);
+    end = end > g.rows ? g.rows : end;
+    begin = begin > end ? end : begin;
+    const uint32_t lane = threadIdx.x % 64;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const uint32_t wm = wave / S::WN * (S::BM / S::WM), wn = wave % S::WN * (S::BN / S::WN);
+    typename Mma<T>::Acc acc[S::FM][S::FN] = {};
+    if (begin < end) {
+        // order through the scalar cache: its loads then do not wait with the vector ones
+        typedef const __attribute__((address_space(4))) int32_t *Scalar;
+        const Scalar order = (Scalar)(uintptr_t)g.order;
+        const char *dy = g.dy + (int64_t)begin * g.lddy + n0 * 2;
+        const char *x = g.x + k0 * 2 + (g.order ? 0 : (int64_t)begin * g.ldx);
+        constexpr int kPerWave = 64 / B::kPieces;  // rows of x of one wave's load
+        uint32_t from[B::kLoads * kPerWave];       // their offsets, looked up half a step ahead
+        uint32_t of_row[kPerWave];                 // all ones in the lanes of each of these rows
+#pragma unroll
+        for (int q = 0; q < kPerWave; ++q)
+            of_row[q] = lane / B::kPieces == (uint32_t)q ? ~0u : 0u;
+        const uint32_t offset = A::row_of(0) * (uint32_t)g.lddy + A::byte_of(high);
+        const uint32_t byte = B::byte_of(wide);
+        const uint32_t count = end - begin, steps = (count + A::kRows - 1) / A::kRows;
+        run_steps_sharing<T, S, A::kLoads + B::kLoads, P::STAGE>(
+            steps, count / A::kRows, acc,
+            [&](auto fast, uint32_t step, uint32_t lds, int i) {
+                if (!decltype(fast)::value && step >= steps) return;
+                if (i < A::kLoads) {
+                    const char *base =
+                        dy + (int64_t)(step * A::kRows + i * A::kRowsEach) * g.lddy;
+                    lds += A::place_of(i, wave);
+                    if constexpr (decltype(fast)::value) load_to_lds(base, offset, lds);
+                    else
+                        load_to_lds(step * A::kRows + A::row_of(i) < count ? base + offset
+                                                                           : (const char *)&kZeros,
+                                    lds);
+                } else {
+                    i -= A::kLoads;
+                    lds += A::kBytes + B::place_of(i, wave);
+                    uint32_t at = 0;
+#pragma unroll
+                    for (int q = 0; q < kPerWave; ++q) at |= from[i * kPerWave + q] & of_row[q];
+                    at += byte;
+                    if constexpr (decltype(fast)::value) load_to_lds(x, at, lds);
+                    else
+                        load_to_lds(step * A::kRows + B::row_of(i) < count ? x + at
+                                                                           : (const char *)&kZeros,
+                                    lds);
+                }
+            },
+            [&](const char *lds, int i, int kk) { return A::frag(lds, wm, i, kk); },
+            [&](const char *lds, int j, int kk) { return B::frag(lds + A::kBytes, wn, j, kk); },
+            [&](uint32_t step) {
+#pragma unroll
+                for (int i = 0; i < B::kLoads; ++i)
+#pragma unroll
+                    for (int q = 0; q < kPerWave; ++q) {
+                        uint32_t s = step * A::kRows + i * B::kRowsEach + wave * kPerWave + q;
+                        s = s < count ? s : count - 1;
+                        if (g.order) {
+                            s = g.divide((uint32_t)order[begin + s]);
+                            s = s < g.x_rows ? s : g.x_rows - 1;
+                        }
+                        from[i * kPerWave + q] = s * (uint32_t)g.ldx;
+                    }
+            });
+    }
+    store_part<T, S::FM, S::FN>(pipe_lds + wave * (S::FM * S::FN * 512),
+                                (T *)g.out + ((int64_t)e * g.n + n0 + wm) * g.k + k0 + wn,
+                                (int64_t)g.k * 2, (int)high - (int)wm, (int)wide - (int)wn,
+                                [&](int i, int j) { return acc[i][j]; });
+}
+
+// Row tiles there can be: a group of c rows has ceil(c / tile), over the
+// experts and the rows past the last kept one.
+inline uint64_t most_row_tiles(uint64_t rows, uint64_t groups, uint32_t tile)
+{
+    const uint64_t m = (rows + groups * (tile - 1)) / tile;
+    return m < rows ? m : rows;
+}
+
+inline uint32_t span_of(uint64_t tiles)
+{
+    const uint64_t s = tiles / 8;
+    return s < 1 ? 1 : s > 32 ? 32 : (uint32_t)s;
+}
+
+// Blocks for `tiles` tiles, in runs of 8 * span, and the span.
+inline uint64_t blocks_for(uint64_t tiles, uint32_t *span)
+{
+    *span = span_of(tiles);
+    return (tiles + 8 * *span - 1) / (8 * *span) * (8 * *span);
+}
+
+template <class K>
+hist_status_t launch(K kernel, uint64_t blocks, uint32_t threads, uint32_t lds, hipStream_t stream,
+                     void *args)
+{
+    if (blocks > INT32_MAX) return HIST_ERR_UNSUPPORTED;
+    if (blocks == 0) return HIST_OK;
+    if (lds > 65536 && hipFuncSetAttribute((const void *)kernel,
+                                           hipFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)lds) != hipSuccess) {
+        (void)hipGetLastError();
+        return HIST_ERR_HIP;
+    }
+    const hipError_t err = hipLaunchKernel((const void *)kernel, dim3((uint32_t)blocks),
+                                           dim3(threads), &args, lds, stream);
+    (void)hipGetLastError();
+    return err == hipSuccess ? HIST_OK : HIST_ERR_HIP;
+}
+
+inline bool aligned16(const void *p, int64_t ld_bytes) { return !misaligned(p, 16) && ld_bytes % 16 == 0; }
+
+template <class T, class O, bool ACROSS, class S>
+hist_status_t launch_pipe(RowsArgs g, hipStream_t stream)
+{
+    g.n_tiles = (g.cols + S::BN - 1) / S::BN;
+    const uint64_t tiles =
+        most_row_tiles(g.rows, g.offsets ? g.experts + 1 : 1, S::BM) * g.n_tiles;
+    const uint64_t blocks = blocks_for(tiles, &g.span);
+    return launch(k_rows_pipe<T, O, S, ACROSS>, blocks, S::THREADS,
+                  2 * RowsParts<T, S, ACROSS>::STAGE, stream, &g);
+}
+
+// Whether `rows` rows from one base lie within 32-bit offsets.
+inline bool near(uint64_t rows, int64_t ld_bytes)
+{
+    return rows * (uint64_t)ld_bytes < ((uint64_t)1 << 32) - 256;
+}
+
+// 256 x 256 results a tile, or 128 x 128: the large tile does more for each byte it reads, the
+// small one wastes less where groups are short.
+inline bool wide_tiles(uint64_t rows, uint64_t groups, uint32_t cols)
+{
+    return rows >= 192 * groups && cols > 128;
+}
+
+template <class T, class O, bool ACROSS>
+hist_status_t launch_rows(RowsArgs g, hipStream_t stream)
+{
+    if (aligned16(g.a, g.lda) && aligned16(g.b, g.ldb) && g.b_stride % 16 == 0 &&
+        g.bytes % 16 == 0 && (!ACROSS || g.cols % 8 == 0) && near(g.order ? g.a_rows : 256, g.lda) &&
+        near(256, g.ldb)) {
+        const uint64_t groups = g.offsets ? g.experts : 1;
+        return wide_tiles(g.rows, groups, g.cols)
+                   ? launch_pipe<T, O, ACROSS, Shape<256, 256, 2, 4, 1>>(g, stream)
+                   : launch_pipe<T, O, ACROSS, Shape<128, 128, 2, 2, 2>>(g, stream);
+    }
+    typedef typename std::conditional<ACROSS, Across<T, kTile, kThreads>,
+                                      Along<T, kTile, kThreads>>::type B;
+    g.n_tiles = (g.cols + kTile - 1) / kTile;
+    const uint64_t tiles =
+        most_row_tiles(g.rows, g.offsets ? g.experts + 1 : 1, kTile) * g.n_tiles;
+    const uint64_t blocks = blocks_for(tiles, &g.span);
+    return launch(k_rows<T, O, B>, blocks, kThreads, 0, stream, &g);
+}
+
+template <class T, class S>
+hist_status_t launch_dw_pipe(DwArgs g, hipStream_t stream)
+{
+    g.n_tiles = (g.n + S::BM - 1) / S::BM;
+    g.k_tiles = (g.k + S::BN - 1) / S::BN;
+    const uint64_t blocks = blocks_for((uint64_t)g.n_tiles * g.k_tiles * g.experts, &g.span);
+    return launch(k_dw_pipe<T, S>, blocks, S::THREADS, 2 * DwParts<T, S>::STAGE, stream, &g);
+}
+
+template <class T>
+hist_status_t launch_dw(DwArgs g, hipStream_t stream)
+{
+    if (aligned16(g.dy, g.lddy) && aligned16(g.x, g.ldx) && g.n % 8 == 0 && g.k % 8 == 0 &&
+        near(64, g.lddy) && near(g.x_rows, g.ldx)) {
+        return launch_dw_pipe<T, Shape<256, 256, 2, 4, 1>>(g, stream);
+    }
+    g.n_tiles = (g.n + kTile - 1) / kTile;
+    g.k_tiles = (g.k + kTile - 1) / kTile;
+    const uint64_t blocks = blocks_for((uint64_t)g.n_tiles * g.k_tiles * g.experts, &g.span);
+    return launch(k_dw<T>, blocks, kThreads, 0, stream, &g);
+}
+
+// Checks that the products share. `unit`: bytes of an element of the result
+// of a leading dimension.
+inline bool bad_matrix(const void *p, int64_t ld, uint64_t width, bool used, uintptr_t align)
+{
+    return (used && !p) || ld < (int64_t)width || misaligned(p, align);
+}
+
+inline hist_status_t check_sizes(uint64_t rows, uint64_t x_rows, uint32_t top_k, uint32_t experts,
+                                 uint32_t n, uint32_t k)
+{
+    if (experts == 0 || n == 0 || k == 0 || top_k == 0) return HIST_ERR_INVALID_ARG;
+    if (experts > EXPERTS_MAX_EXPERTS || top_k > EXPERTS_MAX_TOP_K || n > EXPERTS_MAX_WIDTH || k > EXPERTS_MAX_WIDTH ||
+        rows > EXPERTS_MAX_ROWS || x_rows > EXPERTS_MAX_ROWS)
+        return HIST_ERR_UNSUPPORTED;
+    return HIST_OK;
+}
+
+}  // namespace pca_experts

@@ -21,7 +21,11 @@ namespace pca_experts {
 
 constexpr uint32_t kStepBytes = 128;
 
-// What one matrix instruction takes and gives, by element type.
+// What one matrix instruction takes and gives, by element type. add() keeps the sum
+// in its registers: the compiler's own form names other ones for the result, and in the
+// pipelined kernels, whose sums take half of all registers, it spilled. The compiler does not
+// see what such an instruction needs around it: s_nop 1 stands between it and a
+// move into its operands, and sums_done() must come before the sums are read.
 template <class T> struct Mma;
 template <> struct Mma<__bf16> {
     typedef bf16x8 Frag;
@@ -29,6 +33,10 @@ template <> struct Mma<__bf16> {
     static __device__ __forceinline__ Acc run(Frag a, Frag b, Acc c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ void add(Frag a, Frag b, Acc &c)
+    {
+        asm("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
     }
 };
 template <> struct Mma<_Float16> {
@@ -38,6 +46,10 @@ template <> struct Mma<_Float16> {
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
+    static __device__ __forceinline__ void add(Frag a, Frag b, Acc &c)
+    {
+        asm("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+    }
 };
 template <> struct Mma<int8_t> {
     typedef s32x4 Frag;
@@ -46,7 +58,27 @@ template <> struct Mma<int8_t> {
     {
         return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
     }
+    static __device__ __forceinline__ void add(Frag a, Frag b, Acc &c)
+    {
+        asm("s_nop 1\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+    }
 };
+
+template <class Acc, int FM, int FN>
+__device__ __forceinline__ void sums_done(Acc (&acc)[FM][FN])
+{
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
+    // the longest matrix instruction here is followed by 19 cycles in which its result
+    // must not be read
+    asm volatile("s_nop 15\n\ts_nop 15");
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
+}
 
 // 16 bytes at p, of which only the first `left` belong to the row; the others
 // read 0. Any alignment of T.
@@ -134,7 +166,6 @@ struct Across {
     static constexpr int kLoads = kRows * kPieces / THREADS;
     static constexpr int kRowsEach = THREADS / kPieces;  // rows between a thread's pieces
     static constexpr uint32_t kBytes = kRows * COLS * 2;
-    static_assert(kRowsEach % 16 == 0 && COLS % 128 == 0, "pieces of one permutation");
     int left;      // bytes of the row from this thread's column on
     uint32_t col;  // byte offset of this thread's column
     u32x4 v[kLoads];
@@ -148,6 +179,7 @@ struct Across {
         return i * kRowsEach + threadIdx.x / kPieces;
     }
     // cols: columns of the operand that are left from the tile's first one.
+    // (a thread's rows are 16 apart: one permutation)
     __device__ __forceinline__ void init(int cols)
     {
         const uint32_t r = threadIdx.x / kPieces;
@@ -183,6 +215,155 @@ struct Across {
         } f;
         f.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
         f.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * COLS * 2));
+        return f.whole;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Staging without registers, for rows at 16-byte multiples: each lane's piece goes
+// from memory straight to LDS. The layouts in LDS are those of Along and Across.
+
+// What a piece outside the operand reads.
+static __device__ const u32x4 kZeros = {0, 0, 0, 0};
+
+// 16 bytes from each lane's address to LDS at lds + 16 * lane (lds: byte offset, the
+// same for the wave; m0 carries it, which no other instruction here uses). The
+// instruction has no result register, so nothing that the compiler allocates can
+// be overwritten while it is in flight; wait_loads orders it before the reads.
+__device__ __forceinline__ void load_to_lds(const char *p, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "s"(lds), "v"(p));
+}
+
+// The same from base + each lane's offset; base is the wave's.
+__device__ __forceinline__ void load_to_lds(const char *base, uint32_t offset, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(offset), "s"(base));
+}
+
+// Until at most N of the wave's loads are in flight.
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+__device__ __forceinline__ void block_barrier()
+{
+    asm volatile("" : : : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" : : : "memory");
+}
+
+// n / d for n < 2^30 and 1 <= d <= 64: mul = ceil(2^(31 + s) / d) with s =
+// floor(log2 d) exceeds the real quotient by less than 1, which moves n * mul by
+// less than 2^30 < 2^(31 + s) / d, so the floor is exact.
+struct Divide {
+    uint32_t mul, shift;
+    static Divide by(uint32_t d)
+    {
+        uint32_t s = 0;
+        while (d >> (s + 1)) ++s;
+        return {(uint32_t)(((1ull << (31 + s)) + d - 1) / d), s};
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const
+    {
+        return __umulhi(2 * n, mul) >> shift;
+    }
+};
+
+// Along the reduction. offset[i]: this thread's piece i from the operand's base, in the
+// first step; a step is 128 bytes further.
+template <class T, int ROWS, int THREADS>
+struct PipeAlong : Along<T, ROWS, THREADS> {
+    typedef Along<T, ROWS, THREADS> Layout;
+    uint32_t offset[Layout::kLoads];
+    uint32_t at;
+
+    // offset_of(r): the bytes from the base to row r.
+    template <class F>
+    __device__ __forceinline__ void init(F offset_of)
+    {
+        const uint32_t r = threadIdx.x / 8;
+        at = ((threadIdx.x % 8) ^ ((r >> 1) & 7)) * 16;
+#pragma unroll
+        for (int i = 0; i < Layout::kLoads; ++i) offset[i] = offset_of(i * (THREADS / 8) + r) + at;
+    }
+    // A whole step; and one that the reduction may end in, which reads 0 from there on.
+    __device__ __forceinline__ void load(const char *base, uint32_t step, uint32_t lds, int i) const
+    {
+        load_to_lds(base + (uint64_t)step * kStepBytes, offset[i], lds + i * THREADS * 16);
+    }
+    __device__ __forceinline__ void load_end(const char *base, uint32_t step, uint32_t bytes,
+                                             uint32_t lds, int i) const
+    {
+        const uint32_t from = step * kStepBytes;
+        load_to_lds(from + at < bytes ? base + from + offset[i] : (const char *)&kZeros,
+                    lds + i * THREADS * 16);
+    }
+};
+
+// Across the reduction. One load of a wave holds kTogether whole rows (1024 bytes), so
+// they lie together in LDS; 64 bytes follow them, and 128 more follow each four loads
+// of two rows. Within a row the 32-byte parts are permuted by part ^ r % kTogether.
+// The eight rows that half a wave takes 32 bytes of in one transposing read, r0 to r0 + 3 and r0 + 8
+// to r0 + 11, then meet all 64 banks once, and the fragments of one operand need
+// only kTogether addresses in registers (with a permutation of all of a row's parts by
+// the row, as in Across, each fragment needed its own, and they did not fit).
+template <class T, int COLS, int THREADS>
+struct PipeAcross {
+    static constexpr bool kAcross = true;
+    static constexpr int kRows = kStepBytes / 2;
+    static constexpr int kPieces = COLS / 8;
+    static constexpr int kLoads = kRows * kPieces / THREADS;
+    static constexpr int kRowsEach = THREADS / kPieces;
+    static constexpr int kTogether = 64 / kPieces;
+    static_assert(kRows * kPieces % THREADS == 0 && (kTogether == 2 || kTogether == 4),
+                  "rows of 128 or 256 columns");
+
+    // Where load number l of a step (a wave's) lies.
+    static constexpr __device__ uint32_t place(uint32_t l)
+    {
+        return l * 1088 + (kTogether == 2 ? l / 4 * 128 : 0);
+    }
+    static constexpr uint32_t kBytes = kRows / kTogether * 1088 +
+                                       (kTogether == 2 ? kRows / kTogether / 4 * 128 : 0);
+    // The place of this wave's load i.
+    static __device__ __forceinline__ uint32_t place_of(int i, uint32_t wave)
+    {
+        return place(i * (THREADS / 64) + wave);
+    }
+    static __device__ __forceinline__ uint32_t row_of(int i)
+    {
+        return i * kRowsEach + threadIdx.x / kPieces;
+    }
+    // The byte in a row of this thread's pieces; past the operand's last column the first
+    // one is read (its results are not stored).
+    static __device__ __forceinline__ uint32_t byte_of(uint32_t wide)
+    {
+        const uint32_t mix = threadIdx.x / kPieces % kTogether;
+        const uint32_t byte = ((threadIdx.x % kPieces) ^ (mix << 1)) * 16;
+        return byte < wide * 2 ? byte : 0;
+    }
+    // Fragment i of the part that starts at column first (a multiple of 64), half kk.
+    static __device__ __forceinline__ typename Mma<T>::Frag frag(const char *lds, uint32_t first,
+                                                                 int i, int kk)
+    {
+        const uint32_t lane = threadIdx.x % 64, q = lane % 16, r = lane / 16 * 8 + q / 4;
+        const uint32_t part = (i % kTogether) ^ (r % kTogether);
+        const char *p = lds + place(r / kTogether) + r % kTogether * (COLS * 2) + first * 2 +
+                        part * 32 + q % 4 * 8;
+        p += place(kk * 32 / kTogether) + i / kTogether * kTogether * 32;
+        union {
+            s16x4 half[2];
+            typename Mma<T>::Frag whole;
+        } f;
+        f.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+        f.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + place(4 / kTogether)));
         return f.whole;
     }
 };
