@@ -61,7 +61,7 @@ hist_status_t experts_group_workspace_size(uint64_t tokens, uint32_t top_k, uint
 
 /* ids: int32 (id_bits 32) or int64 (id_bits 64) [tokens][top_k].
  * counts[experts], offsets[experts + 1], order[tokens * top_k],
- * place[tokens * top_k]. workspace: 4-byte aligned. */
+ * place[tokens * top_k]. workspace: 16-byte aligned. */
 hist_status_t experts_group(const void *ids, int32_t id_bits, uint64_t tokens, uint32_t top_k,
                             uint32_t experts, int32_t *counts, int32_t *offsets, int32_t *order,
                             int32_t *place, void *workspace, uint64_t workspace_bytes,

@@ -18,6 +18,7 @@ namespace pca_experts {
 constexpr uint32_t kThreads = 1024;
 constexpr uint32_t kWaves = kThreads / 64;
 constexpr uint32_t kOneChunk = 8 * kThreads;  // up to here one workgroup does it all
+constexpr uint32_t kGroups = 16;              // of lanes, that read the chunks' rows
 constexpr uint32_t kMostChunks = 512;         // each workgroup reads every chunk's row
 
 // Pairs of one workgroup.
@@ -28,6 +29,9 @@ inline uint32_t chunk_size(uint32_t pairs)
     const uint32_t least = (rounds + kMostChunks - 1) / kMostChunks;
     return kThreads * (least > 2 ? least : 2);
 }
+
+// Words of a chunk's row: a multiple of 16 bytes (what lies past the last expert is never used).
+__host__ __device__ inline uint32_t row_words(uint32_t experts) { return (experts + 3) / 4 * 4; }
 
 // The id of pair i, `experts` for one outside the range.
 template <class I>
@@ -55,11 +59,11 @@ __global__ void __launch_bounds__(kThreads) k_group_count(const I *__restrict__ 
     }
     __syncthreads();
     for (uint32_t e = threadIdx.x; e < experts; e += kThreads)
-        rows[blockIdx.x * experts + e] = hist[e];
+        rows[blockIdx.x * row_words(experts) + e] = hist[e];
 }
 
 // rows == nullptr: the grid is one workgroup, which takes all pairs.
-// Dynamic LDS: kWaves rows of `experts` counters.
+// Dynamic LDS: kWaves rows of `experts` counters, then (with rows) 2 * kGroups rows of partial sums.
 template <class I>
 __global__ void __launch_bounds__(kThreads)
     k_group_place(const I *__restrict__ ids, uint32_t pairs, uint32_t experts, uint32_t id_bits,
@@ -67,7 +71,7 @@ __global__ void __launch_bounds__(kThreads)
                   int32_t *__restrict__ counts, int32_t *__restrict__ offsets,
                   int32_t *__restrict__ order, int32_t *__restrict__ place)
 {
-    extern __shared__ uint32_t wave_at[];
+    extern __shared__ __align__(16) uint32_t wave_at[];
     __shared__ uint32_t wave_total[kWaves];
     const uint32_t wave = threadIdx.x / 64, lane = threadIdx.x % 64;
     const uint32_t own = chunk / kWaves;  // pairs of one wave
@@ -85,18 +89,36 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncthreads();
 
-    // One thread an expert (experts <= kThreads): its pairs in earlier chunks and in all.
+    // The experts' pairs in earlier chunks and in all. The rows are read four experts a
+    // lane, by as many groups of lanes as there are (at most kGroups), all loads of a lane in flight.
     const uint32_t e = threadIdx.x;
     uint32_t before = 0, total = 0;
-    if (e < experts) {
-        if (rows) {
-            uint32_t after = 0;
-            for (uint32_t c = 0; c < blockIdx.x; ++c) before += rows[c * experts + e];
-            for (uint32_t c = blockIdx.x; c < chunks; ++c) after += rows[c * experts + e];
-            total = before + after;
-        } else {
-            for (uint32_t w = 0; w < kWaves; ++w) total += wave_at[w * experts + e];
+    if (rows) {
+        uint32_t *part = wave_at + kWaves * experts;
+        const uint32_t quads = row_words(experts) / 4;
+        const uint32_t most = kThreads / quads, groups = most < kGroups ? most : kGroups;
+        const uint32_t quad = threadIdx.x % quads, group = threadIdx.x / quads;
+        if (group < groups) {
+            u32x4 early = {0, 0, 0, 0}, late = {0, 0, 0, 0};
+#pragma unroll 8
+            for (uint32_t c = group; c < chunks; c += groups) {
+                const u32x4 v = ((const u32x4 *)rows)[c * quads + quad];
+                if (c < blockIdx.x) early += v;
+                else late += v;
+            }
+            ((u32x4 *)part)[group * quads + quad] = early;
+            ((u32x4 *)part)[(groups + group) * quads + quad] = late;
         }
+        __syncthreads();
+        if (e < experts) {
+            for (uint32_t c = 0; c < groups; ++c) {
+                before += part[c * quads * 4 + e];
+                total += part[(groups + c) * quads * 4 + e];
+            }
+            total += before;
+        }
+    } else if (e < experts) {
+        for (uint32_t w = 0; w < kWaves; ++w) total += wave_at[w * experts + e];
     }
     const uint32_t inclusive = wave_inclusive_scan(total);
     if (lane == 63) wave_total[wave] = inclusive;
@@ -157,10 +179,14 @@ void launch_group(const void *ids, uint32_t pairs, uint32_t experts, int32_t *co
     const bool one = pairs <= kOneChunk;
     const uint32_t chunk = chunk_size(pairs);
     const uint32_t chunks = one ? 1 : (pairs + chunk - 1) / chunk;
+    // the partial sums start at a multiple of 16 bytes: kWaves rows do
+    const uint32_t quads = row_words(experts) / 4;
+    const uint32_t groups = kThreads / quads < kGroups ? kThreads / quads : kGroups;
+    const uint32_t lds = kWaves * experts * 4 + (one ? 0 : 2 * groups * quads * 16);
     if (!one)
         k_group_count<I><<<chunks, kThreads, 0, stream>>>((const I *)ids, pairs, experts, chunk,
                                                        rows);
-    k_group_place<I><<<chunks, kThreads, kWaves * experts * 4, stream>>>(
+    k_group_place<I><<<chunks, kThreads, lds, stream>>>(
         (const I *)ids, pairs, experts, bits, chunk, chunks, one ? nullptr : rows, counts, offsets,
         order, place);
 }
@@ -177,7 +203,7 @@ extern "C" hist_status_t experts_group_workspace_size(uint64_t tokens, uint32_t 
         tokens > EXPERTS_MAX_ROWS / top_k)
         return HIST_ERR_UNSUPPORTED;
     const uint32_t pairs = (uint32_t)(tokens * top_k), chunk = chunk_size(pairs);
-    *bytes = pairs <= kOneChunk ? 0 : (uint64_t)((pairs + chunk - 1) / chunk) * experts * 4;
+    *bytes = pairs <= kOneChunk ? 0 : (uint64_t)((pairs + chunk - 1) / chunk) * row_words(experts) * 4;
     return HIST_OK;
 }
 
@@ -195,7 +221,7 @@ extern "C" hist_status_t experts_group(const void *ids, int32_t id_bits, uint64_
     if (misaligned(ids, id_bits / 8) || misaligned(counts, 4) || misaligned(offsets, 4) ||
         misaligned(order, 4) || misaligned(place, 4))
         return HIST_ERR_INVALID_ARG;
-    if (need && (!workspace || misaligned(workspace, 4) || workspace_bytes < need))
+    if (need && (!workspace || misaligned(workspace, 16) || workspace_bytes < need))
         return HIST_ERR_WORKSPACE;
     st = device_status();
     if (st != HIST_OK) return st;

@@ -5,47 +5,69 @@
 namespace pca_experts {
 
 // ---------------------------------------------------------------------------
-// One wave a row of x; its pieces stay in registers between the maximum and the
-// rounding where the row is short enough, and come from the cache otherwise.
-template <class T>
+// THREADS lanes a row of x. What of it a lane holds in registers (KEPT pieces of 16 bytes)
+// is read once; the rest of a longer row is read again, from the cache.
+template <class T, int THREADS, int KEPT>
 __global__ void __launch_bounds__(256)
     k_quantize(int8_t *__restrict__ xq, int64_t ldq, float *__restrict__ sx,
                const T *__restrict__ x, int64_t ldx, uint32_t rows, uint32_t k)
 {
     typedef typename Vec8<T>::type V;
-    const uint32_t r = blockIdx.x * 4 + threadIdx.x / 64, lane = threadIdx.x % 64;
-    if (r >= rows) return;
+    typedef int8_t i8x8 __attribute__((ext_vector_type(8)));
+    __shared__ uint32_t tops[4];
+    const uint32_t r = blockIdx.x * (256 / THREADS) + threadIdx.x / THREADS;
+    const uint32_t lane = threadIdx.x % THREADS;
+    if (r >= rows) return;  // a row is a wave's or the workgroup's
     const T *from = x + (int64_t)r * ldx;
     int8_t *to = xq + (int64_t)r * ldq;
+    V kept[KEPT];
     // As whole numbers, magnitudes order like floats, infinity and then NaN above all.
     uint32_t top = 0;
-    for (uint32_t c = lane * 8; c < k; c += 512) {
-        const V v = load8(from + c, (int)(k - c));
+    auto widen = [&](const V &v) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t m = __float_as_uint((float)v[i]) & 0x7fffffffu;
             top = top > m ? top : m;
         }
+    };
+#pragma unroll
+    for (int s = 0; s < KEPT; ++s) {
+        const uint32_t c = (s * THREADS + lane) * 8;
+        kept[s] = c < k ? load8(from + c, (int)(k - c)) : V{};
     }
+#pragma unroll
+    for (int s = 0; s < KEPT; ++s) widen(kept[s]);
+    for (uint32_t c = (KEPT * THREADS + lane) * 8; c < k; c += THREADS * 8)
+        widen(load8(from + c, (int)(k - c)));
 #pragma unroll
     for (int m = 32; m; m >>= 1) {
         const uint32_t o = __shfl_xor(top, m, 64);
         top = top > o ? top : o;
     }
+    if constexpr (THREADS > 64) {
+        if (lane % 64 == 0) tops[threadIdx.x / 64] = top;
+        __syncthreads();
+        top = tops[0];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) top = top > tops[w] ? top : tops[w];
+    }
     const float scale = __uint_as_float(top) / 127.0f;
     const bool finite = top < 0x7f800000u && scale > 0.f;
     if (lane == 0) sx[r] = scale;
-    for (uint32_t c = lane * 8; c < k; c += 512) {
+    // A quotient by the reciprocal is within two steps of 2^-23 of it, so it rounds to the
+    // right whole number or, next to a half, to the one beside it; the same for a
+    // scale whose reciprocal is not a normal number with the division itself.
+    const bool normal = scale > 1e-37f && scale < 1e37f;
+    const float inverse = normal ? 1.0f / scale : 0.f;
+    auto quantize = [&](const V &v, uint32_t c) {
         const int left = (int)(k - c);
-        const V v = load8(from + c, left);
-        typedef int8_t i8x8 __attribute__((ext_vector_type(8)));
         i8x8 q;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float f = (float)v[i];
-            float n = finite ? rintf(f / scale) : 0.f;
-            // The rounded quotient can fall on the wrong side of a half. What n leaves
-            // of f is exact in 32 bits, so comparing it with half the scale decides.
+            float n = finite ? rintf(normal ? f * inverse : f / scale) : 0.f;
+            // What n leaves of f is exact in 32 bits, so comparing it with half the scale
+            // decides.
             const float rest = __builtin_fmaf(-n, scale, f);
             const float twice = 2.f * fabsf(rest);
             const bool odd = ((int)n & 1) != 0;
@@ -61,7 +83,27 @@ __global__ void __launch_bounds__(256)
             for (int i = 0; i < 8; ++i)
                 if (i < left) to[c + i] = q[i];
         }
+    };
+#pragma unroll
+    for (int s = 0; s < KEPT; ++s) {
+        const uint32_t c = (s * THREADS + lane) * 8;
+        if (c < k) quantize(kept[s], c);
     }
+    for (uint32_t c = (KEPT * THREADS + lane) * 8; c < k; c += THREADS * 8)
+        quantize(load8(from + c, (int)(k - c)), c);
+}
+
+// A wave a row up to 1024 columns (two pieces a lane); the workgroup otherwise.
+template <class T>
+void launch_quantize(int8_t *xq, int64_t ldq, float *sx, const void *x, int64_t ldx, uint32_t rows,
+                     uint32_t k, hipStream_t stream)
+{
+    if (k <= 1024)
+        k_quantize<T, 64, 2>
+            <<<(rows + 3) / 4, 256, 0, stream>>>(xq, ldq, sx, (const T *)x, ldx, rows, k);
+    else
+        k_quantize<T, 256, 4>
+            <<<rows, 256, 0, stream>>>(xq, ldq, sx, (const T *)x, ldx, rows, k);
 }
 
 }  // namespace pca_experts
@@ -79,13 +121,8 @@ extern "C" hist_status_t experts_quantize_rows(int8_t *xq, int64_t ldq, float *s
         return HIST_ERR_INVALID_ARG;
     st = device_status();
     if (st != HIST_OK || rows == 0) return st;
-    const uint32_t blocks = (uint32_t)((rows + 3) / 4);
-    if (dtype == EXPERTS_BF16)
-        k_quantize<__bf16><<<blocks, 256, 0, stream>>>(xq, ldq, sx, (const __bf16 *)x, ldx,
-                                                       (uint32_t)rows, k);
-    else
-        k_quantize<_Float16><<<blocks, 256, 0, stream>>>(xq, ldq, sx, (const _Float16 *)x, ldx,
-                                                         (uint32_t)rows, k);
+    (dtype == EXPERTS_BF16 ? launch_quantize<__bf16> : launch_quantize<_Float16>)(
+        xq, ldq, sx, x, ldx, (uint32_t)rows, k, stream);
     return launch_status();
 }
 

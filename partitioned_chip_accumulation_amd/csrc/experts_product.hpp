@@ -287,11 +287,11 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
     };
     constexpr int kReads = FM + FN;
     constexpr int kParts = FM * 3 / 4 > 0 ? FM * 3 / 4 : 1;
-    constexpr int kReadsEach = (kReads + kParts - 1) / kParts;
-    constexpr int kLoadsEach = (LOADS + FM - 1) / FM;
-    constexpr int kReadGap = FN / kReadsEach > 0 ? FN / kReadsEach : 1;
-    constexpr int kLoadGap = FN / kLoadsEach > 0 ? FN / kLoadsEach : 1;
-    static_assert(kReadsEach <= FN && kLoadsEach <= FN, "one of each after a product at most");
+    // reads after a product, over the first three quarters of the rows; loads over all of them
+    constexpr int kSlots = kParts * FN, kReadsEach = (kReads + kSlots - 1) / kSlots;
+    constexpr int kReadGap = kSlots / kReads > 0 ? kSlots / kReads : 1;
+    constexpr int kLoadsEach = (LOADS + FM * FN - 1) / (FM * FN);
+    constexpr int kLoadGap = FM * FN / LOADS > 0 ? FM * FN / LOADS : 1;
     auto read = [&](const char *lds, Frags &f, int kk, int r) {
         if (r < FN) f.b[r] = frag_b(lds, r, kk);
         else f.a[r - FN] = frag_a(lds, r - FN, kk);
@@ -303,12 +303,18 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 acc[i][j] = Mma<T>::run(now.b[j], now.a[i], acc[i][j]);
-                const int r = i * kReadsEach + j / kReadGap, p = i * kLoadsEach + j / kLoadGap;
-                if (j % kReadGap == 0 && j / kReadGap < kReadsEach && r < kReads)
-                    read(lds, then, kk, r);
+                const int slot = i * FN + j;
+                if (slot % kReadGap == 0)
+#pragma unroll
+                    for (int q = 0; q < kReadsEach; ++q)
+                        if (slot / kReadGap * kReadsEach + q < kReads)
+                            read(lds, then, kk, slot / kReadGap * kReadsEach + q);
                 if constexpr (decltype(with_loads)::value)
-                    if (j % kLoadGap == 0 && j / kLoadGap < kLoadsEach && p < LOADS)
-                        load(fast, step, to, p);
+                    if (slot % kLoadGap == 0)
+#pragma unroll
+                        for (int q = 0; q < kLoadsEach; ++q)
+                            if (slot / kLoadGap * kLoadsEach + q < LOADS)
+                                load(fast, step, to, slot / kLoadGap * kLoadsEach + q);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -624,6 +630,130 @@ __global__ void __launch_bounds__(S::THREADS)
                                 [&](int i, int j) { return acc[i][j]; });
 }
 
+// ---------------------------------------------------------------------------
+// Few rows: the time goes into reading the weights once, so what counts is how many bytes are
+// in flight. A workgroup takes 16 * FN columns and 16 * RM rows; its four waves
+// divide the reduction, 128 bytes of it in turn, and add their sums through LDS at the
+// end, in the order of the waves. The fragments come from memory to registers as the
+// matrix instruction wants them (a lane's 16 bytes are consecutive in a row), with no LDS
+// between, `DEEP` pieces of 128 bytes ahead. Any alignment.
+template <class T, class O, int RM, int FN, int DEEP>
+__global__ void __launch_bounds__(256) k_rows_thin(RowsArgs g)
+{
+    typedef typename Mma<T>::Acc Acc;
+    typedef typename Mma<T>::Frag Frag;
+    __shared__ __align__(16) Acc sums[4][RM * FN][64];
+    const Tile t = find_tile(tile_of_block(blockIdx.x, g.span), g.offsets, g.experts, g.rows,
+                             4 + __builtin_ctz(RM), g.n_tiles);
+    if (t.group > g.experts) return;
+    const uint32_t m0 = t.begin + t.m * 16 * RM, n0 = t.n * 16 * FN;
+    const uint32_t high = t.end - m0 < 16 * RM ? t.end - m0 : 16 * RM;
+    const uint32_t wide = g.cols - n0 < 16 * FN ? g.cols - n0 : 16 * FN;
+    const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const bool real = !g.offsets || t.group < g.experts;
+    Acc acc[RM][FN] = {};
+    if (real) {
+        const char *a[RM], *b[FN];
+        const uint32_t at = lane / 16 * 16;
+#pragma unroll
+        for (int i = 0; i < RM; ++i) {
+            const uint32_t r = i * 16 + lane % 16;
+            a[i] = g.a + (int64_t)source_row(g, m0 + (r < high ? r : high - 1)) * g.lda + at;
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const uint32_t c = j * 16 + lane % 16;
+            b[j] = g.b + (int64_t)t.group * g.b_stride +
+                   (int64_t)(n0 + (c < wide ? c : wide - 1)) * g.ldb + at;
+        }
+        struct Piece {
+            u32x4 a[RM][2], b[FN][2];
+        };
+        // whole: the piece's 128 bytes lie in the rows
+        auto fetch = [&](Piece &p, uint32_t from, auto whole) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t f = from + h * 64;
+                const int left = decltype(whole)::value ? 16 : (int)g.bytes - (int)(f + at);
+#pragma unroll
+                for (int j = 0; j < FN; ++j) p.b[j][h] = load16<T>(b[j] + f, left);
+#pragma unroll
+                for (int i = 0; i < RM; ++i) p.a[i][h] = load16<T>(a[i] + f, left);
+            }
+        };
+        auto multiply = [&](const Piece &p) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < RM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        acc[i][j] = Mma<T>::run(__builtin_bit_cast(Frag, p.b[j][h]),
+                                                __builtin_bit_cast(Frag, p.a[i][h]), acc[i][j]);
+        };
+        constexpr uint32_t kTurn = 4 * kStepBytes;
+        uint32_t from = wave * kStepBytes;
+        // DEEP pieces in flight while the DEEP before them are multiplied
+        const uint32_t mine = g.bytes > from ? (g.bytes - from + kTurn - kStepBytes) / kTurn : 0;
+        uint32_t left = mine / DEEP * DEEP;  // whole pieces of this wave, in groups
+        Piece p[DEEP];
+        if (left) {
+#pragma unroll
+            for (int d = 0; d < DEEP; ++d) fetch(p[d], from + d * kTurn, std::true_type());
+            from += DEEP * kTurn;
+            for (left -= DEEP; left; left -= DEEP) {
+#pragma unroll
+                for (int d = 0; d < DEEP; ++d) {
+                    multiply(p[d]);
+                    fetch(p[d], from + d * kTurn, std::true_type());
+                }
+                from += DEEP * kTurn;
+            }
+#pragma unroll
+            for (int d = 0; d < DEEP; ++d) multiply(p[d]);
+        }
+        for (; from < g.bytes; from += kTurn) {
+            fetch(p[0], from, std::false_type());
+            multiply(p[0]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) sums[wave][i * FN + j][lane] = acc[i][j];
+    __syncthreads();
+    for (uint32_t f = wave; f < RM * FN; f += 4) {
+        Acc s = sums[0][f][lane];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) s += sums[w][f][lane];
+        const uint32_t r = f / FN * 16 + lane % 16, c = f % FN * 16 + lane / 16 * 4;
+        if (r >= high || c >= wide) continue;
+        const int left = (int)(wide - c);
+        typedef O O4 __attribute__((ext_vector_type(4)));
+        float v[4];
+        if constexpr (sizeof(T) == 1) {
+            const float sa = real ? g.sa[source_row(g, m0 + r)] : 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[q] = real && q < left
+                           ? (float)s[q] * sa * g.sb[(uint64_t)t.group * g.cols + n0 + c + q]
+                           : 0.f;
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = s[q];
+        }
+        O *out = (O *)(g.out + (int64_t)(m0 + r) * g.ldo) + n0 + c;
+        const O4 o = {(O)v[0], (O)v[1], (O)v[2], (O)v[3]};
+        if (left >= 4) {
+            store_any(out, o);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+                if (q < left) out[q] = o[q];
+        }
+    }
+}
+
 // Row tiles there can be: a group of c rows has ceil(c / tile), over the
 // experts and the rows past the last kept one.
 inline uint64_t most_row_tiles(uint64_t rows, uint64_t groups, uint32_t tile)
@@ -682,30 +812,65 @@ inline bool near(uint64_t rows, int64_t ld_bytes)
     return rows * (uint64_t)ld_bytes < ((uint64_t)1 << 32) - 256;
 }
 
-// 256 x 256 results a tile, or 128 x 128: the large tile does more for each byte it reads, the
-// small one wastes less where groups are short.
-inline bool wide_tiles(uint64_t rows, uint64_t groups, uint32_t cols)
+template <class T, class O, int RM, int FN, int DEEP>
+hist_status_t launch_thin(RowsArgs g, hipStream_t stream)
 {
-    return rows >= 192 * groups && cols > 128;
+    g.n_tiles = (g.cols + 16 * FN - 1) / (16 * FN);
+    const uint64_t tiles =
+        most_row_tiles(g.rows, g.offsets ? g.experts + 1 : 1, 16 * RM) * g.n_tiles;
+    const uint64_t blocks = blocks_for(tiles, &g.span);
+    return launch(k_rows_thin<T, O, RM, FN, DEEP>, blocks, 256, 0, stream, &g);
 }
 
+// The kernel for a product of rows. What decides is the rows of an expert on average (the
+// host knows no more) and whether the tiles are enough for 256 CUs. Measured with 32 experts of
+// 2560 x 2048 (bf16, us; thin 16 x 16, 32 x 128, 64 x 128, 128 x 128, 256 x 256):
+//   rows    2:  47.8   62.7   63.5   76.6   91.9      rows   64:  313   93.7   92.9   98.7    118
+//   rows    8:  72.3   73.0   73.4   93.0    112      rows  128:  593    125    111    100    121
+//   rows   16:   107   73.7   74.6   93.4    113      rows  256: 1145    199    154    145    128
+//   rows   32:   179   81.6   77.1   95.1    115      rows  512: 2262    348    258    221    218
+// and with a dense weight of 8192 x 4096 in 8 bits (thin 32 x 64, 64 x 64, 64 x 128, 128 x 128,
+// 256 x 256): rows 32: 18.6, 20.5, 23.5, 25.3, 41.5; rows 256: 52.0, 22.4, 25.0, 27.6, 44.3;
+// rows 1024: 186, 56.4, 53.8, 39.8, 48.7.
 template <class T, class O, bool ACROSS>
 hist_status_t launch_rows(RowsArgs g, hipStream_t stream)
 {
+    const uint64_t groups = g.offsets ? g.experts : 1, each = g.rows / groups;
+    // about so many: half a tile of each group is empty
+    auto tiles = [&](uint32_t bm, uint32_t bn) {
+        const uint64_t m = groups == 1 ? (each + bm - 1) / bm : g.rows / bm + (groups + 1) / 2;
+        return (m < g.rows ? m : g.rows) * ((g.cols + bn - 1) / bn);
+    };
+    // The thin kernels divide the reduction among waves, the others do not, so the choice between
+    // them does not depend on alignment: a product's bits are the same at every address.
+    if constexpr (!ACROSS) {
+        if (each <= 6) return launch_thin<T, O, 1, 1, 4>(g, stream);
+        if (each <= 64 && tiles(64, 64) < 256) return launch_thin<T, O, 2, 4, 2>(g, stream);
+    }
     if (aligned16(g.a, g.lda) && aligned16(g.b, g.ldb) && g.b_stride % 16 == 0 &&
-        g.bytes % 16 == 0 && (!ACROSS || g.cols % 8 == 0) && near(g.order ? g.a_rows : 256, g.lda) &&
-        near(256, g.ldb)) {
-        const uint64_t groups = g.offsets ? g.experts : 1;
-        return wide_tiles(g.rows, groups, g.cols)
-                   ? launch_pipe<T, O, ACROSS, Shape<256, 256, 2, 4, 1>>(g, stream)
-                   : launch_pipe<T, O, ACROSS, Shape<128, 128, 2, 2, 2>>(g, stream);
+        g.bytes % 16 == 0 && (!ACROSS || g.cols % 8 == 0) &&
+        near(g.order ? g.a_rows : 256, g.lda) && near(256, g.ldb)) {
+        if (each >= 192 && g.cols > 128 && tiles(256, 256) >= 256)
+            return launch_pipe<T, O, ACROSS, Shape<256, 256, 2, 4, 1>>(g, stream);
+        if (each >= 80 && tiles(128, 128) >= 256)
+            return launch_pipe<T, O, ACROSS, Shape<128, 128, 2, 2, 2>>(g, stream);
+        if (each > 24 && tiles(64, 128) >= 512)
+            return launch_pipe<T, O, ACROSS, Shape<64, 128, 2, 2, 3>>(g, stream);
+        if constexpr (ACROSS) {
+            return each > 24 ? launch_pipe<T, O, ACROSS, Shape<64, 128, 2, 2, 3>>(g, stream)
+                             : launch_pipe<T, O, ACROSS, Shape<32, 128, 2, 2, 4>>(g, stream);
+        } else {
+            if (each <= 24 && tiles(32, 128) >= 256)
+                return launch_pipe<T, O, ACROSS, Shape<32, 128, 1, 4, 4>>(g, stream);
+            return launch_pipe<T, O, ACROSS, Shape<64, 64, 2, 2, 4>>(g, stream);
+        }
     }
     typedef typename std::conditional<ACROSS, Across<T, kTile, kThreads>,
                                       Along<T, kTile, kThreads>>::type B;
     g.n_tiles = (g.cols + kTile - 1) / kTile;
-    const uint64_t tiles =
+    const uint64_t all =
         most_row_tiles(g.rows, g.offsets ? g.experts + 1 : 1, kTile) * g.n_tiles;
-    const uint64_t blocks = blocks_for(tiles, &g.span);
+    const uint64_t blocks = blocks_for(all, &g.span);
     return launch(k_rows<T, O, B>, blocks, kThreads, 0, stream, &g);
 }
 
@@ -723,7 +888,10 @@ hist_status_t launch_dw(DwArgs g, hipStream_t stream)
 {
     if (aligned16(g.dy, g.lddy) && aligned16(g.x, g.ldx) && g.n % 8 == 0 && g.k % 8 == 0 &&
         near(64, g.lddy) && near(g.x_rows, g.ldx)) {
-        return launch_dw_pipe<T, Shape<256, 256, 2, 4, 1>>(g, stream);
+        // enough large tiles for 256 CUs, or small ones
+        return (uint64_t)g.experts * ((g.n + 255) / 256) * ((g.k + 255) / 256) >= 256
+                   ? launch_dw_pipe<T, Shape<256, 256, 2, 4, 1>>(g, stream)
+                   : launch_dw_pipe<T, Shape<128, 128, 2, 2, 2>>(g, stream);
     }
     g.n_tiles = (g.n + kTile - 1) / kTile;
     g.k_tiles = (g.k + kTile - 1) / kTile;

@@ -34,6 +34,7 @@ from . import hist
 
 MAX_EXPERTS = 1024
 MAX_TOP_K = 64
+_ONE_WORKGROUP = 8192  # pairs that experts_group sorts without a workspace
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 _vp, _u32, _u64, _i32, _i64 = (ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int32,
@@ -54,28 +55,30 @@ _SIGNATURES = {
     "experts_int8_matmul": [_vp, _i64, _vp, _i64, _u64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _u64,
                             _u32, _u32, _u32, _u32, _i32, _vp],
 }
-_bound = None
+_functions: dict = {}
+_raw_stream = torch._C._cuda_getCurrentRawStream  # 0.1 us; current_stream().cuda_stream takes 2.8
 
 
 def _library():
-    global _bound
-    if _bound is None:
-        lib = hist.library()
+    lib = hist.library()
+    if not _functions:
         for name, args in _SIGNATURES.items():
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = _i32, args
-        _bound = lib
-    return _bound
+            _functions[name] = fn
+    return lib
 
 
 def _call(name: str, device: torch.device, *args):
     """The call on the current stream of the device."""
-    fn = getattr(_library(), name)
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if not _functions:
+        _library()
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = _functions[name](*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(index):
+            status = _functions[name](*args, _raw_stream(index))
     if status:
         raise hist.HistError(status, name)
 
@@ -88,76 +91,92 @@ class Groups(NamedTuple):
     place: torch.Tensor    # [tokens, top_k] pair -> sorted place, -1 where dropped
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
-
+# The checks run on every call, so what they say is only put together when one fails.
 
 def _matrix(t: torch.Tensor, name: str, dtypes=_DTYPES, dim: int = 2) -> int:
     """Checks a matrix (or a stack of them) and returns its leading dimension."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda, f"{name} must be a CUDA tensor")
-    _need(t.dtype in dtypes, f"{name} must be of type {' or '.join(map(str, dtypes))}")
-    _need(t.dim() == dim, f"{name} must have {dim} dimensions")
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == dim):
+        raise ValueError(f"{name} must be a CUDA tensor of {dim} dimensions and of type "
+                         f"{' or '.join(map(str, dtypes))}")
     rows, width = t.shape[-2:]
-    _need(width > 0, f"{name} must have columns")
-    _need(width == 1 or t.stride(-1) == 1, f"{name}'s rows must have unit stride")
-    ld = t.stride(-2) if rows > 1 else width
-    _need(ld >= width, f"{name}'s rows must not overlap")
+    stride = t.stride()
+    ld = stride[-2] if rows > 1 else width
+    if width == 0 or (width > 1 and stride[-1] != 1) or ld < width:
+        raise ValueError(f"{name} must have columns, and rows of unit stride that do not overlap")
     return ld
 
 
 def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: torch.device):
-    _need(isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and
-          tuple(t.shape) == shape and t.is_contiguous(),
-          f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device and
+            t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
 
 
 def _groups(g: Groups, device: torch.device) -> tuple[int, int, int]:
     """Checks the groups and returns (experts, pairs, top_k)."""
-    experts, (tokens, top_k) = g.counts.shape[0], g.place.shape
-    _vector(g.offsets, "offsets", torch.int32, (experts + 1,), device)
-    _vector(g.order, "order", torch.int32, (tokens * top_k,), device)
-    _vector(g.place, "place", torch.int32, (tokens, top_k), device)
-    return experts, tokens * top_k, top_k
+    _, offsets, order, place = g
+    if place.dim() != 2:
+        raise ValueError("place must have the shape [tokens, top_k]")
+    tokens, top_k = place.shape
+    experts, pairs = offsets.numel() - 1, tokens * top_k
+    _vector(offsets, "offsets", torch.int32, (g.counts.numel() + 1,), device)
+    _vector(order, "order", torch.int32, (pairs,), device)
+    _vector(place, "place", torch.int32, (tokens, top_k), device)
+    return experts, pairs, top_k
 
 
 def _rows(x: torch.Tensor, g: Groups, pairs: int, gather: bool, name: str):
-    tokens = g.place.shape[0]
-    want = tokens if gather else pairs
-    _need(x.shape[0] == want,
-          f"{name} must have {want} rows, one for each {'token' if gather else 'pair'}")
+    want = g.place.shape[0] if gather else pairs
+    if x.shape[0] != want:
+        raise ValueError(
+            f"{name} must have {want} rows, one for each {'token' if gather else 'pair'}")
 
 
 def _weights(w: torch.Tensor, experts: int, device: torch.device, dtype: torch.dtype):
     """Leading dimension and stride of the experts' weights [experts, n, k]."""
     ld = _matrix(w, "w", (dtype,), 3)
-    _need(w.device == device and w.shape[0] == experts,
-          f"w must hold {experts} experts' weights on {device}")
-    _need(w.shape[1] > 0, "w must have rows")
-    _need(experts == 1 or w.stride(0) >= 0, "w's experts must have a stride")
+    if w.device != device or w.shape[0] != experts or w.shape[1] == 0:
+        raise ValueError(f"w must hold {experts} experts' weights, with rows, on {device}")
     return ld, w.stride(0) if experts > 1 else 0
+
+
+def _same(a: int, b: int, what: str):
+    if a != b:
+        raise ValueError(f"{what} must agree, not be {a} and {b}")
+
+
+def _device(a: torch.Tensor, b: torch.Tensor, what: str):
+    if a.device != b.device:
+        raise ValueError(f"{what} must be on one device")
 
 
 def group_rows(ids: torch.Tensor, experts: int) -> Groups:
     """Count and sort the pairs of ``ids`` (int32 or int64, [tokens, top_k],
     contiguous) by expert; pairs of one expert keep their order."""
-    _need(isinstance(ids, torch.Tensor) and ids.is_cuda and ids.dim() == 2 and
-          ids.dtype in (torch.int32, torch.int64) and ids.is_contiguous(),
-          "ids must be a contiguous int32 or int64 CUDA tensor of shape [tokens, top_k]")
+    if not (isinstance(ids, torch.Tensor) and ids.is_cuda and ids.dim() == 2 and
+            ids.dtype in (torch.int32, torch.int64) and ids.is_contiguous()):
+        raise ValueError("ids must be a contiguous int32 or int64 CUDA tensor of shape "
+                         "[tokens, top_k]")
     tokens, top_k = ids.shape
-    _need(top_k > 0 and experts > 0, "top_k and experts must be positive")
-    need = _u64()
-    status = _library().experts_group_workspace_size(tokens, top_k, experts, ctypes.byref(need))
-    if status:
-        raise hist.HistError(status, "experts_group_workspace_size")
-    pairs, words = tokens * top_k, need.value // 4
-    # one allocation for the results and the workspace
-    buf = torch.empty(2 * experts + 1 + 2 * pairs + words, dtype=torch.int32, device=ids.device)
-    counts, offsets, order, place, work = buf.split([experts, experts + 1, pairs, pairs, words])
+    if top_k <= 0 or experts <= 0:
+        raise ValueError("top_k and experts must be positive")
+    pairs, work = tokens * top_k, 0
+    if pairs > _ONE_WORKGROUP:
+        need = _u64()
+        status = _library().experts_group_workspace_size(tokens, top_k, experts,
+                                                         ctypes.byref(need))
+        if status:
+            raise hist.HistError(status, "experts_group_workspace_size")
+        work = need.value // 4
+    # one allocation, the workspace first (its start is aligned)
+    buf = torch.empty(work + 2 * experts + 1 + 2 * pairs, dtype=torch.int32, device=ids.device)
+    counts, offsets, order, place = buf[work:].split((experts, experts + 1, pairs, pairs)) \
+        if work else buf.split((experts, experts + 1, pairs, pairs))
     at = buf.data_ptr()
+    c = at + 4 * work
     _call("experts_group", ids.device, ids.data_ptr(), ids.element_size() * 8, tokens, top_k,
-          experts, at, at + 4 * experts, at + 4 * (2 * experts + 1),
-          at + 4 * (2 * experts + 1 + pairs), at + 4 * (2 * experts + 1 + 2 * pairs), 4 * words)
+          experts, c, c + 4 * experts, c + 4 * (2 * experts + 1),
+          c + 4 * (2 * experts + 1 + pairs), at, 4 * work)
     return Groups(counts, offsets, order, place.view(tokens, top_k))
 
 
@@ -168,7 +187,7 @@ def matmul(x: torch.Tensor, w: torch.Tensor, g: Groups, gather: bool = False) ->
     experts, pairs, top_k = _groups(g, x.device)
     ldw, stride = _weights(w, experts, x.device, x.dtype)
     n, k = w.shape[1:]
-    _need(x.shape[1] == k, f"x and w must have the same last dimension, not {x.shape[1]} and {k}")
+    _same(x.shape[1], k, "the last dimensions of x and w")
     _rows(x, g, pairs, gather, "x")
     y = torch.empty(pairs, n, dtype=x.dtype, device=x.device)
     _call("experts_matmul", x.device, y.data_ptr(), n, x.data_ptr(), ldx, x.shape[0], w.data_ptr(),
@@ -184,7 +203,7 @@ def matmul_dx(dy: torch.Tensor, w: torch.Tensor, g: Groups) -> torch.Tensor:
     experts, pairs, _ = _groups(g, dy.device)
     ldw, stride = _weights(w, experts, dy.device, dy.dtype)
     n, k = w.shape[1:]
-    _need(dy.shape[1] == n, f"dy must have w's {n} rows as columns, not {dy.shape[1]}")
+    _same(dy.shape[1], n, "the columns of dy and the rows of w")
     _rows(dy, g, pairs, False, "dy")
     dx = torch.empty(pairs, k, dtype=dy.dtype, device=dy.device)
     _call("experts_matmul_dx", dy.device, dx.data_ptr(), k, dy.data_ptr(), lddy, w.data_ptr(), ldw,
@@ -196,7 +215,7 @@ def matmul_dw(dy: torch.Tensor, x: torch.Tensor, g: Groups, gather: bool = False
     """dw[e] = sum over e's sorted pairs p of dy[p]^T x[p]; x as in ``matmul``."""
     lddy, ldx = _matrix(dy, "dy"), _matrix(x, "x", (dy.dtype,))
     experts, pairs, top_k = _groups(g, dy.device)
-    _need(x.device == dy.device, "dy and x must be on one device")
+    _device(x, dy, "dy and x")
     _rows(dy, g, pairs, False, "dy")
     _rows(x, g, pairs, gather, "x")
     n, k = dy.shape[1], x.shape[1]
@@ -228,10 +247,11 @@ def combine_backward(dout: torch.Tensor, y: torch.Tensor, g: Groups,
     """``combine``'s gradients: (dy [pairs, n], dweights float32 [tokens, top_k])."""
     lddout, ldy = _matrix(dout, "dout"), _matrix(y, "y", (dout.dtype,))
     _, pairs, top_k = _groups(g, y.device)
-    _need(dout.device == y.device, "dout and y must be on one device")
+    _device(dout, y, "dout and y")
     _rows(y, g, pairs, False, "y")
     tokens, n = g.place.shape[0], y.shape[1]
-    _need(tuple(dout.shape) == (tokens, n), f"dout must have the shape {(tokens, n)}")
+    if dout.shape != (tokens, n):
+        raise ValueError(f"dout must have the shape {(tokens, n)}")
     _vector(weights, "weights", torch.float32, (tokens, top_k), y.device)
     dy = torch.empty(pairs, n, dtype=y.dtype, device=y.device)
     dweights = torch.empty(tokens, top_k, dtype=torch.float32, device=y.device)
@@ -261,14 +281,17 @@ def int8_matmul(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: torch.
     """(xq wq^T) scaled by sx for rows and sw for columns. Dense without ``g``:
     wq is [n, k], sw [n]. By expert with it: wq is [experts, n, k], sw
     [experts, n], and xq and sx are per token with ``gather``, else per pair."""
-    _need(out_dtype in _DTYPES, "out_dtype must be torch.bfloat16 or torch.float16")
+    if out_dtype not in _DTYPES:
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float16")
     ldq = _matrix(xq, "xq", (torch.int8,))
     device, x_rows = xq.device, xq.shape[0]
     _vector(sx, "sx", torch.float32, (x_rows,), device)
     if g is None:
-        _need(not gather, "gather needs the groups")
+        if gather:
+            raise ValueError("gather needs the groups")
         ldw, stride = _matrix(wq, "wq", (torch.int8,)), 0
-        _need(wq.device == device and wq.shape[0] > 0, f"wq must have rows and be on {device}")
+        if wq.device != device or wq.shape[0] == 0:
+            raise ValueError(f"wq must have rows and be on {device}")
         experts, pairs, top_k, offsets, order = 1, x_rows, 1, None, None
     else:
         experts, pairs, top_k = _groups(g, device)
@@ -276,9 +299,8 @@ def int8_matmul(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: torch.
         _rows(xq, g, pairs, gather, "xq")
         offsets, order = g.offsets.data_ptr(), g.order.data_ptr() if gather else None
     n, k = wq.shape[-2:]
-    _need(xq.shape[1] == k,
-          f"xq and wq must have the same last dimension, not {xq.shape[1]} and {k}")
-    _vector(sw, "sw", torch.float32, tuple(wq.shape[:-1]), device)
+    _same(xq.shape[1], k, "the last dimensions of xq and wq")
+    _vector(sw, "sw", torch.float32, wq.shape[:-1], device)
     y = torch.empty(pairs, n, dtype=out_dtype, device=device)
     _call("experts_int8_matmul", device, y.data_ptr(), n, xq.data_ptr(), ldq, x_rows,
           sx.data_ptr(), wq.data_ptr(), ldw, stride, sw.data_ptr(), offsets, order, pairs, top_k,
