@@ -8,12 +8,6 @@
 
 namespace pca_experts {
 
-// The tile: 128 x 128 results by four waves of 64 x 64 each.
-constexpr int kTile = 128;
-constexpr int kThreads = 256;
-constexpr int kPart = 64;         // rows and columns of one wave
-constexpr int kFrags = kPart / 16;
-
 struct RowsArgs {
     char *out;
     const char *a;
@@ -110,72 +104,6 @@ __device__ __forceinline__ void store_rows(const RowsArgs &g, char *lds, const T
     }
 }
 
-// T: element of the operands; O: of the result; B: how the weights are staged.
-template <class T, class O, class B>
-__global__ void __launch_bounds__(kThreads) k_rows(RowsArgs g)
-{
-    typedef Along<T, kTile, kThreads> A;
-    typedef typename Mma<T>::Acc Acc;
-    __shared__ __align__(16) char lds[2][A::kBytes + B::kBytes];
-    const Tile t = find_tile(tile_of_block(blockIdx.x, g.span), g.offsets, g.experts, g.rows, 7,
-                             g.n_tiles);
-    if (t.group > g.experts) return;
-    const uint32_t m0 = t.begin + t.m * kTile, n0 = t.n * kTile;
-    const uint32_t high = t.end - m0 < kTile ? t.end - m0 : kTile;
-    const uint32_t wide = g.cols - n0 < kTile ? g.cols - n0 : kTile;
-    const uint32_t wave = threadIdx.x / 64;
-    const uint32_t wm = wave / 2 * kPart, wn = wave % 2 * kPart;
-    Acc acc[kFrags][kFrags] = {};
-
-    if (!g.offsets || t.group < g.experts) {
-        A a;
-        B b;
-        a.init([&](uint32_t r) {
-            return g.a + (int64_t)source_row(g, m0 + (r < high ? r : high - 1)) * g.lda;
-        });
-        const char *w = g.b + (int64_t)t.group * g.b_stride;
-        if constexpr (B::kAcross) b.init((int)wide);
-        else b.init([&](uint32_t r) { return w + (int64_t)(n0 + (r < wide ? r : wide - 1)) * g.ldb; });
-        const uint32_t steps = (g.bytes + kStepBytes - 1) / kStepBytes;
-        auto fetch = [&](uint32_t step) {
-            a.fetch(step, g.bytes);
-            if constexpr (B::kAcross)
-                b.fetch([&](uint32_t r) -> const char * {
-                    const uint32_t at = step * B::kRows + r;
-                    return at * 2 < g.bytes ? w + (int64_t)at * g.ldb + n0 * 2 : nullptr;
-                });
-            else b.fetch(step, g.bytes);
-        };
-        fetch(0);
-        for (uint32_t step = 0; step < steps; ++step) {
-            char *la = lds[step & 1], *lb = la + A::kBytes;
-            a.store(la);
-            b.store(lb);
-            __syncthreads();  // every wave is then past the other half's reads
-            if (step + 1 < steps) fetch(step + 1);
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                typename Mma<T>::Frag fa[kFrags], fb[kFrags];
-#pragma unroll
-                for (int i = 0; i < kFrags; ++i) {
-                    fa[i] = A::frag(la, wm + i * 16, kk);
-                    fb[i] = B::frag(lb, wn + i * 16, kk);
-                }
-#pragma unroll
-                for (int i = 0; i < kFrags; ++i)
-#pragma unroll
-                    for (int j = 0; j < kFrags; ++j)
-                        acc[i][j] = Mma<T>::run(fb[j], fa[i], acc[i][j]);
-            }
-        }
-    }
-
-    __syncthreads();
-    store_rows<T, O>(g, lds[0] + wave * kPart * kPart * 2, t, acc,
-                     !g.offsets || t.group < g.experts, m0 + wm, n0 + wn, (int)high - (int)wm,
-                     (int)wide - (int)wn);
-}
-
 struct DwArgs {
     char *out;
     const char *dy;
@@ -187,70 +115,6 @@ struct DwArgs {
     uint32_t n_tiles, k_tiles, span;
     Divide divide;  // by top_k
 };
-
-template <class T>
-__global__ void __launch_bounds__(kThreads) k_dw(DwArgs g)
-{
-    typedef Across<T, kTile, kThreads> A;
-    typedef typename Mma<T>::Acc Acc;
-    __shared__ __align__(16) char lds[2][2 * A::kBytes];
-    const uint32_t tile = tile_of_block(blockIdx.x, g.span);
-    const uint32_t each = g.n_tiles * g.k_tiles, e = tile / each;
-    if (e >= g.experts) return;
-    const uint32_t in = tile - e * each;
-    const uint32_t n0 = in % g.n_tiles * kTile, k0 = in / g.n_tiles * kTile;
-    const uint32_t high = g.n - n0 < kTile ? g.n - n0 : kTile;
-    const uint32_t wide = g.k - k0 < kTile ? g.k - k0 : kTile;
-    uint32_t end = __builtin_amdgcn_readfirstlane(g.offsets[e + 1]);
-    uint32_t begin = __builtin_amdgcn_readfirstlane(g.offsets[e]);
-    end = end > g.rows ? g.rows : end;
-    begin = begin > end ? end : begin;
-    const uint32_t wave = threadIdx.x / 64;
-    const uint32_t wm = wave / 2 * kPart, wn = wave % 2 * kPart;
-    Acc acc[kFrags][kFrags] = {};
-    A a, b;
-    a.init((int)high);
-    b.init((int)wide);
-    auto fetch = [&](uint32_t p0) {
-        a.fetch([&](uint32_t r) -> const char * {
-            const uint32_t p = p0 + r;
-            return p < end ? g.dy + (int64_t)p * g.lddy + n0 * 2 : nullptr;
-        });
-        b.fetch([&](uint32_t r) -> const char * {
-            const uint32_t p = p0 + r;
-            if (p >= end) return nullptr;
-            const uint32_t s = g.order ? g.divide((uint32_t)g.order[p]) : p;
-            return s < g.x_rows ? g.x + (int64_t)s * g.ldx + k0 * 2 : nullptr;
-        });
-    };
-    if (begin < end) fetch(begin);
-    uint32_t half = 0;
-    for (uint32_t p0 = begin; p0 < end; p0 += A::kRows, half ^= 1) {
-        char *la = lds[half], *lb = la + A::kBytes;
-        a.store(la);
-        b.store(lb);
-        __syncthreads();
-        if (p0 + A::kRows < end) fetch(p0 + A::kRows);
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            typename Mma<T>::Frag fa[kFrags], fb[kFrags];
-#pragma unroll
-            for (int i = 0; i < kFrags; ++i) {
-                fa[i] = A::frag(la, wm + i * 16, kk);
-                fb[i] = A::frag(lb, wn + i * 16, kk);
-            }
-#pragma unroll
-            for (int i = 0; i < kFrags; ++i)
-#pragma unroll
-                for (int j = 0; j < kFrags; ++j)
-                    acc[i][j] = Mma<T>::run(fb[j], fa[i], acc[i][j]);
-        }
-    }
-    __syncthreads();
-    store_part<T, kFrags, kFrags>(lds[0] + wave * kPart * kPart * 2, (T *)g.out + ((int64_t)e * g.n + n0 + wm) * g.k + k0 + wn,
-                     (int64_t)g.k * 2, (int)high - (int)wm, (int)wide - (int)wn,
-                     [&](int i, int j) { return acc[i][j]; });
-}
 
 // ---------------------------------------------------------------------------
 // The pipelined products.
@@ -266,9 +130,12 @@ struct Shape {
 
 extern __shared__ __align__(16) char pipe_lds[];
 
-// The loop over the steps. load(fast, step, lds, i) queues piece i of LOADS of a step
-// (fast: a whole one, of which there are `whole`), frag_a and frag_b read the fragments
-// of half a step, and ahead(step) may look up what the loads of that step need.
+// The loop over the steps. load(fast, parity, step, lds, i) queues piece i of LOADS of a step
+// (fast: a whole one, of which there are `whole`; parity: the step's). Where it is not
+// DIRECT, it puts the piece, which is in registers by then, and fetches that of two steps later,
+// and first(parity, i) fetches those of steps 0 and 1.
+// frag_a and frag_b read the fragments of half a step, and ahead(step) may look up what
+// the loads of that step need.
 //
 // A step is two halves. At its top the first half's fragments are in registers (or
 // on their way), and the next step's pieces are. While the first half is multiplied
@@ -276,12 +143,14 @@ extern __shared__ __align__(16) char pipe_lds[];
 // half is multiplied the pieces of the step after the next go there, and the next step's
 // first fragments are read. So there is one barrier a step, loads have a step to
 // arrive, and all reads and loads are issued between products.
-template <class T, class S, int LOADS, uint32_t STAGE, class L, class FA, class FB, class H>
+template <class T, class S, bool DIRECT, int LOADS, uint32_t STAGE, class F, class L, class FA,
+          class FB, class H>
 __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
-                                          typename Mma<T>::Acc (&acc)[S::FM][S::FN], L load,
+                                          typename Mma<T>::Acc (&acc)[S::FM][S::FN], F first, L load,
                                           FA frag_a, FB frag_b, H ahead)
 {
     constexpr int FM = S::FM, FN = S::FN;
+    constexpr uint32_t kAhead = DIRECT ? 2 : 4;  // steps from a step to what it fetches
     struct Frags {
         typename Mma<T>::Frag a[FM], b[FN];
     };
@@ -296,7 +165,7 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
         if (r < FN) f.b[r] = frag_b(lds, r, kk);
         else f.a[r - FN] = frag_a(lds, r - FN, kk);
     };
-    auto half = [&](auto with_loads, auto fast, const Frags &now, Frags &then, const char *lds,
+    auto half = [&](auto with_loads, auto fast, auto stage, const Frags &now, Frags &then, const char *lds,
                     int kk, uint32_t step, uint32_t to) {
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
@@ -314,7 +183,7 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
 #pragma unroll
                         for (int q = 0; q < kLoadsEach; ++q)
                             if (slot / kLoadGap * kLoadsEach + q < LOADS)
-                                load(fast, step, to, slot / kLoadGap * kLoadsEach + q);
+                                load(fast, stage, step, to, slot / kLoadGap * kLoadsEach + q);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -324,31 +193,41 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
     auto step = [&](auto fast, auto stage, uint32_t k) {
         constexpr uint32_t kHere = decltype(stage)::value * STAGE;
         constexpr uint32_t kThere = STAGE - kHere;
-        ahead(k + 2);
-        half(std::false_type(), fast, f[0], f[1], pipe_lds + kHere, 1, 0, 0);
+        ahead(k + kAhead);
+        half(std::false_type(), fast, stage, f[0], f[1], pipe_lds + kHere, 1, 0, 0);
         __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave has left the stage
-        wait_loads<0>();
+        if constexpr (DIRECT) wait_loads<0>();
         block_barrier();
-        half(std::true_type(), fast, f[1], f[0], pipe_lds + kThere, 0, k + 2, base + kHere);
+        half(std::true_type(), fast, stage, f[1], f[0], pipe_lds + kThere, 0, k + 2, base + kHere);
     };
     typedef std::integral_constant<int, 0> Even;
     typedef std::integral_constant<int, 1> Odd;
     ahead(0);
+    if constexpr (!DIRECT) {
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) load(std::false_type(), 0, base, i);
-    ahead(1);
-    if (steps > 1) {
+        for (int i = 0; i < LOADS; ++i) first(Even(), i);
+        ahead(1);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load(std::false_type(), 1, base + STAGE, i);
-        wait_loads<LOADS>();
+        for (int i = 0; i < LOADS; ++i) first(Odd(), i);
+        ahead(2);
+    }
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) load(std::false_type(), Even(), 0, base, i);
+    ahead(kAhead - 1);
+    if (steps > 1)
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load(std::false_type(), Odd(), 1, base + STAGE, i);
+    if constexpr (DIRECT) {
+        if (steps > 1) wait_loads<LOADS>();
+        else wait_loads<0>();
     } else {
-        wait_loads<0>();
+        __builtin_amdgcn_s_waitcnt(0xc07f);
     }
     block_barrier();
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(pipe_lds, f[0], 0, r);
     uint32_t k = 0;
-    for (; k + 3 < whole; k += 2) {
+    for (; k + kAhead + 1 < whole; k += 2) {
         step(std::true_type(), Even(), k);
         step(std::true_type(), Odd(), k + 1);
     }
@@ -363,12 +242,14 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
 // operands across the reduction: a fragment of A takes the registers of the one that has just
 // been used up (those of B alternate), so the reads of the second half end with the first
 // half's products, and the barrier comes a few rows of products into the second.
-template <class T, class S, int LOADS, uint32_t STAGE, class L, class FA, class FB, class H>
+template <class T, class S, bool DIRECT, int LOADS, uint32_t STAGE, class F, class L, class FA,
+          class FB, class H>
 __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole,
-                                          typename Mma<T>::Acc (&acc)[S::FM][S::FN], L load,
+                                          typename Mma<T>::Acc (&acc)[S::FM][S::FN], F first, L load,
                                           FA frag_a, FB frag_b, H ahead)
 {
     constexpr int FM = S::FM, FN = S::FN;
+    constexpr uint32_t kAhead = DIRECT ? 2 : 4;  // steps from a step to what it fetches
     constexpr int kWait = FM / 4;  // rows of the second half before the barrier
     constexpr int kReads = (FM + FN + FM - kWait - 1) / (FM - kWait);
     constexpr int kLoads = (LOADS + FM - kWait - 1) / (FM - kWait);
@@ -383,7 +264,7 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
     auto step = [&](auto fast, auto stage, uint32_t k) {
         constexpr uint32_t kHere = decltype(stage)::value * STAGE;
         constexpr uint32_t kThere = STAGE - kHere;
-        ahead(k + 2);
+        ahead(k + kAhead);
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             products(i, b[0]);
@@ -396,7 +277,7 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
             products(i, b[1]);
             if (i == kWait - 1) {
                 __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave has left the stage
-                wait_loads<0>();
+                if constexpr (DIRECT) wait_loads<0>();
                 block_barrier();
             } else if (i >= kWait) {
 #pragma unroll
@@ -406,7 +287,7 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
                 }
 #pragma unroll
                 for (int p = (i - kWait) * kLoads; p < (i - kWait + 1) * kLoads; ++p)
-                    if (p < LOADS) load(fast, k + 2, base + kHere, p);
+                    if (p < LOADS) load(fast, stage, k + 2, base + kHere, p);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -414,15 +295,25 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
     typedef std::integral_constant<int, 0> Even;
     typedef std::integral_constant<int, 1> Odd;
     ahead(0);
+    if constexpr (!DIRECT) {
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) load(std::false_type(), 0, base, i);
-    ahead(1);
-    if (steps > 1) {
+        for (int i = 0; i < LOADS; ++i) first(Even(), i);
+        ahead(1);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load(std::false_type(), 1, base + STAGE, i);
-        wait_loads<LOADS>();
+        for (int i = 0; i < LOADS; ++i) first(Odd(), i);
+        ahead(2);
+    }
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) load(std::false_type(), Even(), 0, base, i);
+    ahead(kAhead - 1);
+    if (steps > 1)
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load(std::false_type(), Odd(), 1, base + STAGE, i);
+    if constexpr (DIRECT) {
+        if (steps > 1) wait_loads<LOADS>();
+        else wait_loads<0>();
     } else {
-        wait_loads<0>();
+        __builtin_amdgcn_s_waitcnt(0xc07f);
     }
     block_barrier();
 #pragma unroll
@@ -430,7 +321,7 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
 #pragma unroll
     for (int i = 0; i < FM; ++i) a[i] = frag_a(pipe_lds, i, 0);
     uint32_t k = 0;
-    for (; k + 3 < whole; k += 2) {
+    for (; k + kAhead + 1 < whole; k += 2) {
         step(std::true_type(), Even(), k);
         step(std::true_type(), Odd(), k + 1);
     }
@@ -445,22 +336,24 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
 // How the operands of a product of rows, and of the weights' gradient, are staged.
 template <class T, class S, bool ACROSS>
 struct RowsParts {
-    typedef PipeAlong<T, S::BM, S::THREADS> A;
-    typedef typename std::conditional<ACROSS, PipeAcross<T, S::BN, S::THREADS>,
-                                      PipeAlong<T, S::BN, S::THREADS>>::type B;
+    typedef Along<T, S::BM, S::THREADS> A;
+    typedef typename std::conditional<ACROSS, Across<T, S::BN, S::THREADS>,
+                                      Along<T, S::BN, S::THREADS>>::type B;
     static constexpr uint32_t STAGE = A::kBytes + B::kBytes;
 };
 template <class T, class S>
 struct DwParts {
-    typedef PipeAcross<T, S::BM, S::THREADS> A;
-    typedef PipeAcross<T, S::BN, S::THREADS> B;
+    typedef Across<T, S::BM, S::THREADS> A;
+    typedef Across<T, S::BN, S::THREADS> B;
     static constexpr uint32_t STAGE = A::kBytes + B::kBytes;
 };
 
-template <class T, class O, class S, bool ACROSS>
+// T: element of the operands; O: of the result; ACROSS: the weights lie across the
+// reduction; DIRECT: every row at a multiple of 16 bytes, and all rows that a tile can take within
+// 32-bit offsets of one address.
+template <class T, class O, class S, bool ACROSS, bool DIRECT>
 __global__ void __launch_bounds__(S::THREADS)
-    __attribute__((amdgpu_waves_per_eu(S::WAVES_PER_SIMD, S::WAVES_PER_SIMD)))
-    k_rows_pipe(RowsArgs g)
+    __attribute__((amdgpu_waves_per_eu(S::WAVES_PER_SIMD, S::WAVES_PER_SIMD))) k_rows(RowsArgs g)
 {
     typedef RowsParts<T, S, ACROSS> P;
     typedef typename P::A A;
@@ -469,7 +362,11 @@ __global__ void __launch_bounds__(S::THREADS)
     const Tile t = find_tile(tile_of_block(blockIdx.x, g.span), g.offsets, g.experts, g.rows, kLog2,
                              g.n_tiles);
     if (t.group > g.experts) return;
-    const uint32_t m0 = t.begin + t.m * S::BM, n0 = t.n * S::BN;
+    const uint32_t m0 = t.begin + t.m * S::BM;
+    // (a last tile across that passes through registers starts where it ends with the last column:
+    // no piece then reaches past a row, and the columns that two tiles share get the same bits)
+    const bool full = ACROSS && !DIRECT && g.cols >= S::BN;
+    const uint32_t n0 = full && g.cols - t.n * S::BN < S::BN ? g.cols - S::BN : t.n * S::BN;
     const uint32_t high = t.end - m0 < S::BM ? t.end - m0 : S::BM;
     const uint32_t wide = g.cols - n0 < S::BN ? g.cols - n0 : S::BN;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -478,74 +375,124 @@ __global__ void __launch_bounds__(S::THREADS)
     typename Mma<T>::Acc acc[S::FM][S::FN] = {};
 
     if (real) {
-        A a;
+        // rows past the tile's last one read that one: their results are not stored
         const char *rows = g.order ? g.a : g.a + (int64_t)m0 * g.lda;
-        a.init([&](uint32_t r) {
-            r = r < high ? r : high - 1;
-            return (g.order ? source_row(g, m0 + r) : r) * (uint32_t)g.lda;
-        });
-        const char *w = g.b + (int64_t)t.group * g.b_stride;
-        const uint32_t steps = (g.bytes + kStepBytes - 1) / kStepBytes;
-        const uint32_t whole = g.bytes / kStepBytes, mine = wave * 1024;
-        auto fa = [&](const char *lds, int i, int kk) { return A::frag(lds, wm + i * 16, kk); };
-        auto fb = [&](const char *lds, int j, int kk) {
-            if constexpr (ACROSS) return B::frag(lds + A::kBytes, wn, j, kk);
-            else return B::frag(lds + A::kBytes, wn + j * 16, kk);
+        auto row_a = [&](int i) {
+            const uint32_t r = A::row_of(i) < high ? A::row_of(i) : high - 1;
+            return g.order ? source_row(g, m0 + r) : r;
         };
-        if constexpr (ACROSS) {
-            w += n0 * 2;
-            const uint32_t offset = B::row_of(0) * (uint32_t)g.ldb + B::byte_of(wide);
-            run_steps<T, S, A::kLoads + B::kLoads, P::STAGE>(
-                steps, whole, acc,
-                [&](auto fast, uint32_t step, uint32_t lds, int i) {
-                    if (!decltype(fast)::value && step >= steps) return;
-                    if (i < A::kLoads) {
-                        if constexpr (decltype(fast)::value) a.load(rows, step, lds + mine, i);
-                        else a.load_end(rows, step, g.bytes, lds + mine, i);
+        const char *w = g.b + (int64_t)t.group * g.b_stride +
+                        (ACROSS ? (int64_t)n0 * sizeof(T) : (int64_t)n0 * g.ldb);
+        auto row_b = [&](int i) { return B::row_of(i) < wide ? B::row_of(i) : wide - 1; };
+        const uint32_t steps = (g.bytes + kStepBytes - 1) / kStepBytes;
+        // steps that need no check: all but the reduction's ragged end
+        const uint32_t whole = ACROSS && !DIRECT && !full ? 0 : g.bytes / kStepBytes;
+        auto fa = [&](const char *lds, int i, int kk) { return A::frag(lds, wm, i, kk); };
+        auto fb = [&](const char *lds, int j, int kk) {
+            return B::frag(lds + A::kBytes, wn, j, kk);
+        };
+        const uint32_t byte_a = A::byte(), byte_b = B::byte();
+        if constexpr (DIRECT) {
+            uint32_t at_a[A::kLoads], at_b[ACROSS ? 1 : B::kLoads];
+#pragma unroll
+            for (int i = 0; i < A::kLoads; ++i) at_a[i] = row_a(i) * (uint32_t)g.lda + byte_a;
+            if constexpr (ACROSS) {
+                // a piece past the last column reads the first one
+                at_b[0] = B::row_of(0) * (uint32_t)g.ldb + (byte_b < wide * 2 ? byte_b : 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < B::kLoads; ++i) at_b[i] = row_b(i) * (uint32_t)g.ldb + byte_b;
+            }
+            auto load = [&](auto fast, auto parity, uint32_t step, uint32_t lds, int i) {
+                if (!decltype(fast)::value && step >= steps) return;
+                const uint32_t from = step * kStepBytes;
+                const char *base;
+                uint32_t at;
+                bool in = true;
+                if (i < A::kLoads) {
+                    base = rows + from, at = at_a[i], lds += A::place_of(i, wave);
+                    if constexpr (!decltype(fast)::value) in = from + byte_a < g.bytes;
+                } else {
+                    i -= A::kLoads;
+                    lds += A::kBytes + B::place_of(i, wave);
+                    if constexpr (ACROSS) {
+                        const uint32_t r = step * B::kRows + i * B::kRowsEach;
+                        base = w + (int64_t)r * g.ldb, at = at_b[0];
+                        if constexpr (!decltype(fast)::value)
+                            in = (step * B::kRows + B::row_of(i)) * 2 < g.bytes;
                     } else {
-                        i -= A::kLoads;
-                        lds += A::kBytes + B::place_of(i, wave);
-                        const char *base =
-                            w + (int64_t)(step * B::kRows + i * B::kRowsEach) * g.ldb;
-                        if constexpr (decltype(fast)::value) load_to_lds(base, offset, lds);
-                        else
-                            load_to_lds((step * B::kRows + B::row_of(i)) * 2 < g.bytes
-                                            ? base + offset
-                                            : (const char *)&kZeros,
-                                        lds);
+                        base = w + from, at = at_b[i];
+                        if constexpr (!decltype(fast)::value) in = from + byte_b < g.bytes;
                     }
-                },
-                fa, fb, [](uint32_t) {});
+                }
+                if constexpr (decltype(fast)::value) load_to_lds(base, at, lds);
+                else load_to_lds(in ? base + at : (const char *)&kZeros, lds);
+            };
+            run_steps<T, S, true, A::kLoads + B::kLoads, P::STAGE>(
+                steps, whole, acc, [](auto, int) {}, load, fa, fb, [](uint32_t) {});
         } else {
-            B b;
-            w += (int64_t)n0 * g.ldb;
-            b.init([&](uint32_t r) { return (r < wide ? r : wide - 1) * (uint32_t)g.ldb; });
-            run_steps<T, S, A::kLoads + B::kLoads, P::STAGE>(
-                steps, whole, acc,
-                [&](auto fast, uint32_t step, uint32_t lds, int i) {
-                    if (!decltype(fast)::value && step >= steps) return;
-                    lds += mine;
-                    if (i < A::kLoads) {
-                        if constexpr (decltype(fast)::value) a.load(rows, step, lds, i);
-                        else a.load_end(rows, step, g.bytes, lds, i);
+            const char *from_a[A::kLoads], *from_b[ACROSS ? 1 : B::kLoads];
+            u32x4 kept_a[2][A::kLoads], kept_b[2][B::kLoads];
+#pragma unroll
+            for (int i = 0; i < A::kLoads; ++i) from_a[i] = rows + (int64_t)row_a(i) * g.lda + byte_a;
+            if constexpr (ACROSS) {
+                from_b[0] = w + (int64_t)B::row_of(0) * g.ldb + byte_b;
+            } else {
+#pragma unroll
+                for (int i = 0; i < B::kLoads; ++i)
+                    from_b[i] = w + (int64_t)row_b(i) * g.ldb + byte_b;
+            }
+            const int left_b = (int)(g.cols - n0) * 2 - (int)byte_b;  // ACROSS: of a row
+            auto fetch = [&](auto fast, auto parity, uint32_t step, int i) {
+                constexpr int kTo = decltype(parity)::value;
+                if (!decltype(fast)::value && step >= steps) return;
+                const uint32_t from = step * kStepBytes;
+                const bool whole_step = decltype(fast)::value;
+                if (i < A::kLoads) {
+                    kept_a[kTo][i] = load16<T>(from_a[i] + from,
+                                          whole_step ? 16 : (int)g.bytes - (int)(from + byte_a));
+                } else {
+                    i -= A::kLoads;
+                    if constexpr (ACROSS) {
+                        const uint32_t r = step * B::kRows + i * B::kRowsEach;
+                        const bool in =
+                            whole_step || (step * B::kRows + B::row_of(i)) * 2 < g.bytes;
+                        kept_b[kTo][i] =
+                            load16<T>(from_b[0] + (int64_t)r * g.ldb,
+                                      whole_step || (full && in) ? 16 : in ? left_b : 0);
                     } else {
-                        i -= A::kLoads;
-                        lds += A::kBytes;
-                        if constexpr (decltype(fast)::value) b.load(w, step, lds, i);
-                        else b.load_end(w, step, g.bytes, lds, i);
+                        kept_b[kTo][i] =
+                            load16<T>(from_b[i] + from,
+                                      whole_step ? 16 : (int)g.bytes - (int)(from + byte_b));
                     }
-                },
-                fa, fb, [](uint32_t) {});
+                }
+            };
+            auto load = [&](auto fast, auto parity, uint32_t step, uint32_t lds, int i) {
+                if (!decltype(fast)::value && step >= steps) return;
+                if (i < A::kLoads) put_in_lds(kept_a[decltype(parity)::value][i], lds + A::place_of(i, wave));
+                else
+                    put_in_lds(kept_b[decltype(parity)::value][i - A::kLoads],
+                               lds + A::kBytes + B::place_of(i - A::kLoads, wave));
+                fetch(fast, parity, step + 2, i);
+            };
+            auto first = [&](auto parity, int i) {
+                fetch(std::false_type(), parity, decltype(parity)::value, i);
+            };
+            if constexpr (S::FM >= 4)
+                run_steps_sharing<T, S, false, A::kLoads + B::kLoads, P::STAGE>(
+                    steps, whole, acc, first, load, fa, fb, [](uint32_t) {});
+            else
+                run_steps<T, S, false, A::kLoads + B::kLoads, P::STAGE>(
+                    steps, whole, acc, first, load, fa, fb, [](uint32_t) {});
         }
     }
     store_rows<T, O>(g, pipe_lds + wave * (S::FM * S::FN * 512), t, acc, real, m0 + wm, n0 + wn,
                      (int)high - (int)wm, (int)wide - (int)wn);
 }
 
-template <class T, class S>
+template <class T, class S, bool DIRECT>
 __global__ void __launch_bounds__(S::THREADS)
-    __attribute__((amdgpu_waves_per_eu(S::WAVES_PER_SIMD, S::WAVES_PER_SIMD)))
-    k_dw_pipe(DwArgs g)
+    __attribute__((amdgpu_waves_per_eu(S::WAVES_PER_SIMD, S::WAVES_PER_SIMD))) k_dw(DwArgs g)
 {
     typedef DwParts<T, S> P;
     typedef typename P::A A;
@@ -554,7 +501,13 @@ __global__ void __launch_bounds__(S::THREADS)
     const uint32_t each = g.n_tiles * g.k_tiles, e = tile / each;
     if (e >= g.experts) return;
     const uint32_t in = tile - e * each;
-    const uint32_t n0 = in % g.n_tiles * S::BM, k0 = in / g.n_tiles * S::BN;
+    uint32_t n0 = in % g.n_tiles * S::BM, k0 = in / g.n_tiles * S::BN;
+    // (last tiles that pass through registers start where they end with the last column)
+    const bool full = !DIRECT && g.n >= S::BM && g.k >= S::BN;
+    if (full) {
+        n0 = g.n - n0 < S::BM ? g.n - S::BM : n0;
+        k0 = g.k - k0 < S::BN ? g.k - S::BN : k0;
+    }
     const uint32_t high = g.n - n0 < S::BM ? g.n - n0 : S::BM;
     const uint32_t wide = g.k - k0 < S::BN ? g.k - k0 : S::BN;
     uint32_t end = __builtin_amdgcn_readfirstlane(g.offsets[e + 1]);
@@ -572,57 +525,100 @@ __global__ void __launch_bounds__(S::THREADS)
         const char *dy = g.dy + (int64_t)begin * g.lddy + n0 * 2;
         const char *x = g.x + k0 * 2 + (g.order ? 0 : (int64_t)begin * g.ldx);
         constexpr int kPerWave = 64 / B::kPieces;  // rows of x of one wave's load
-        uint32_t from[B::kLoads * kPerWave];       // their offsets, looked up half a step ahead
-        uint32_t of_row[kPerWave];                 // all ones in the lanes of each of these rows
+        uint32_t from[B::kLoads * kPerWave];       // these rows, looked up half a step ahead
+        uint32_t of_row[kPerWave];                 // all ones in the lanes of each of them
 #pragma unroll
         for (int q = 0; q < kPerWave; ++q)
             of_row[q] = lane / B::kPieces == (uint32_t)q ? ~0u : 0u;
-        const uint32_t offset = A::row_of(0) * (uint32_t)g.lddy + A::byte_of(high);
-        const uint32_t byte = B::byte_of(wide);
+        const uint32_t byte_a = A::byte(), byte_b = B::byte();
         const uint32_t count = end - begin, steps = (count + A::kRows - 1) / A::kRows;
-        run_steps_sharing<T, S, A::kLoads + B::kLoads, P::STAGE>(
-            steps, count / A::kRows, acc,
-            [&](auto fast, uint32_t step, uint32_t lds, int i) {
+        const uint32_t whole = !DIRECT && !full ? 0 : count / A::kRows;
+        auto ahead = [&](uint32_t step) {
+#pragma unroll
+            for (int i = 0; i < B::kLoads; ++i)
+#pragma unroll
+                for (int q = 0; q < kPerWave; ++q) {
+                    uint32_t s = step * A::kRows + i * B::kRowsEach + wave * kPerWave + q;
+                    s = s < count ? s : count - 1;
+                    if (g.order) {
+                        s = g.divide((uint32_t)order[begin + s]);
+                        s = s < g.x_rows ? s : g.x_rows - 1;
+                    }
+                    from[i * kPerWave + q] = DIRECT ? s * (uint32_t)g.ldx : s;
+                }
+        };
+        auto row_x = [&](int i) {
+            uint32_t at = 0;
+#pragma unroll
+            for (int q = 0; q < kPerWave; ++q) at |= from[i * kPerWave + q] & of_row[q];
+            return at;
+        };
+        auto fa = [&](const char *lds, int i, int kk) { return A::frag(lds, wm, i, kk); };
+        auto fb = [&](const char *lds, int j, int kk) {
+            return B::frag(lds + A::kBytes, wn, j, kk);
+        };
+        if constexpr (DIRECT) {
+            // a piece past the last column reads the first one: its results are not stored
+            const uint32_t at_a =
+                A::row_of(0) * (uint32_t)g.lddy + (byte_a < high * 2 ? byte_a : 0);
+            const uint32_t at_b = byte_b < wide * 2 ? byte_b : 0;
+            auto load = [&](auto fast, auto parity, uint32_t step, uint32_t lds, int i) {
                 if (!decltype(fast)::value && step >= steps) return;
+                const char *base = x;
+                uint32_t at, row;
                 if (i < A::kLoads) {
-                    const char *base =
-                        dy + (int64_t)(step * A::kRows + i * A::kRowsEach) * g.lddy;
-                    lds += A::place_of(i, wave);
-                    if constexpr (decltype(fast)::value) load_to_lds(base, offset, lds);
-                    else
-                        load_to_lds(step * A::kRows + A::row_of(i) < count ? base + offset
-                                                                           : (const char *)&kZeros,
-                                    lds);
+                    base = dy + (int64_t)(step * A::kRows + i * A::kRowsEach) * g.lddy;
+                    at = at_a, row = A::row_of(i), lds += A::place_of(i, wave);
                 } else {
                     i -= A::kLoads;
+                    at = row_x(i) + at_b, row = B::row_of(i);
                     lds += A::kBytes + B::place_of(i, wave);
-                    uint32_t at = 0;
-#pragma unroll
-                    for (int q = 0; q < kPerWave; ++q) at |= from[i * kPerWave + q] & of_row[q];
-                    at += byte;
-                    if constexpr (decltype(fast)::value) load_to_lds(x, at, lds);
-                    else
-                        load_to_lds(step * A::kRows + B::row_of(i) < count ? x + at
-                                                                           : (const char *)&kZeros,
-                                    lds);
                 }
-            },
-            [&](const char *lds, int i, int kk) { return A::frag(lds, wm, i, kk); },
-            [&](const char *lds, int j, int kk) { return B::frag(lds + A::kBytes, wn, j, kk); },
-            [&](uint32_t step) {
-#pragma unroll
-                for (int i = 0; i < B::kLoads; ++i)
-#pragma unroll
-                    for (int q = 0; q < kPerWave; ++q) {
-                        uint32_t s = step * A::kRows + i * B::kRowsEach + wave * kPerWave + q;
-                        s = s < count ? s : count - 1;
-                        if (g.order) {
-                            s = g.divide((uint32_t)order[begin + s]);
-                            s = s < g.x_rows ? s : g.x_rows - 1;
-                        }
-                        from[i * kPerWave + q] = s * (uint32_t)g.ldx;
-                    }
-            });
+                if constexpr (decltype(fast)::value) load_to_lds(base, at, lds);
+                else
+                    load_to_lds(step * A::kRows + row < count ? base + at : (const char *)&kZeros,
+                                lds);
+            };
+            run_steps_sharing<T, S, true, A::kLoads + B::kLoads, P::STAGE>(
+                steps, whole, acc, [](auto, int) {}, load, fa, fb, ahead);
+        } else {
+            u32x4 kept_a[2][A::kLoads], kept_b[2][B::kLoads];
+            const int left_a = (int)(g.n - n0) * 2 - (int)byte_a;
+            const int left_b = (int)(g.k - k0) * 2 - (int)byte_b;
+            const char *from_a = dy + (int64_t)A::row_of(0) * g.lddy + byte_a, *from_b = x + byte_b;
+            auto fetch = [&](auto fast, auto parity, uint32_t step, int i) {
+                constexpr int kTo = decltype(parity)::value;
+                if (!decltype(fast)::value && step >= steps) return;
+                if (i < A::kLoads) {
+                    const bool in =
+                        decltype(fast)::value || step * A::kRows + A::row_of(i) < count;
+                    kept_a[kTo][i] = load16<T>(
+                        from_a + (int64_t)(step * A::kRows + i * A::kRowsEach) * g.lddy,
+                        decltype(fast)::value || (full && in) ? 16 : in ? left_a : 0);
+                } else {
+                    i -= A::kLoads;
+                    const bool in =
+                        decltype(fast)::value || step * A::kRows + B::row_of(i) < count;
+                    kept_b[kTo][i] =
+                        load16<T>(from_b + (int64_t)row_x(i) * g.ldx,
+                                  decltype(fast)::value || (full && in) ? 16 : in ? left_b : 0);
+                }
+            };
+            auto load = [&](auto fast, auto parity, uint32_t step, uint32_t lds, int i) {
+                if (!decltype(fast)::value && step >= steps) return;
+                if (i < A::kLoads) put_in_lds(kept_a[decltype(parity)::value][i], lds + A::place_of(i, wave));
+                else
+                    put_in_lds(kept_b[decltype(parity)::value][i - A::kLoads],
+                               lds + A::kBytes + B::place_of(i - A::kLoads, wave));
+                fetch(fast, parity, step + 2, i);
+            };
+            run_steps_sharing<T, S, false, A::kLoads + B::kLoads, P::STAGE>(
+                steps, whole, acc,
+                [&](auto parity, int i) {
+                    fetch(std::false_type(), parity, decltype(parity)::value, i);
+                },
+                load, fa, fb, ahead);
+        }
     }
     store_part<T, S::FM, S::FN>(pipe_lds + wave * (S::FM * S::FN * 512),
                                 (T *)g.out + ((int64_t)e * g.n + n0 + wm) * g.k + k0 + wn,
@@ -795,14 +791,14 @@ hist_status_t launch(K kernel, uint64_t blocks, uint32_t threads, uint32_t lds, 
 
 inline bool aligned16(const void *p, int64_t ld_bytes) { return !misaligned(p, 16) && ld_bytes % 16 == 0; }
 
-template <class T, class O, bool ACROSS, class S>
-hist_status_t launch_pipe(RowsArgs g, hipStream_t stream)
+template <class T, class O, bool ACROSS, bool DIRECT, class S>
+hist_status_t launch_tiles(RowsArgs g, hipStream_t stream)
 {
     g.n_tiles = (g.cols + S::BN - 1) / S::BN;
     const uint64_t tiles =
         most_row_tiles(g.rows, g.offsets ? g.experts + 1 : 1, S::BM) * g.n_tiles;
     const uint64_t blocks = blocks_for(tiles, &g.span);
-    return launch(k_rows_pipe<T, O, S, ACROSS>, blocks, S::THREADS,
+    return launch(k_rows<T, O, S, ACROSS, DIRECT>, blocks, S::THREADS,
                   2 * RowsParts<T, S, ACROSS>::STAGE, stream, &g);
 }
 
@@ -851,36 +847,31 @@ hist_status_t launch_rows(RowsArgs g, hipStream_t stream)
         g.bytes % 16 == 0 && (!ACROSS || g.cols % 8 == 0) &&
         near(g.order ? g.a_rows : 256, g.lda) && near(256, g.ldb)) {
         if (each >= 192 && g.cols > 128 && tiles(256, 256) >= 256)
-            return launch_pipe<T, O, ACROSS, Shape<256, 256, 2, 4, 1>>(g, stream);
+            return launch_tiles<T, O, ACROSS, true, Shape<256, 256, 2, 4, 1>>(g, stream);
         if (each >= 80 && tiles(128, 128) >= 256)
-            return launch_pipe<T, O, ACROSS, Shape<128, 128, 2, 2, 2>>(g, stream);
+            return launch_tiles<T, O, ACROSS, true, Shape<128, 128, 2, 2, 2>>(g, stream);
         if (each > 24 && tiles(64, 128) >= 512)
-            return launch_pipe<T, O, ACROSS, Shape<64, 128, 2, 2, 3>>(g, stream);
+            return launch_tiles<T, O, ACROSS, true, Shape<64, 128, 2, 2, 3>>(g, stream);
         if constexpr (ACROSS) {
-            return each > 24 ? launch_pipe<T, O, ACROSS, Shape<64, 128, 2, 2, 3>>(g, stream)
-                             : launch_pipe<T, O, ACROSS, Shape<32, 128, 2, 2, 4>>(g, stream);
+            return each > 24 ? launch_tiles<T, O, ACROSS, true, Shape<64, 128, 2, 2, 3>>(g, stream)
+                             : launch_tiles<T, O, ACROSS, true, Shape<32, 128, 2, 2, 4>>(g, stream);
         } else {
             if (each <= 24 && tiles(32, 128) >= 256)
-                return launch_pipe<T, O, ACROSS, Shape<32, 128, 1, 4, 4>>(g, stream);
-            return launch_pipe<T, O, ACROSS, Shape<64, 64, 2, 2, 4>>(g, stream);
+                return launch_tiles<T, O, ACROSS, true, Shape<32, 128, 1, 4, 4>>(g, stream);
+            return launch_tiles<T, O, ACROSS, true, Shape<64, 64, 2, 2, 4>>(g, stream);
         }
     }
-    typedef typename std::conditional<ACROSS, Across<T, kTile, kThreads>,
-                                      Along<T, kTile, kThreads>>::type B;
-    g.n_tiles = (g.cols + kTile - 1) / kTile;
-    const uint64_t all =
-        most_row_tiles(g.rows, g.offsets ? g.experts + 1 : 1, kTile) * g.n_tiles;
-    const uint64_t blocks = blocks_for(all, &g.span);
-    return launch(k_rows<T, O, B>, blocks, kThreads, 0, stream, &g);
+    return each > 24 ? launch_tiles<T, O, ACROSS, false, Shape<128, 128, 2, 2, 2>>(g, stream)
+                     : launch_tiles<T, O, ACROSS, false, Shape<32, 128, 2, 2, 3>>(g, stream);
 }
 
-template <class T, class S>
-hist_status_t launch_dw_pipe(DwArgs g, hipStream_t stream)
+template <class T, bool DIRECT, class S>
+hist_status_t launch_dw_tiles(DwArgs g, hipStream_t stream)
 {
     g.n_tiles = (g.n + S::BM - 1) / S::BM;
     g.k_tiles = (g.k + S::BN - 1) / S::BN;
     const uint64_t blocks = blocks_for((uint64_t)g.n_tiles * g.k_tiles * g.experts, &g.span);
-    return launch(k_dw_pipe<T, S>, blocks, S::THREADS, 2 * DwParts<T, S>::STAGE, stream, &g);
+    return launch(k_dw<T, S, DIRECT>, blocks, S::THREADS, 2 * DwParts<T, S>::STAGE, stream, &g);
 }
 
 template <class T>
@@ -890,13 +881,10 @@ hist_status_t launch_dw(DwArgs g, hipStream_t stream)
         near(64, g.lddy) && near(g.x_rows, g.ldx)) {
         // enough large tiles for 256 CUs, or small ones
         return (uint64_t)g.experts * ((g.n + 255) / 256) * ((g.k + 255) / 256) >= 256
-                   ? launch_dw_pipe<T, Shape<256, 256, 2, 4, 1>>(g, stream)
-                   : launch_dw_pipe<T, Shape<128, 128, 2, 2, 2>>(g, stream);
+                   ? launch_dw_tiles<T, true, Shape<256, 256, 2, 4, 1>>(g, stream)
+                   : launch_dw_tiles<T, true, Shape<128, 128, 2, 2, 2>>(g, stream);
     }
-    g.n_tiles = (g.n + kTile - 1) / kTile;
-    g.k_tiles = (g.k + kTile - 1) / kTile;
-    const uint64_t blocks = blocks_for((uint64_t)g.n_tiles * g.k_tiles * g.experts, &g.span);
-    return launch(k_dw<T>, blocks, kThreads, 0, stream, &g);
+    return launch_dw_tiles<T, false, Shape<128, 128, 2, 2, 2>>(g, stream);
 }
 
 // Checks that the products share. `unit`: bytes of an element of the result

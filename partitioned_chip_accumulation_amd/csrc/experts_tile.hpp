@@ -3,13 +3,13 @@
 // in the ragged list of the experts' rows.
 //
 // A tile is D[m][n] = sum_r A[m][r] B[n][r]. An operand lies in memory either
-// along the reduction (kAlong: a row of memory is one m or n, its elements
-// consecutive r) or across it (kAcross: a row of memory is one r, its
+// along the reduction (Along: a row of memory is one m or n, its elements
+// consecutive r) or across it (Across: a row of memory is one r, its
 // elements consecutive m or n). Both are staged in steps of 128 bytes of
 // reduction (64 16-bit elements, 128 8-bit ones):
 //
-//   kAlong   [rows][128 bytes]; a lane's fragment is one 16-byte read.
-//   kAcross  [64][columns]; a lane's fragment is two transposing 8-byte reads.
+//   Along   [rows][128 bytes]; a lane's fragment is one 16-byte read.
+//   Across  [64][columns]; a lane's fragment is two transposing 8-byte reads.
 //
 // The fragments go to the matrix instruction with B first, so that a lane
 // holds four consecutive columns n of one row m of the result.
@@ -102,50 +102,39 @@ __device__ __forceinline__ u32x4 load16(const char *p, int left)
 }
 
 // ---------------------------------------------------------------------------
-// Staging. A thread moves kLoads 16-byte pieces of the operand per step; piece
-// i * THREADS + thread goes to that place in LDS, and the place in the row
-// that it comes from is permuted so that the fragments' reads meet no bank
-// twice.
+// ---------------------------------------------------------------------------
+// How an operand lies in LDS. A thread moves kLoads 16-byte pieces of it per step; the pieces of
+// one load of a wave lie together, in the order of the lanes, and the place in the
+// row that a piece comes from is permuted so that the fragments' reads meet no bank twice.
 
-// Along the reduction: ROWS rows of 128 bytes. Eight pieces a row, piece s of
-// row r holding the row's bytes 16 * (s ^ (r >> 1) % 8).
+// Along the reduction: ROWS rows of 128 bytes. Eight pieces a row, piece s of row r holding
+// the row's bytes 16 * (s ^ (r >> 1) % 8). (A 16-byte read serves 16 lanes at a time: 0-3, 12-15
+// and 20-27 first, then 4-11, 16-19 and 28-31, and so in the upper half.)
 template <class T, int ROWS, int THREADS>
 struct Along {
     static constexpr bool kAcross = false;
     static constexpr int kLoads = ROWS * 8 / THREADS;
     static constexpr uint32_t kBytes = ROWS * kStepBytes;
     static_assert(ROWS * 8 % THREADS == 0 && THREADS / 8 % 16 == 0, "pieces of one permutation");
-    const char *row[kLoads];
-    uint32_t at;  // this thread's byte within a row's step
-    u32x4 v[kLoads];
 
-    // row_of(r): the address of row r's first element, for r < ROWS.
-    template <class F>
-    __device__ __forceinline__ void init(F row_of)
+    static __device__ __forceinline__ uint32_t row_of(int i)
     {
-        const uint32_t r = threadIdx.x / 8;
-        at = ((threadIdx.x % 8) ^ ((r >> 1) & 7)) * 16;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) row[i] = row_of(i * (THREADS / 8) + r);
+        return i * (THREADS / 8) + threadIdx.x / 8;
     }
-    __device__ __forceinline__ void fetch(uint32_t step, uint32_t bytes)
+    // This thread's byte within a row's step, and the place of its wave's load i.
+    static __device__ __forceinline__ uint32_t byte()
     {
-        const uint32_t from = step * kStepBytes + at;
-        const int left = (int)bytes - (int)from;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) v[i] = load16<T>(row[i] + from, left);
+        return ((threadIdx.x % 8) ^ ((threadIdx.x / 16) & 7)) * 16;
     }
-    __device__ __forceinline__ void store(char *lds) const
+    static __device__ __forceinline__ uint32_t place_of(int i, uint32_t wave)
     {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            *(u32x4 *)(lds + (i * THREADS + threadIdx.x) * 16) = v[i];
+        return (i * (THREADS / 64) + wave) * 1024;
     }
-    // Fragment of rows [first, first + 16), reduction part kk (64 bytes).
+    // Fragment i of the part that starts at row first, half kk (64 bytes) of the step.
     static __device__ __forceinline__ typename Mma<T>::Frag frag(const char *lds, uint32_t first,
-                                                                 uint32_t kk)
+                                                                 int i, int kk)
     {
-        const uint32_t lane = threadIdx.x % 64, r = first + lane % 16;
+        const uint32_t lane = threadIdx.x % 64, r = first + i * 16 + lane % 16;
         const uint32_t piece = (lane / 16 + 4 * kk) ^ ((r >> 1) & 7);
         return *(const typename Mma<T>::Frag *)(lds + r * kStepBytes + piece * 16);
     }
@@ -154,74 +143,67 @@ struct Along {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// Across the reduction: 64 rows of COLS 16-bit elements. The 32-byte parts of
-// row r are permuted by part ^ h(r), h(r) = r % 4 + 4 * (r / 8 % 2): the 16 lanes of
-// a transposing read take 32 bytes from each of four rows, and the eight rows
-// that half a wave takes then lie in eight different bank groups.
+// Across the reduction. One load of a wave holds kTogether whole rows (1024 bytes), so
+// they lie together in LDS; 64 bytes follow them, and 128 more follow each four loads
+// of two rows. Within a row the 32-byte parts are permuted by part ^ r % kTogether.
+// The eight rows that half a wave takes 32 bytes of in one transposing read, r0 to r0 + 3 and r0 + 8
+// to r0 + 11, then meet all 64 banks once, and the fragments of one operand need
+// only kTogether addresses in registers (with a permutation of all of a row's parts by
+// the row each fragment needed its own, and they did not fit).
 template <class T, int COLS, int THREADS>
 struct Across {
     static constexpr bool kAcross = true;
     static constexpr int kRows = kStepBytes / 2;
-    static constexpr int kPieces = COLS / 8;  // of one row
+    static constexpr int kPieces = COLS / 8;
     static constexpr int kLoads = kRows * kPieces / THREADS;
-    static constexpr int kRowsEach = THREADS / kPieces;  // rows between a thread's pieces
-    static constexpr uint32_t kBytes = kRows * COLS * 2;
-    int left;      // bytes of the row from this thread's column on
-    uint32_t col;  // byte offset of this thread's column
-    u32x4 v[kLoads];
+    static constexpr int kRowsEach = THREADS / kPieces;
+    static constexpr int kTogether = 64 / kPieces;
+    static_assert(kRows * kPieces % THREADS == 0 && (kTogether == 2 || kTogether == 4),
+                  "rows of 128 or 256 columns");
 
-    static __device__ __forceinline__ uint32_t mix(uint32_t r)
+    // Where load number l of a step (a wave's) lies.
+    static constexpr __device__ uint32_t place(uint32_t l)
     {
-        return (r & 3) | ((r >> 1) & 4);
+        return l * 1088 + (kTogether == 2 ? l / 4 * 128 : 0);
+    }
+    static constexpr uint32_t kBytes = kRows / kTogether * 1088 +
+                                       (kTogether == 2 ? kRows / kTogether / 4 * 128 : 0);
+    // The place of this wave's load i.
+    static __device__ __forceinline__ uint32_t place_of(int i, uint32_t wave)
+    {
+        return place(i * (THREADS / 64) + wave);
     }
     static __device__ __forceinline__ uint32_t row_of(int i)
     {
         return i * kRowsEach + threadIdx.x / kPieces;
     }
-    // cols: columns of the operand that are left from the tile's first one.
-    // (a thread's rows are 16 apart: one permutation)
-    __device__ __forceinline__ void init(int cols)
+    // The byte in a row of this thread's pieces.
+    static __device__ __forceinline__ uint32_t byte()
     {
-        const uint32_t r = threadIdx.x / kPieces;
-        col = ((threadIdx.x % kPieces) ^ (mix(r) << 1)) * 16;
-        left = cols * 2 - (int)col;
+        return ((threadIdx.x % kPieces) ^ (threadIdx.x / kPieces % kTogether << 1)) * 16;
     }
-    // address(r): the tile's first column in row r of this step, or nullptr
-    // for a row past the end (which reads 0).
-    template <class F>
-    __device__ __forceinline__ void fetch(F address)
-    {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const char *p = address(row_of(i));
-            v[i] = load16<T>(p + col, p ? left : 0);
-        }
-    }
-    __device__ __forceinline__ void store(char *lds) const
-    {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            *(u32x4 *)(lds + (i * THREADS + threadIdx.x) * 16) = v[i];
-    }
+    // Fragment i of the part that starts at column first (a multiple of 64), half kk.
     static __device__ __forceinline__ typename Mma<T>::Frag frag(const char *lds, uint32_t first,
-                                                                 uint32_t kk)
+                                                                 int i, int kk)
     {
-        const uint32_t lane = threadIdx.x % 64, i = lane % 16;
-        const uint32_t r = kk * 32 + lane / 16 * 8 + i / 4;  // mix(r) == mix(r + 4)
-        const char *p = lds + r * (COLS * 2) + ((first / 16) ^ mix(r)) * 32 + i % 4 * 8;
+        const uint32_t lane = threadIdx.x % 64, q = lane % 16, r = lane / 16 * 8 + q / 4;
+        const uint32_t part = (i % kTogether) ^ (r % kTogether);
+        const char *p = lds + place(r / kTogether) + r % kTogether * (COLS * 2) + first * 2 +
+                        part * 32 + q % 4 * 8;
+        p += place(kk * 32 / kTogether) + i / kTogether * kTogether * 32;
         union {
             s16x4 half[2];
             typename Mma<T>::Frag whole;
         } f;
         f.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-        f.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * COLS * 2));
+        f.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + place(4 / kTogether)));
         return f.whole;
     }
 };
 
 // ---------------------------------------------------------------------------
-// Staging without registers, for rows at 16-byte multiples: each lane's piece goes
-// from memory straight to LDS. The layouts in LDS are those of Along and Across.
+// Rows at 16-byte multiples go straight from memory to LDS, a lane's piece at a time; others
+// pass through registers.
 
 // What a piece outside the operand reads.
 static __device__ const u32x4 kZeros = {0, 0, 0, 0};
@@ -243,6 +225,13 @@ __device__ __forceinline__ void load_to_lds(const char *base, uint32_t offset, u
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(lds), "v"(offset), "s"(base));
+}
+
+// The way through registers: a lane's piece to LDS.
+__device__ __forceinline__ void put_in_lds(u32x4 v, uint32_t lds)
+{
+    typedef __attribute__((address_space(3))) u32x4 Piece;
+    *(Piece *)(uintptr_t)(lds + threadIdx.x % 64 * 16) = v;
 }
 
 // Until at most N of the wave's loads are in flight.
@@ -273,98 +262,6 @@ struct Divide {
     __device__ __forceinline__ uint32_t operator()(uint32_t n) const
     {
         return __umulhi(2 * n, mul) >> shift;
-    }
-};
-
-// Along the reduction. offset[i]: this thread's piece i from the operand's base, in the
-// first step; a step is 128 bytes further.
-template <class T, int ROWS, int THREADS>
-struct PipeAlong : Along<T, ROWS, THREADS> {
-    typedef Along<T, ROWS, THREADS> Layout;
-    uint32_t offset[Layout::kLoads];
-    uint32_t at;
-
-    // offset_of(r): the bytes from the base to row r.
-    template <class F>
-    __device__ __forceinline__ void init(F offset_of)
-    {
-        const uint32_t r = threadIdx.x / 8;
-        at = ((threadIdx.x % 8) ^ ((r >> 1) & 7)) * 16;
-#pragma unroll
-        for (int i = 0; i < Layout::kLoads; ++i) offset[i] = offset_of(i * (THREADS / 8) + r) + at;
-    }
-    // A whole step; and one that the reduction may end in, which reads 0 from there on.
-    __device__ __forceinline__ void load(const char *base, uint32_t step, uint32_t lds, int i) const
-    {
-        load_to_lds(base + (uint64_t)step * kStepBytes, offset[i], lds + i * THREADS * 16);
-    }
-    __device__ __forceinline__ void load_end(const char *base, uint32_t step, uint32_t bytes,
-                                             uint32_t lds, int i) const
-    {
-        const uint32_t from = step * kStepBytes;
-        load_to_lds(from + at < bytes ? base + from + offset[i] : (const char *)&kZeros,
-                    lds + i * THREADS * 16);
-    }
-};
-
-// Across the reduction. One load of a wave holds kTogether whole rows (1024 bytes), so
-// they lie together in LDS; 64 bytes follow them, and 128 more follow each four loads
-// of two rows. Within a row the 32-byte parts are permuted by part ^ r % kTogether.
-// The eight rows that half a wave takes 32 bytes of in one transposing read, r0 to r0 + 3 and r0 + 8
-// to r0 + 11, then meet all 64 banks once, and the fragments of one operand need
-// only kTogether addresses in registers (with a permutation of all of a row's parts by
-// the row, as in Across, each fragment needed its own, and they did not fit).
-template <class T, int COLS, int THREADS>
-struct PipeAcross {
-    static constexpr bool kAcross = true;
-    static constexpr int kRows = kStepBytes / 2;
-    static constexpr int kPieces = COLS / 8;
-    static constexpr int kLoads = kRows * kPieces / THREADS;
-    static constexpr int kRowsEach = THREADS / kPieces;
-    static constexpr int kTogether = 64 / kPieces;
-    static_assert(kRows * kPieces % THREADS == 0 && (kTogether == 2 || kTogether == 4),
-                  "rows of 128 or 256 columns");
-
-    // Where load number l of a step (a wave's) lies.
-    static constexpr __device__ uint32_t place(uint32_t l)
-    {
-        return l * 1088 + (kTogether == 2 ? l / 4 * 128 : 0);
-    }
-    static constexpr uint32_t kBytes = kRows / kTogether * 1088 +
-                                       (kTogether == 2 ? kRows / kTogether / 4 * 128 : 0);
-    // The place of this wave's load i.
-    static __device__ __forceinline__ uint32_t place_of(int i, uint32_t wave)
-    {
-        return place(i * (THREADS / 64) + wave);
-    }
-    static __device__ __forceinline__ uint32_t row_of(int i)
-    {
-        return i * kRowsEach + threadIdx.x / kPieces;
-    }
-    // The byte in a row of this thread's pieces; past the operand's last column the first
-    // one is read (its results are not stored).
-    static __device__ __forceinline__ uint32_t byte_of(uint32_t wide)
-    {
-        const uint32_t mix = threadIdx.x / kPieces % kTogether;
-        const uint32_t byte = ((threadIdx.x % kPieces) ^ (mix << 1)) * 16;
-        return byte < wide * 2 ? byte : 0;
-    }
-    // Fragment i of the part that starts at column first (a multiple of 64), half kk.
-    static __device__ __forceinline__ typename Mma<T>::Frag frag(const char *lds, uint32_t first,
-                                                                 int i, int kk)
-    {
-        const uint32_t lane = threadIdx.x % 64, q = lane % 16, r = lane / 16 * 8 + q / 4;
-        const uint32_t part = (i % kTogether) ^ (r % kTogether);
-        const char *p = lds + place(r / kTogether) + r % kTogether * (COLS * 2) + first * 2 +
-                        part * 32 + q % 4 * 8;
-        p += place(kk * 32 / kTogether) + i / kTogether * kTogether * 32;
-        union {
-            s16x4 half[2];
-            typename Mma<T>::Frag whole;
-        } f;
-        f.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-        f.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + place(4 / kTogether)));
-        return f.whole;
     }
 };
 
