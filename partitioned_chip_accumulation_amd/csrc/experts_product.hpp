@@ -428,8 +428,12 @@ __global__ void __launch_bounds__(S::THREADS)
                 if constexpr (decltype(fast)::value) load_to_lds(base, at, lds);
                 else load_to_lds(in ? base + at : (const char *)&kZeros, lds);
             };
-            run_steps<T, S, true, A::kLoads + B::kLoads, P::STAGE>(
-                steps, whole, acc, [](auto, int) {}, load, fa, fb, [](uint32_t) {});
+            if constexpr (ACROSS && S::FM * S::FN == 32)
+                run_steps_sharing<T, S, true, A::kLoads + B::kLoads, P::STAGE>(
+                    steps, whole, acc, [](auto, int) {}, load, fa, fb, [](uint32_t) {});
+            else
+                run_steps<T, S, true, A::kLoads + B::kLoads, P::STAGE>(
+                    steps, whole, acc, [](auto, int) {}, load, fa, fb, [](uint32_t) {});
         } else {
             const char *from_a[A::kLoads], *from_b[ACROSS ? 1 : B::kLoads];
             u32x4 kept_a[2][A::kLoads], kept_b[2][B::kLoads];
