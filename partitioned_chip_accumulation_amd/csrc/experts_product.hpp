@@ -502,9 +502,13 @@ __global__ void __launch_bounds__(S::THREADS)
     typedef typename P::A A;
     typedef typename P::B B;
     const uint32_t tile = tile_of_block(blockIdx.x, g.span);
-    const uint32_t each = g.n_tiles * g.k_tiles, e = tile / each;
-    if (e >= g.experts) return;
-    const uint32_t in = tile - e * each;
+    const uint32_t each = g.n_tiles * g.k_tiles, rank = tile / each;
+    if (rank >= g.experts) return;
+    const uint32_t e = g.experts <= 64    ? expert_of_rank<1>(g.offsets, g.experts, g.rows, rank)
+                       : g.experts <= 256 ? expert_of_rank<4>(g.offsets, g.experts, g.rows, rank)
+                                          : expert_of_rank<EXPERTS_MAX_EXPERTS / 64>(
+                                                g.offsets, g.experts, g.rows, rank);
+    const uint32_t in = tile - rank * each;
     uint32_t n0 = in % g.n_tiles * S::BM, k0 = in / g.n_tiles * S::BN;
     // (last tiles that pass through registers start where they end with the last column)
     const bool full = !DIRECT && g.n >= S::BM && g.k >= S::BN;

@@ -338,4 +338,53 @@ __device__ __forceinline__ Tile find_tile(uint32_t tile, const int32_t *__restri
     return t;
 }
 
+// The expert with the rank-th most rows (0: the most; equals in the order of their numbers), so
+// that the workgroups with the most steps start first. The rank-th largest count is
+// found bit by bit: a bit stays set if more than `rank` experts have at least so many
+// rows, which a ballot of the wave counts.
+template <uint32_t kMost>  // 64 experts each
+__device__ __forceinline__ uint32_t expert_of_rank(const int32_t *__restrict__ offsets,
+                                                   uint32_t experts, uint32_t rows, uint32_t rank)
+{
+    const uint32_t lane = threadIdx.x % 64;
+    uint32_t count[kMost];  // of experts g * 64 + lane, plus 1; 0: no such expert
+#pragma unroll
+    for (uint32_t g = 0; g < kMost; ++g) {
+        count[g] = 0;
+        if (g * 64 + lane < experts) {
+            uint32_t e = (uint32_t)offsets[g * 64 + lane + 1], b = (uint32_t)offsets[g * 64 + lane];
+            e = e > rows ? rows : e;
+            count[g] = e > b ? e - b + 1 : 1;
+        }
+    }
+    auto at_least = [&](uint32_t c) {
+        uint32_t n = 0;
+#pragma unroll
+        for (uint32_t g = 0; g < kMost; ++g)
+            n += (uint32_t)__popcll(__ballot(count[g] >= c));
+        return n;
+    };
+    uint32_t value = 0;
+    for (uint32_t bit = 1u << (31 - __builtin_clz(rows + 1)); bit; bit >>= 1)
+        if (at_least(value | bit) > rank) value |= bit;
+    uint32_t left = rank - at_least(value + 1), found = 0;  // how many equals come before it
+    bool done = false;
+#pragma unroll
+    for (uint32_t g = 0; g < kMost; ++g) {
+        if (!done) {
+            const uint64_t equal = __ballot(count[g] == value);
+            const uint32_t n = (uint32_t)__popcll(equal);
+            const bool here = (equal >> lane & 1) &&
+                              (uint32_t)__popcll(equal & ((1ull << lane) - 1)) == left;
+            const uint64_t mine = __ballot(here);
+            if (mine) {
+                found = g * 64 + (uint32_t)__builtin_ctzll(mine);
+                done = true;
+            }
+            left -= n;
+        }
+    }
+    return found;
+}
+
 }  // namespace pca_experts
