@@ -8,6 +8,8 @@
 
 namespace pca_experts {
 
+constexpr uint32_t kCus = 256;  // of the device
+
 struct RowsArgs {
     char *out;
     const char *a;
@@ -333,6 +335,28 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
     block_barrier();
 }
 
+// The loads and barriers of either loop, for a wave whose rows a short tile does not have.
+template <int LOADS, uint32_t STAGE, class L>
+__device__ __forceinline__ void run_steps_idle(uint32_t steps, L load)
+{
+    typedef std::integral_constant<int, 0> Any;
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)pipe_lds;
+    for (uint32_t s = 0; s < 2 && s < steps; ++s)
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load(std::false_type(), Any(), s, base + s * STAGE, i);
+    if (steps > 1) wait_loads<LOADS>();
+    else wait_loads<0>();
+    block_barrier();
+    for (uint32_t k = 0; k < steps; ++k) {
+        wait_loads<0>();
+        block_barrier();
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            load(std::false_type(), Any(), k + 2, base + (k & 1) * STAGE, i);
+    }
+    block_barrier();
+}
+
 // How the operands of a product of rows, and of the weights' gradient, are staged.
 template <class T, class S, bool ACROSS>
 struct RowsParts {
@@ -359,15 +383,33 @@ __global__ void __launch_bounds__(S::THREADS)
     typedef typename P::A A;
     typedef typename P::B B;
     constexpr int kLog2 = __builtin_ctz(S::BM);
-    const Tile t = find_tile(tile_of_block(blockIdx.x, g.span), g.offsets, g.experts, g.rows, kLog2,
-                             g.n_tiles);
+    uint32_t tile = tile_of_block(blockIdx.x, g.span), part = 0, parts = 1;
+    if constexpr (S::BM == 256) {
+        // A workgroup fills a CU. Where the last round of tiles is at most half full, two
+        // workgroups take half the rows of each of them.
+        const uint32_t all =
+            count_row_tiles(g.offsets, g.experts, g.rows, kLog2) * g.n_tiles;
+        const uint32_t last = all % kCus, first = all - last;
+        if (last <= kCus / 2 && tile >= first) {
+            if (tile < first + 2 * last) {
+                parts = 2;
+                part = (tile - first) % 2;
+                tile = first + (tile - first) / 2;
+            } else {
+                tile -= last;
+            }
+        }
+    }
+    const Tile t = find_tile(tile, g.offsets, g.experts, g.rows, kLog2, g.n_tiles);
     if (t.group > g.experts) return;
-    const uint32_t m0 = t.begin + t.m * S::BM;
+    const uint32_t rows_each = S::BM / parts;
+    const uint32_t m0 = t.begin + t.m * S::BM + part * rows_each;
+    if (m0 >= t.end) return;
     // (a last tile across that passes through registers starts where it ends with the last column:
     // no piece then reaches past a row, and the columns that two tiles share get the same bits)
     const bool full = ACROSS && !DIRECT && g.cols >= S::BN;
     const uint32_t n0 = full && g.cols - t.n * S::BN < S::BN ? g.cols - S::BN : t.n * S::BN;
-    const uint32_t high = t.end - m0 < S::BM ? t.end - m0 : S::BM;
+    const uint32_t high = t.end - m0 < rows_each ? t.end - m0 : rows_each;
     const uint32_t wide = g.cols - n0 < S::BN ? g.cols - n0 : S::BN;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t wm = wave / S::WN * (S::BM / S::WM), wn = wave % S::WN * (S::BN / S::WN);
@@ -428,7 +470,9 @@ __global__ void __launch_bounds__(S::THREADS)
                 if constexpr (decltype(fast)::value) load_to_lds(base, at, lds);
                 else load_to_lds(in ? base + at : (const char *)&kZeros, lds);
             };
-            if constexpr (ACROSS && S::FM * S::FN == 32)
+            if (S::BM == 256 && wm >= high)
+                run_steps_idle<A::kLoads + B::kLoads, P::STAGE>(steps, load);
+            else if constexpr (ACROSS && S::FM * S::FN == 32)
                 run_steps_sharing<T, S, true, A::kLoads + B::kLoads, P::STAGE>(
                     steps, whole, acc, [](auto, int) {}, load, fa, fb, [](uint32_t) {});
             else
@@ -648,7 +692,7 @@ __global__ void __launch_bounds__(256) k_rows_thin(RowsArgs g)
     typedef typename Mma<T>::Frag Frag;
     __shared__ __align__(16) Acc sums[4][RM * FN][64];
     const Tile t = find_tile(tile_of_block(blockIdx.x, g.span), g.offsets, g.experts, g.rows,
-                             4 + __builtin_ctz(RM), g.n_tiles);
+                                    4 + __builtin_ctz(RM), g.n_tiles);
     if (t.group > g.experts) return;
     const uint32_t m0 = t.begin + t.m * 16 * RM, n0 = t.n * 16 * FN;
     const uint32_t high = t.end - m0 < 16 * RM ? t.end - m0 : 16 * RM;
@@ -805,7 +849,8 @@ hist_status_t launch_tiles(RowsArgs g, hipStream_t stream)
     g.n_tiles = (g.cols + S::BN - 1) / S::BN;
     const uint64_t tiles =
         most_row_tiles(g.rows, g.offsets ? g.experts + 1 : 1, S::BM) * g.n_tiles;
-    const uint64_t blocks = blocks_for(tiles, &g.span);
+    // (and a workgroup more for each tile of a last round that is at most half full)
+    const uint64_t blocks = blocks_for(tiles + (S::BM == 256 ? kCus / 2 : 0), &g.span);
     return launch(k_rows<T, O, S, ACROSS, DIRECT>, blocks, S::THREADS,
                   2 * RowsParts<T, S, ACROSS>::STAGE, stream, &g);
 }

@@ -338,6 +338,28 @@ __device__ __forceinline__ Tile find_tile(uint32_t tile, const int32_t *__restri
     return t;
 }
 
+// Row tiles of all experts (without the rows past the last kept one).
+__device__ __forceinline__ uint32_t count_row_tiles(const int32_t *__restrict__ offsets,
+                                                    uint32_t experts, uint32_t rows,
+                                                    uint32_t rows_log2)
+{
+    const uint32_t past_one = (1u << rows_log2) - 1;
+    if (!offsets) return (rows + past_one) >> rows_log2;
+    uint32_t all = 0;
+    for (uint32_t g0 = 0; g0 < experts; g0 += 64) {
+        const uint32_t g = g0 + threadIdx.x % 64;
+        uint32_t b = 0, e = 0;
+        if (g < experts) {
+            b = (uint32_t)offsets[g];
+            e = (uint32_t)offsets[g + 1];
+            e = e > rows ? rows : e;
+            b = b > e ? e : b;
+        }
+        all += __builtin_amdgcn_readlane(wave_inclusive_scan((e - b + past_one) >> rows_log2), 63);
+    }
+    return all;
+}
+
 // The expert with the rank-th most rows (0: the most; equals in the order of their numbers), so
 // that the workgroups with the most steps start first. The rank-th largest count is
 // found bit by bit: a bit stays set if more than `rank` experts have at least so many
