@@ -121,11 +121,11 @@ struct DwArgs {
 // ---------------------------------------------------------------------------
 // The pipelined products.
 
-// BM x BN results by WM x WN waves, PER_CU workgroups on a CU.
-template <int BM_, int BN_, int WM_, int WN_, int PER_CU_>
+// BM x BN results by WM x WN waves, PER_CU workgroups on a CU, STAGES steps in LDS.
+template <int BM_, int BN_, int WM_, int WN_, int PER_CU_, int STAGES_ = 2>
 struct Shape {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
-    static constexpr int THREADS = WM * WN * 64, PER_CU = PER_CU_;
+    static constexpr int THREADS = WM * WN * 64, PER_CU = PER_CU_, STAGES = STAGES_;
     static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // fragments of a wave
     static constexpr int WAVES_PER_SIMD = THREADS / 256 * PER_CU;
 };
@@ -152,7 +152,9 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
                                           FA frag_a, FB frag_b, H ahead)
 {
     constexpr int FM = S::FM, FN = S::FN;
-    constexpr uint32_t kAhead = DIRECT ? 2 : 4;  // steps from a step to what it fetches
+    constexpr int N = S::STAGES;
+    static_assert(DIRECT || N == 2, "pieces in registers alternate");
+    constexpr uint32_t kAhead = DIRECT ? N : 4;  // steps from a step to what it fetches
     struct Frags {
         typename Mma<T>::Frag a[FM], b[FN];
     };
@@ -194,13 +196,16 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
     Frags f[2];
     auto step = [&](auto fast, auto stage, uint32_t k) {
         constexpr uint32_t kHere = decltype(stage)::value * STAGE;
-        constexpr uint32_t kThere = STAGE - kHere;
+        constexpr uint32_t kThere = (decltype(stage)::value + 1) % N * STAGE;
         ahead(k + kAhead);
         half(std::false_type(), fast, stage, f[0], f[1], pipe_lds + kHere, 1, 0, 0);
         __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave has left the stage
-        if constexpr (DIRECT) wait_loads<0>();
+        if constexpr (DIRECT) {  // the next step's pieces are here
+            if (N == 2 || (!decltype(fast)::value && k + N - 1 >= steps)) wait_loads<0>();
+            else wait_loads<LOADS *(N - 2)>();
+        }
         block_barrier();
-        half(std::true_type(), fast, stage, f[1], f[0], pipe_lds + kThere, 0, k + 2, base + kHere);
+        half(std::true_type(), fast, stage, f[1], f[0], pipe_lds + kThere, 0, k + N, base + kHere);
     };
     typedef std::integral_constant<int, 0> Even;
     typedef std::integral_constant<int, 1> Odd;
@@ -215,12 +220,14 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
     }
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) load(std::false_type(), Even(), 0, base, i);
-    ahead(kAhead - 1);
-    if (steps > 1)
+    ahead(kAhead - N + 1);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load(std::false_type(), Odd(), 1, base + STAGE, i);
+    for (int s = 1; s < N; ++s)
+        if ((uint32_t)s < steps)
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) load(std::false_type(), Odd(), s, base + s * STAGE, i);
     if constexpr (DIRECT) {
-        if (steps > 1) wait_loads<LOADS>();
+        if (steps >= N) wait_loads<LOADS *(N - 1)>();
         else wait_loads<0>();
     } else {
         __builtin_amdgcn_s_waitcnt(0xc07f);
@@ -229,13 +236,21 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(pipe_lds, f[0], 0, r);
     uint32_t k = 0;
-    for (; k + kAhead + 1 < whole; k += 2) {
+    typedef std::integral_constant<int, 2 % N> Third;
+    typedef std::integral_constant<int, 3 % N> Fourth;
+    for (; k + kAhead + N - 1 < whole; k += N) {
         step(std::true_type(), Even(), k);
         step(std::true_type(), Odd(), k + 1);
+        if constexpr (N > 2) step(std::true_type(), Third(), k + 2);
+        if constexpr (N > 3) step(std::true_type(), Fourth(), k + 3);
     }
-    for (; k < steps; k += 2) {
+    for (; k < steps; k += N) {
         step(std::false_type(), Even(), k);
         if (k + 1 < steps) step(std::false_type(), Odd(), k + 1);
+        if constexpr (N > 2)
+            if (k + 2 < steps) step(std::false_type(), Third(), k + 2);
+        if constexpr (N > 3)
+            if (k + 3 < steps) step(std::false_type(), Fourth(), k + 3);
     }
     block_barrier();
 }
@@ -852,7 +867,7 @@ hist_status_t launch_tiles(RowsArgs g, hipStream_t stream)
     // (and a workgroup more for each tile of a last round that is at most half full)
     const uint64_t blocks = blocks_for(tiles + (S::BM == 256 ? kCus / 2 : 0), &g.span);
     return launch(k_rows<T, O, S, ACROSS, DIRECT>, blocks, S::THREADS,
-                  2 * RowsParts<T, S, ACROSS>::STAGE, stream, &g);
+                  S::STAGES * RowsParts<T, S, ACROSS>::STAGE, stream, &g);
 }
 
 // Whether `rows` rows from one base lie within 32-bit offsets.
@@ -873,14 +888,22 @@ hist_status_t launch_thin(RowsArgs g, hipStream_t stream)
 
 // The kernel for a product of rows. What decides is the rows of an expert on average (the
 // host knows no more) and whether the tiles are enough for 256 CUs. Measured with 32 experts of
-// 2560 x 2048 (bf16, us; thin 16 x 16, 32 x 128, 64 x 128, 128 x 128, 256 x 256):
-//   rows    2:  47.8   62.7   63.5   76.6   91.9      rows   64:  313   93.7   92.9   98.7    118
-//   rows    8:  72.3   73.0   73.4   93.0    112      rows  128:  593    125    111    100    121
-//   rows   16:   107   73.7   74.6   93.4    113      rows  256: 1145    199    154    145    128
-//   rows   32:   179   81.6   77.1   95.1    115      rows  512: 2262    348    258    221    218
-// and with a dense weight of 8192 x 4096 in 8 bits (thin 32 x 64, 64 x 64, 64 x 128, 128 x 128,
-// 256 x 256): rows 32: 18.6, 20.5, 23.5, 25.3, 41.5; rows 256: 52.0, 22.4, 25.0, 27.6, 44.3;
-// rows 1024: 186, 56.4, 53.8, 39.8, 48.7.
+// 2560 x 2048 whose weights come from memory (bf16, us; thin 16 x 16, then tiles with the
+// stages and workgroups that are used):
+//              thin   32x128  64x128 128x128 128x256 256x256
+//   rows   2   47.8     62.7    63.5    76.6            91.9
+//   rows   8   72.3     73.0    73.4    93.0             112
+//   rows  16    107     71.7    76.4    93.8    91.5     107
+//   rows  32    179     73.6    76.5    94.9    92.5     108
+//   rows  64    313     90.4    80.9     102    94.9     115
+//   rows 128    593      128     103     101    94.1     113
+//   rows 192    873      170     125     124     113     119
+//   rows 256   1145      210     154     144     136     125
+// The tiles below 256 x 256 are for groups whose time is the reading of the weights: more
+// stages, so that more of it is in flight (64 rows, 64 x 128: 97 us with two stages and three
+// workgroups a CU). Few tiles, a dense weight of 8192 x 4096 in 8 bits (64x64, 64x128, 128x128,
+// 256x256): rows 256: 20.0, 19.3, 27.6, 38.8; rows 512: 32.5, 28.7, 30.1, 40.0; rows 1024: 54.8,
+// 47.9, 40.0, 43.5; and thin 32 x 64 against 64 x 64: rows 32: 18.6, 20.5; rows 64: 18.9, 20.8.
 template <class T, class O, bool ACROSS>
 hist_status_t launch_rows(RowsArgs g, hipStream_t stream)
 {
@@ -899,19 +922,23 @@ hist_status_t launch_rows(RowsArgs g, hipStream_t stream)
     if (aligned16(g.a, g.lda) && aligned16(g.b, g.ldb) && g.b_stride % 16 == 0 &&
         g.bytes % 16 == 0 && (!ACROSS || g.cols % 8 == 0) &&
         near(g.order ? g.a_rows : 256, g.lda) && near(256, g.ldb)) {
-        if (each >= 192 && g.cols > 128 && tiles(256, 256) >= 256)
+        typedef Shape<64, 128, 2, 2, 2, 3> Low;
+        typedef Shape<32, 128, ACROSS ? 2 : 1, ACROSS ? 2 : 4, 2, 4> Lowest;
+        if (each >= 224 && g.cols > 128 && tiles(256, 256) >= 256)
             return launch_tiles<T, O, ACROSS, true, Shape<256, 256, 2, 4, 1>>(g, stream);
-        if (each >= 80 && tiles(128, 128) >= 256)
+        if (each >= 80 && g.cols > 128 && tiles(128, 256) >= 384)
+            return launch_tiles<T, O, ACROSS, true, Shape<128, 256, 2, 4, 1, 3>>(g, stream);
+        if (each >= 80 && tiles(128, 128) >= 384)
             return launch_tiles<T, O, ACROSS, true, Shape<128, 128, 2, 2, 2>>(g, stream);
-        if (each > 24 && tiles(64, 128) >= 512)
-            return launch_tiles<T, O, ACROSS, true, Shape<64, 128, 2, 2, 3>>(g, stream);
+        if (each > 40 && tiles(64, 128) >= 256)
+            return launch_tiles<T, O, ACROSS, true, Low>(g, stream);
         if constexpr (ACROSS) {
-            return each > 24 ? launch_tiles<T, O, ACROSS, true, Shape<64, 128, 2, 2, 3>>(g, stream)
-                             : launch_tiles<T, O, ACROSS, true, Shape<32, 128, 2, 2, 4>>(g, stream);
+            return each > 40 ? launch_tiles<T, O, ACROSS, true, Low>(g, stream)
+                             : launch_tiles<T, O, ACROSS, true, Lowest>(g, stream);
         } else {
-            if (each <= 24 && tiles(32, 128) >= 256)
-                return launch_tiles<T, O, ACROSS, true, Shape<32, 128, 1, 4, 4>>(g, stream);
-            return launch_tiles<T, O, ACROSS, true, Shape<64, 64, 2, 2, 4>>(g, stream);
+            if (each <= 40 && tiles(32, 128) >= 256)
+                return launch_tiles<T, O, ACROSS, true, Lowest>(g, stream);
+            return launch_tiles<T, O, ACROSS, true, Shape<64, 64, 2, 2, 3, 3>>(g, stream);
         }
     }
     return each > 24 ? launch_tiles<T, O, ACROSS, false, Shape<128, 128, 2, 2, 2>>(g, stream)
