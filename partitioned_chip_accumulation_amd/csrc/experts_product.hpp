@@ -375,6 +375,7 @@ __device__ __forceinline__ void run_steps_idle(uint32_t steps, L load)
 // How the operands of a product of rows, and of the weights' gradient, are staged.
 template <class T, class S, bool ACROSS>
 struct RowsParts {
+    static_assert(!ACROSS || S::BN / S::WN % 64 == 0, "a wave's fragments across start at 64 columns");
     typedef Along<T, S::BM, S::THREADS> A;
     typedef typename std::conditional<ACROSS, Across<T, S::BN, S::THREADS>,
                                       Along<T, S::BN, S::THREADS>>::type B;
@@ -382,6 +383,7 @@ struct RowsParts {
 };
 template <class T, class S>
 struct DwParts {
+    static_assert(S::BM / S::WM % 64 == 0 && S::BN / S::WN % 64 == 0, "as in RowsParts");
     typedef Across<T, S::BM, S::THREADS> A;
     typedef Across<T, S::BN, S::THREADS> B;
     static constexpr uint32_t STAGE = A::kBytes + B::kBytes;
@@ -506,23 +508,25 @@ __global__ void __launch_bounds__(S::THREADS)
                     from_b[i] = w + (int64_t)row_b(i) * g.ldb + byte_b;
             }
             const int left_b = (int)(g.cols - n0) * 2 - (int)byte_b;  // ACROSS: of a row
+            const uint32_t reduction = g.bytes / sizeof(T);
             auto fetch = [&](auto fast, auto parity, uint32_t step, int i) {
                 constexpr int kTo = decltype(parity)::value;
                 if (!decltype(fast)::value && step >= steps) return;
                 const uint32_t from = step * kStepBytes;
                 const bool whole_step = decltype(fast)::value;
                 if (i < A::kLoads) {
-                    kept_a[kTo][i] = load16<T>(from_a[i] + from,
-                                          whole_step ? 16 : (int)g.bytes - (int)(from + byte_a));
+                    kept_a[kTo][i] = load16<T>(
+                        from_a[i] + from, whole_step ? 16 : (int)g.bytes - (int)(from + byte_a));
                 } else {
                     i -= A::kLoads;
                     if constexpr (ACROSS) {
-                        const uint32_t r = step * B::kRows + i * B::kRowsEach;
-                        const bool in =
-                            whole_step || (step * B::kRows + B::row_of(i)) * 2 < g.bytes;
-                        kept_b[kTo][i] =
-                            load16<T>(from_b[0] + (int64_t)r * g.ldb,
-                                      whole_step || (full && in) ? 16 : in ? left_b : 0);
+                        // a row past the last one reads that one (and counts as 0 below)
+                        const int r = (int)(step * B::kRows) + i * B::kRowsEach;
+                        const int most = (int)reduction - 1 - (int)B::row_of(0);
+                        const char *p =
+                            from_b[0] + (int64_t)(whole_step || r <= most ? r : most) * g.ldb;
+                        if (whole_step || full) kept_b[kTo][i] = load_any<u32x4>(p);
+                        else kept_b[kTo][i] = load16<T>(p, left_b);
                     } else {
                         kept_b[kTo][i] =
                             load16<T>(from_b[i] + from,
@@ -532,10 +536,16 @@ __global__ void __launch_bounds__(S::THREADS)
             };
             auto load = [&](auto fast, auto parity, uint32_t step, uint32_t lds, int i) {
                 if (!decltype(fast)::value && step >= steps) return;
-                if (i < A::kLoads) put_in_lds(kept_a[decltype(parity)::value][i], lds + A::place_of(i, wave));
-                else
-                    put_in_lds(kept_b[decltype(parity)::value][i - A::kLoads],
-                               lds + A::kBytes + B::place_of(i - A::kLoads, wave));
+                if (i < A::kLoads) {
+                    put_in_lds(kept_a[decltype(parity)::value][i], lds + A::place_of(i, wave));
+                } else {
+                    const int j = i - A::kLoads;
+                    u32x4 v = kept_b[decltype(parity)::value][j];
+                    if constexpr (ACROSS)
+                        if (!decltype(fast)::value && step * B::kRows + B::row_of(j) >= reduction)
+                            v = u32x4{0, 0, 0, 0};
+                    put_in_lds(v, lds + A::kBytes + B::place_of(j, wave));
+                }
                 fetch(fast, parity, step + 2, i);
             };
             auto first = [&](auto parity, int i) {
@@ -653,30 +663,32 @@ __global__ void __launch_bounds__(S::THREADS)
             const int left_a = (int)(g.n - n0) * 2 - (int)byte_a;
             const int left_b = (int)(g.k - k0) * 2 - (int)byte_b;
             const char *from_a = dy + (int64_t)A::row_of(0) * g.lddy + byte_a, *from_b = x + byte_b;
+            // rows past the last one read that one (and count as 0 below)
+            const int most_a = (int)count - 1 - (int)A::row_of(0);
             auto fetch = [&](auto fast, auto parity, uint32_t step, int i) {
                 constexpr int kTo = decltype(parity)::value;
                 if (!decltype(fast)::value && step >= steps) return;
                 if (i < A::kLoads) {
-                    const bool in =
-                        decltype(fast)::value || step * A::kRows + A::row_of(i) < count;
-                    kept_a[kTo][i] = load16<T>(
-                        from_a + (int64_t)(step * A::kRows + i * A::kRowsEach) * g.lddy,
-                        decltype(fast)::value || (full && in) ? 16 : in ? left_a : 0);
+                    const int r = (int)(step * A::kRows) + i * A::kRowsEach;
+                    const char *p = from_a + (int64_t)(decltype(fast)::value || r <= most_a ? r : most_a) * g.lddy;
+                    if (decltype(fast)::value || full) kept_a[kTo][i] = load_any<u32x4>(p);
+                    else kept_a[kTo][i] = load16<T>(p, left_a);
                 } else {
                     i -= A::kLoads;
-                    const bool in =
-                        decltype(fast)::value || step * A::kRows + B::row_of(i) < count;
-                    kept_b[kTo][i] =
-                        load16<T>(from_b + (int64_t)row_x(i) * g.ldx,
-                                  decltype(fast)::value || (full && in) ? 16 : in ? left_b : 0);
+                    const char *p = from_b + (int64_t)row_x(i) * g.ldx;
+                    if (decltype(fast)::value || full) kept_b[kTo][i] = load_any<u32x4>(p);
+                    else kept_b[kTo][i] = load16<T>(p, left_b);
                 }
             };
             auto load = [&](auto fast, auto parity, uint32_t step, uint32_t lds, int i) {
                 if (!decltype(fast)::value && step >= steps) return;
-                if (i < A::kLoads) put_in_lds(kept_a[decltype(parity)::value][i], lds + A::place_of(i, wave));
-                else
-                    put_in_lds(kept_b[decltype(parity)::value][i - A::kLoads],
-                               lds + A::kBytes + B::place_of(i - A::kLoads, wave));
+                const int j = i < A::kLoads ? i : i - A::kLoads;
+                u32x4 v = i < A::kLoads ? kept_a[decltype(parity)::value][j % A::kLoads]
+                                        : kept_b[decltype(parity)::value][j % B::kLoads];
+                const uint32_t row = i < A::kLoads ? A::row_of(j) : B::row_of(j);
+                if (!decltype(fast)::value && step * A::kRows + row >= count) v = u32x4{0, 0, 0, 0};
+                put_in_lds(v, lds + (i < A::kLoads ? A::place_of(j, wave)
+                                                   : A::kBytes + B::place_of(j, wave)));
                 fetch(fast, parity, step + 2, i);
             };
             run_steps_sharing<T, S, false, A::kLoads + B::kLoads, P::STAGE>(
@@ -917,32 +929,49 @@ hist_status_t launch_rows(RowsArgs g, hipStream_t stream)
     // them does not depend on alignment: a product's bits are the same at every address.
     if constexpr (!ACROSS) {
         if (each <= 6) return launch_thin<T, O, 1, 1, 4>(g, stream);
-        if (each <= 64 && tiles(64, 64) < 256) return launch_thin<T, O, 2, 4, 2>(g, stream);
+        if (tiles(64, 64) < (each <= 64 ? 256 : 128)) return launch_thin<T, O, 2, 4, 2>(g, stream);
     }
     if (aligned16(g.a, g.lda) && aligned16(g.b, g.ldb) && g.b_stride % 16 == 0 &&
         g.bytes % 16 == 0 && (!ACROSS || g.cols % 8 == 0) &&
         near(g.order ? g.a_rows : 256, g.lda) && near(256, g.ldb)) {
         typedef Shape<64, 128, 2, 2, 2, 3> Low;
-        typedef Shape<32, 128, ACROSS ? 2 : 1, ACROSS ? 2 : 4, 2, 4> Lowest;
+        constexpr int kWm = ACROSS ? 2 : 1, kWn = ACROSS ? 2 : 4;
+        typedef Shape<32, 128, kWm, kWn, 2, 4> Lowest;
+        typedef Shape<32, 128, kWm, kWn, 4, 2> LowestShort;
+        // a short reduction has no use for stages, but for workgroups
+        const bool brief = g.bytes <= 8 * kStepBytes;
         if (each >= 224 && g.cols > 128 && tiles(256, 256) >= 256)
             return launch_tiles<T, O, ACROSS, true, Shape<256, 256, 2, 4, 1>>(g, stream);
         if (each >= 80 && g.cols > 128 && tiles(128, 256) >= 384)
             return launch_tiles<T, O, ACROSS, true, Shape<128, 256, 2, 4, 1, 3>>(g, stream);
-        if (each >= 80 && tiles(128, 128) >= 384)
+        // a workgroup on each CU at most: stages instead of a second one (8 bits, 8192 x 4096, 512
+        // rows: 25 us, with two stages 30)
+        if (each >= 80 && tiles(128, 128) >= 128 && tiles(128, 128) <= 256)
+            return launch_tiles<T, O, ACROSS, true, Shape<128, 128, 4, 2, 1, 4>>(g, stream);
+        if (each >= 80 && tiles(128, 128) >= 256)
             return launch_tiles<T, O, ACROSS, true, Shape<128, 128, 2, 2, 2>>(g, stream);
         if (each > 40 && tiles(64, 128) >= 256)
             return launch_tiles<T, O, ACROSS, true, Low>(g, stream);
         if constexpr (ACROSS) {
-            return each > 40 ? launch_tiles<T, O, ACROSS, true, Low>(g, stream)
-                             : launch_tiles<T, O, ACROSS, true, Lowest>(g, stream);
+            if (each > 40) return launch_tiles<T, O, ACROSS, true, Low>(g, stream);
+            return brief ? launch_tiles<T, O, ACROSS, true, LowestShort>(g, stream)
+                         : launch_tiles<T, O, ACROSS, true, Lowest>(g, stream);
         } else {
             if (each <= 40 && tiles(32, 128) >= 256)
-                return launch_tiles<T, O, ACROSS, true, Lowest>(g, stream);
+                return brief ? launch_tiles<T, O, ACROSS, true, LowestShort>(g, stream)
+                             : launch_tiles<T, O, ACROSS, true, Lowest>(g, stream);
             return launch_tiles<T, O, ACROSS, true, Shape<64, 64, 2, 2, 3, 3>>(g, stream);
         }
     }
-    return each > 24 ? launch_tiles<T, O, ACROSS, false, Shape<128, 128, 2, 2, 2>>(g, stream)
-                     : launch_tiles<T, O, ACROSS, false, Shape<32, 128, 2, 2, 3>>(g, stream);
+    // Through registers. A load that is not aligned takes the CU's path to its cache twice, so a tile
+    // that loads less for its products counts for more: 16 experts of 1024 rows on average, 2560 x
+    // 2053, 256 x 128 against 128 x 128: 286 and 302 us, the gradient of the rows 231 and 267.
+    if (each >= 192 && tiles(256, 128) >= 256)
+        return launch_tiles<T, O, ACROSS, false, Shape<256, 128, 4, 2, 1>>(g, stream);
+    if (each >= 80 && tiles(128, 128) >= 256)
+        return launch_tiles<T, O, ACROSS, false, Shape<128, 128, 2, 2, 2>>(g, stream);
+    if constexpr (ACROSS) return launch_tiles<T, O, ACROSS, false, Shape<32, 128, 2, 2, 3>>(g, stream);
+    else return launch_tiles<T, O, ACROSS, false, Shape<64, 64, 2, 2, 3>>(g, stream);
 }
 
 template <class T, bool DIRECT, class S>
@@ -957,14 +986,20 @@ hist_status_t launch_dw_tiles(DwArgs g, hipStream_t stream)
 template <class T>
 hist_status_t launch_dw(DwArgs g, hipStream_t stream)
 {
+    auto tiles = [&](uint32_t bm, uint32_t bn) {
+        return (uint64_t)g.experts * ((g.n + bm - 1) / bm) * ((g.k + bn - 1) / bn);
+    };
     if (aligned16(g.dy, g.lddy) && aligned16(g.x, g.ldx) && g.n % 8 == 0 && g.k % 8 == 0 &&
         near(64, g.lddy) && near(g.x_rows, g.ldx)) {
-        // enough large tiles for 256 CUs, or small ones
-        return (uint64_t)g.experts * ((g.n + 255) / 256) * ((g.k + 255) / 256) >= 256
+        // large tiles for most of 256 CUs, or small ones
+        return tiles(256, 256) >= 176
                    ? launch_dw_tiles<T, true, Shape<256, 256, 2, 4, 1>>(g, stream)
                    : launch_dw_tiles<T, true, Shape<128, 128, 2, 2, 2>>(g, stream);
     }
-    return launch_dw_tiles<T, false, Shape<128, 128, 2, 2, 2>>(g, stream);
+    // (the same sizes: 404 and 516 us)
+    return tiles(256, 128) >= 256
+               ? launch_dw_tiles<T, false, Shape<256, 128, 4, 2, 1>>(g, stream)
+               : launch_dw_tiles<T, false, Shape<128, 128, 2, 2, 2>>(g, stream);
 }
 
 // Checks that the products share. `unit`: bytes of an element of the result

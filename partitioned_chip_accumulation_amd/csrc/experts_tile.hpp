@@ -87,6 +87,7 @@ __device__ __forceinline__ u32x4 load16(const char *p, int left)
 {
     if (left >= 16) return load_any<u32x4>(p);
     u32x4 v = {0, 0, 0, 0};
+    if (left <= 0) return v;
     constexpr int kEach = 16 / sizeof(T);
     constexpr uint32_t kMask = sizeof(T) == 1 ? 0xffu : 0xffffu;
 #pragma unroll
