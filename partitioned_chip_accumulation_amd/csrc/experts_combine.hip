@@ -136,16 +136,13 @@ extern "C" hist_status_t experts_combine(void *out, int64_t ldo, const void *y, 
     while (lanes_log2 < 6 && (kCols << lanes_log2) < n) ++lanes_log2;
     const uint32_t parts = (n + (kCols << lanes_log2) - 1) / (kCols << lanes_log2);
     const uint64_t blocks = (((tokens * parts) << lanes_log2) + kThreads - 1) / kThreads;
-    if (blocks > INT32_MAX) return HIST_ERR_UNSUPPORTED;
     if (dtype == EXPERTS_BF16)
-        k_combine<__bf16><<<(uint32_t)blocks, kThreads, 0, stream>>>(
-            (__bf16 *)out, ldo, (const __bf16 *)y, ldy, (uint32_t)rows, place, weights,
-            (uint32_t)tokens, top_k, n, lanes_log2, parts);
-    else
-        k_combine<_Float16><<<(uint32_t)blocks, kThreads, 0, stream>>>(
-            (_Float16 *)out, ldo, (const _Float16 *)y, ldy, (uint32_t)rows, place, weights,
-            (uint32_t)tokens, top_k, n, lanes_log2, parts);
-    return launch_status();
+        return launch(k_combine<__bf16>, blocks, kThreads, 0, stream, (__bf16 *)out, ldo,
+                      (const __bf16 *)y, ldy, (uint32_t)rows, place, weights, (uint32_t)tokens,
+                      top_k, n, lanes_log2, parts);
+    return launch(k_combine<_Float16>, blocks, kThreads, 0, stream, (_Float16 *)out, ldo,
+                  (const _Float16 *)y, ldy, (uint32_t)rows, place, weights, (uint32_t)tokens, top_k,
+                  n, lanes_log2, parts);
 }
 
 extern "C" hist_status_t experts_combine_backward(void *dy, int64_t lddy, float *dweights,
@@ -168,12 +165,10 @@ extern "C" hist_status_t experts_combine_backward(void *dy, int64_t lddy, float 
     const uint32_t pairs = (uint32_t)(tokens * top_k);
     const uint32_t blocks = (pairs + kThreads / 64 - 1) / (kThreads / 64);
     if (dtype == EXPERTS_BF16)
-        k_combine_backward<__bf16><<<blocks, kThreads, 0, stream>>>(
-            (__bf16 *)dy, lddy, dweights, (const __bf16 *)dout, lddout, (const __bf16 *)y, ldy,
-            order, place, weights, pairs, top_k, n);
-    else
-        k_combine_backward<_Float16><<<blocks, kThreads, 0, stream>>>(
-            (_Float16 *)dy, lddy, dweights, (const _Float16 *)dout, lddout, (const _Float16 *)y,
-            ldy, order, place, weights, pairs, top_k, n);
-    return launch_status();
+        return launch(k_combine_backward<__bf16>, blocks, kThreads, 0, stream, (__bf16 *)dy, lddy,
+                      dweights, (const __bf16 *)dout, lddout, (const __bf16 *)y, ldy, order, place,
+                      weights, pairs, top_k, n);
+    return launch(k_combine_backward<_Float16>, blocks, kThreads, 0, stream, (_Float16 *)dy, lddy,
+                  dweights, (const _Float16 *)dout, lddout, (const _Float16 *)y, ldy, order, place,
+                  weights, pairs, top_k, n);
 }

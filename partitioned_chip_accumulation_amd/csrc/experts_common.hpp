@@ -99,8 +99,20 @@ inline hist_status_t device_status()
     return pca_host::device_supported(dev);
 }
 
-inline hist_status_t launch_status()
+// Queues a kernel. A launch is limited to 2^32 - 1 threads.
+template <class... P, class... A>
+hist_status_t launch(void (*kernel)(P...), uint64_t blocks, uint32_t threads, uint32_t lds,
+                     hipStream_t stream, A... args)
 {
+    if (blocks > UINT32_MAX / threads) return HIST_ERR_UNSUPPORTED;
+    if (blocks == 0) return HIST_OK;
+    if (lds > 65536 && hipFuncSetAttribute((const void *)kernel,
+                                           hipFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)lds) != hipSuccess) {
+        (void)hipGetLastError();
+        return HIST_ERR_HIP;
+    }
+    kernel<<<(uint32_t)blocks, threads, lds, stream>>>(((P)args)...);
     return hipGetLastError() == hipSuccess ? HIST_OK : HIST_ERR_HIP;
 }
 

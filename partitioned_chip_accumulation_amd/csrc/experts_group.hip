@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <class I>
-void launch_group(const void *ids, uint32_t pairs, uint32_t experts, int32_t *counts,
+hist_status_t launch_group(const void *ids, uint32_t pairs, uint32_t experts, int32_t *counts,
                   int32_t *offsets, int32_t *order, int32_t *place, uint32_t *rows,
                   hipStream_t stream)
 {
@@ -183,12 +183,13 @@ void launch_group(const void *ids, uint32_t pairs, uint32_t experts, int32_t *co
     const uint32_t quads = row_words(experts) / 4;
     const uint32_t groups = kThreads / quads < kGroups ? kThreads / quads : kGroups;
     const uint32_t lds = kWaves * experts * 4 + (one ? 0 : 2 * groups * quads * 16);
-    if (!one)
-        k_group_count<I><<<chunks, kThreads, 0, stream>>>((const I *)ids, pairs, experts, chunk,
-                                                       rows);
-    k_group_place<I><<<chunks, kThreads, lds, stream>>>(
-        (const I *)ids, pairs, experts, bits, chunk, chunks, one ? nullptr : rows, counts, offsets,
-        order, place);
+    if (!one) {
+        const hist_status_t st = launch(k_group_count<I>, chunks, kThreads, 0, stream,
+                                        (const I *)ids, pairs, experts, chunk, rows);
+        if (st != HIST_OK) return st;
+    }
+    return launch(k_group_place<I>, chunks, kThreads, lds, stream, (const I *)ids, pairs, experts,
+                  bits, chunk, chunks, one ? nullptr : rows, counts, offsets, order, place);
 }
 
 }  // namespace pca_experts
@@ -225,8 +226,7 @@ extern "C" hist_status_t experts_group(const void *ids, int32_t id_bits, uint64_
         return HIST_ERR_WORKSPACE;
     st = device_status();
     if (st != HIST_OK) return st;
-    (id_bits == 32 ? launch_group<int32_t> : launch_group<int64_t>)(
+    return (id_bits == 32 ? launch_group<int32_t> : launch_group<int64_t>)(
         ids, (uint32_t)(tokens * top_k), experts, counts, offsets, order, place,
         (uint32_t *)workspace, stream);
-    return launch_status();
 }

@@ -95,15 +95,13 @@ __global__ void __launch_bounds__(256)
 
 // A wave a row up to 1024 columns (two pieces a lane); the workgroup otherwise.
 template <class T>
-void launch_quantize(int8_t *xq, int64_t ldq, float *sx, const void *x, int64_t ldx, uint32_t rows,
-                     uint32_t k, hipStream_t stream)
+hist_status_t launch_quantize(int8_t *xq, int64_t ldq, float *sx, const void *x, int64_t ldx,
+                              uint32_t rows, uint32_t k, hipStream_t stream)
 {
-    if (k <= 1024)
-        k_quantize<T, 64, 2>
-            <<<(rows + 3) / 4, 256, 0, stream>>>(xq, ldq, sx, (const T *)x, ldx, rows, k);
-    else
-        k_quantize<T, 256, 4>
-            <<<rows, 256, 0, stream>>>(xq, ldq, sx, (const T *)x, ldx, rows, k);
+    return k <= 1024 ? launch(k_quantize<T, 64, 2>, (rows + 3) / 4, 256, 0, stream, xq, ldq, sx,
+                              (const T *)x, ldx, rows, k)
+                     : launch(k_quantize<T, 256, 4>, rows, 256, 0, stream, xq, ldq, sx,
+                              (const T *)x, ldx, rows, k);
 }
 
 }  // namespace pca_experts
@@ -121,9 +119,8 @@ extern "C" hist_status_t experts_quantize_rows(int8_t *xq, int64_t ldq, float *s
         return HIST_ERR_INVALID_ARG;
     st = device_status();
     if (st != HIST_OK || rows == 0) return st;
-    (dtype == EXPERTS_BF16 ? launch_quantize<__bf16> : launch_quantize<_Float16>)(
+    return (dtype == EXPERTS_BF16 ? launch_quantize<__bf16> : launch_quantize<_Float16>)(
         xq, ldq, sx, x, ldx, (uint32_t)rows, k, stream);
-    return launch_status();
 }
 
 extern "C" hist_status_t experts_int8_matmul(void *y, int64_t ldy, const int8_t *xq, int64_t ldq,

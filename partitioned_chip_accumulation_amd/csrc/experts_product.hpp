@@ -850,25 +850,10 @@ inline uint64_t blocks_for(uint64_t tiles, uint32_t *span)
     return (tiles + 8 * *span - 1) / (8 * *span) * (8 * *span);
 }
 
-template <class K>
-hist_status_t launch(K kernel, uint64_t blocks, uint32_t threads, uint32_t lds, hipStream_t stream,
-                     void *args)
+inline bool aligned16(const void *p, int64_t ld_bytes)
 {
-    if (blocks > INT32_MAX) return HIST_ERR_UNSUPPORTED;
-    if (blocks == 0) return HIST_OK;
-    if (lds > 65536 && hipFuncSetAttribute((const void *)kernel,
-                                           hipFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)lds) != hipSuccess) {
-        (void)hipGetLastError();
-        return HIST_ERR_HIP;
-    }
-    const hipError_t err = hipLaunchKernel((const void *)kernel, dim3((uint32_t)blocks),
-                                           dim3(threads), &args, lds, stream);
-    (void)hipGetLastError();
-    return err == hipSuccess ? HIST_OK : HIST_ERR_HIP;
+    return !misaligned(p, 16) && ld_bytes % 16 == 0;
 }
-
-inline bool aligned16(const void *p, int64_t ld_bytes) { return !misaligned(p, 16) && ld_bytes % 16 == 0; }
 
 template <class T, class O, bool ACROSS, bool DIRECT, class S>
 hist_status_t launch_tiles(RowsArgs g, hipStream_t stream)
@@ -879,7 +864,7 @@ hist_status_t launch_tiles(RowsArgs g, hipStream_t stream)
     // (and a workgroup more for each tile of a last round that is at most half full)
     const uint64_t blocks = blocks_for(tiles + (S::BM == 256 ? kCus / 2 : 0), &g.span);
     return launch(k_rows<T, O, S, ACROSS, DIRECT>, blocks, S::THREADS,
-                  S::STAGES * RowsParts<T, S, ACROSS>::STAGE, stream, &g);
+                  S::STAGES * RowsParts<T, S, ACROSS>::STAGE, stream, g);
 }
 
 // Whether `rows` rows from one base lie within 32-bit offsets.
@@ -895,7 +880,7 @@ hist_status_t launch_thin(RowsArgs g, hipStream_t stream)
     const uint64_t tiles =
         most_row_tiles(g.rows, g.offsets ? g.experts + 1 : 1, 16 * RM) * g.n_tiles;
     const uint64_t blocks = blocks_for(tiles, &g.span);
-    return launch(k_rows_thin<T, O, RM, FN, DEEP>, blocks, 256, 0, stream, &g);
+    return launch(k_rows_thin<T, O, RM, FN, DEEP>, blocks, 256, 0, stream, g);
 }
 
 // The kernel for a product of rows. What decides is the rows of an expert on average (the
@@ -980,7 +965,7 @@ hist_status_t launch_dw_tiles(DwArgs g, hipStream_t stream)
     g.n_tiles = (g.n + S::BM - 1) / S::BM;
     g.k_tiles = (g.k + S::BN - 1) / S::BN;
     const uint64_t blocks = blocks_for((uint64_t)g.n_tiles * g.k_tiles * g.experts, &g.span);
-    return launch(k_dw<T, S, DIRECT>, blocks, S::THREADS, 2 * DwParts<T, S>::STAGE, stream, &g);
+    return launch(k_dw<T, S, DIRECT>, blocks, S::THREADS, 2 * DwParts<T, S>::STAGE, stream, g);
 }
 
 template <class T>
