@@ -101,7 +101,7 @@ def _matrix(t: torch.Tensor, name: str, dtypes=_DTYPES, dim: int = 2) -> int:
     rows, width = t.shape[-2:]
     stride = t.stride()
     ld = stride[-2] if rows > 1 else width
-    if width == 0 or (width > 1 and stride[-1] != 1) or ld < width:
+    if width == 0 or (rows and width > 1 and stride[-1] != 1) or ld < width:
         raise ValueError(f"{name} must have columns, and rows of unit stride that do not overlap")
     return ld
 

@@ -47,7 +47,9 @@ def test_matmul(tokens, num, n, k, dtype):
 
 
 @pytest.mark.parametrize("tokens,num,n,k", SIZES)
-def test_int8(tokens, num, n, k):
+@pytest.mark.parametrize("aligned", [False, True])
+def test_int8(tokens, num, n, k, aligned):
+    k = (k + 15) // 16 * 16 if aligned else k  # 16-byte rows: straight to LDS
     g = pairs_of(tokens, num)
     xq, sx = experts.quantize_rows(normal(1, tokens, k, dtype=torch.bfloat16))
     wq, sw = int8_weight(2, num, n, k)
