@@ -136,8 +136,7 @@ extern __shared__ __align__(16) char pipe_lds[];
 // (fast: a whole one, of which there are `whole`; parity: the step's). Where it is not
 // DIRECT, it puts the piece, which is in registers by then, and fetches that of two steps later,
 // and first(parity, i) fetches those of steps 0 and 1.
-// frag_a and frag_b read the fragments of half a step, and ahead(step) may look up what
-// the loads of that step need.
+// frag_a and frag_b read the fragments of half a step.
 //
 // A step is two halves. At its top the first half's fragments are in registers (or
 // on their way), and the next step's pieces are. While the first half is multiplied
@@ -146,10 +145,10 @@ extern __shared__ __align__(16) char pipe_lds[];
 // first fragments are read. So there is one barrier a step, loads have a step to
 // arrive, and all reads and loads are issued between products.
 template <class T, class S, bool DIRECT, int LOADS, uint32_t STAGE, class F, class L, class FA,
-          class FB, class H>
+          class FB>
 __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
                                           typename Mma<T>::Acc (&acc)[S::FM][S::FN], F first, L load,
-                                          FA frag_a, FB frag_b, H ahead)
+                                          FA frag_a, FB frag_b)
 {
     constexpr int FM = S::FM, FN = S::FN;
     constexpr int N = S::STAGES;
@@ -197,7 +196,6 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
     auto step = [&](auto fast, auto stage, uint32_t k) {
         constexpr uint32_t kHere = decltype(stage)::value * STAGE;
         constexpr uint32_t kThere = (decltype(stage)::value + 1) % N * STAGE;
-        ahead(k + kAhead);
         half(std::false_type(), fast, stage, f[0], f[1], pipe_lds + kHere, 1, 0, 0);
         __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave has left the stage
         if constexpr (DIRECT) {  // the next step's pieces are here
@@ -209,18 +207,14 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
     };
     typedef std::integral_constant<int, 0> Even;
     typedef std::integral_constant<int, 1> Odd;
-    ahead(0);
     if constexpr (!DIRECT) {
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) first(Even(), i);
-        ahead(1);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) first(Odd(), i);
-        ahead(2);
     }
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) load(std::false_type(), Even(), 0, base, i);
-    ahead(kAhead - N + 1);
 #pragma unroll
     for (int s = 1; s < N; ++s)
         if ((uint32_t)s < steps)
@@ -258,12 +252,13 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
 // The same where two sets of fragments do not fit beside the sums, as with two
 // operands across the reduction: a fragment of A takes the registers of the one that has just
 // been used up (those of B alternate), so the reads of the second half end with the first
-// half's products, and the barrier comes a few rows of products into the second.
+// half's products, and the barrier comes a few rows of products into the second. look(step)
+// asks for what the loads of that step need (row numbers), turn(step) makes addresses of it.
 template <class T, class S, bool DIRECT, int LOADS, uint32_t STAGE, class F, class L, class FA,
-          class FB, class H>
+          class FB, class K, class U>
 __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole,
                                           typename Mma<T>::Acc (&acc)[S::FM][S::FN], F first, L load,
-                                          FA frag_a, FB frag_b, H ahead)
+                                          FA frag_a, FB frag_b, K look, U turn)
 {
     constexpr int FM = S::FM, FN = S::FN;
     constexpr uint32_t kAhead = DIRECT ? 2 : 4;  // steps from a step to what it fetches
@@ -281,7 +276,6 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
     auto step = [&](auto fast, auto stage, uint32_t k) {
         constexpr uint32_t kHere = decltype(stage)::value * STAGE;
         constexpr uint32_t kThere = STAGE - kHere;
-        ahead(k + kAhead);
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             products(i, b[0]);
@@ -295,6 +289,8 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
             if (i == kWait - 1) {
                 __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave has left the stage
                 if constexpr (DIRECT) wait_loads<0>();
+                turn(k + kAhead);  // what it looked up has arrived with the pieces
+                look(k + kAhead + 1);
                 block_barrier();
             } else if (i >= kWait) {
 #pragma unroll
@@ -311,18 +307,22 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
     };
     typedef std::integral_constant<int, 0> Even;
     typedef std::integral_constant<int, 1> Odd;
-    ahead(0);
+    look(0);
+    turn(0);
     if constexpr (!DIRECT) {
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) first(Even(), i);
-        ahead(1);
+        look(1);
+        turn(1);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) first(Odd(), i);
-        ahead(2);
+        look(2);
+        turn(2);
     }
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) load(std::false_type(), Even(), 0, base, i);
-    ahead(kAhead - 1);
+    look(kAhead - 1);
+    turn(kAhead - 1);
     if (steps > 1)
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) load(std::false_type(), Odd(), 1, base + STAGE, i);
@@ -332,6 +332,7 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
     } else {
         __builtin_amdgcn_s_waitcnt(0xc07f);
     }
+    look(kAhead);
     block_barrier();
 #pragma unroll
     for (int j = 0; j < FN; ++j) b[0][j] = frag_b(pipe_lds, j, 0);
@@ -491,10 +492,11 @@ __global__ void __launch_bounds__(S::THREADS)
                 run_steps_idle<A::kLoads + B::kLoads, P::STAGE>(steps, load);
             else if constexpr (ACROSS && S::FM * S::FN == 32)
                 run_steps_sharing<T, S, true, A::kLoads + B::kLoads, P::STAGE>(
-                    steps, whole, acc, [](auto, int) {}, load, fa, fb, [](uint32_t) {});
+                    steps, whole, acc, [](auto, int) {}, load, fa, fb, [](uint32_t) {},
+                    [](uint32_t) {});
             else
                 run_steps<T, S, true, A::kLoads + B::kLoads, P::STAGE>(
-                    steps, whole, acc, [](auto, int) {}, load, fa, fb, [](uint32_t) {});
+                    steps, whole, acc, [](auto, int) {}, load, fa, fb);
         } else {
             const char *from_a[A::kLoads], *from_b[ACROSS ? 1 : B::kLoads];
             u32x4 kept_a[2][A::kLoads], kept_b[2][B::kLoads];
@@ -553,10 +555,10 @@ __global__ void __launch_bounds__(S::THREADS)
             };
             if constexpr (S::FM >= 4)
                 run_steps_sharing<T, S, false, A::kLoads + B::kLoads, P::STAGE>(
-                    steps, whole, acc, first, load, fa, fb, [](uint32_t) {});
+                    steps, whole, acc, first, load, fa, fb, [](uint32_t) {}, [](uint32_t) {});
             else
                 run_steps<T, S, false, A::kLoads + B::kLoads, P::STAGE>(
-                    steps, whole, acc, first, load, fa, fb, [](uint32_t) {});
+                    steps, whole, acc, first, load, fa, fb);
         }
     }
     store_rows<T, O>(g, pipe_lds + wave * (S::FM * S::FN * 512), t, acc, real, m0 + wm, n0 + wn,
@@ -591,44 +593,38 @@ __global__ void __launch_bounds__(S::THREADS)
     uint32_t begin = __builtin_amdgcn_readfirstlane(g.offsets[e]);
     end = end > g.rows ? g.rows : end;
     begin = begin > end ? end : begin;
-    const uint32_t lane = threadIdx.x % 64;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t wm = wave / S::WN * (S::BM / S::WM), wn = wave % S::WN * (S::BN / S::WN);
     typename Mma<T>::Acc acc[S::FM][S::FN] = {};
     if (begin < end) {
-        // order through the scalar cache: its loads then do not wait with the vector ones
-        typedef const __attribute__((address_space(4))) int32_t *Scalar;
-        const Scalar order = (Scalar)(uintptr_t)g.order;
         const char *dy = g.dy + (int64_t)begin * g.lddy + n0 * 2;
         const char *x = g.x + k0 * 2 + (g.order ? 0 : (int64_t)begin * g.ldx);
-        constexpr int kPerWave = 64 / B::kPieces;  // rows of x of one wave's load
-        uint32_t from[B::kLoads * kPerWave];       // these rows, looked up half a step ahead
-        uint32_t of_row[kPerWave];                 // all ones in the lanes of each of them
-#pragma unroll
-        for (int q = 0; q < kPerWave; ++q)
-            of_row[q] = lane / B::kPieces == (uint32_t)q ? ~0u : 0u;
         const uint32_t byte_a = A::byte(), byte_b = B::byte();
         const uint32_t count = end - begin, steps = (count + A::kRows - 1) / A::kRows;
         const uint32_t whole = !DIRECT && !full ? 0 : count / A::kRows;
-        auto ahead = [&](uint32_t step) {
-#pragma unroll
-            for (int i = 0; i < B::kLoads; ++i)
-#pragma unroll
-                for (int q = 0; q < kPerWave; ++q) {
-                    uint32_t s = step * A::kRows + i * B::kRowsEach + wave * kPerWave + q;
-                    s = s < count ? s : count - 1;
-                    if (g.order) {
-                        s = g.divide((uint32_t)order[begin + s]);
-                        s = s < g.x_rows ? s : g.x_rows - 1;
-                    }
-                    from[i * kPerWave + q] = DIRECT ? s * (uint32_t)g.ldx : s;
-                }
+        uint32_t pair[B::kLoads], row_x[B::kLoads];  // of this lane's pieces of x
+        auto row_in = [&](uint32_t step, int i) {
+            const uint32_t r = step * A::kRows + B::row_of(i);
+            return r < count ? r : count - 1;
         };
-        auto row_x = [&](int i) {
-            uint32_t at = 0;
+        auto look = [&](uint32_t step) {
+            if (g.order)
 #pragma unroll
-            for (int q = 0; q < kPerWave; ++q) at |= from[i * kPerWave + q] & of_row[q];
-            return at;
+                for (int i = 0; i < B::kLoads; ++i)
+                    pair[i] = (uint32_t)g.order[begin + row_in(step, i)];
+        };
+        auto turn = [&](uint32_t step) {
+#pragma unroll
+            for (int i = 0; i < B::kLoads; ++i) {
+                uint32_t s;
+                if (g.order) {
+                    s = g.divide(pair[i]);
+                    s = s < g.x_rows ? s : g.x_rows - 1;
+                } else {
+                    s = row_in(step, i);
+                }
+                row_x[i] = DIRECT ? s * (uint32_t)g.ldx : s;
+            }
         };
         auto fa = [&](const char *lds, int i, int kk) { return A::frag(lds, wm, i, kk); };
         auto fb = [&](const char *lds, int j, int kk) {
@@ -648,7 +644,7 @@ __global__ void __launch_bounds__(S::THREADS)
                     at = at_a, row = A::row_of(i), lds += A::place_of(i, wave);
                 } else {
                     i -= A::kLoads;
-                    at = row_x(i) + at_b, row = B::row_of(i);
+                    at = row_x[i] + at_b, row = B::row_of(i);
                     lds += A::kBytes + B::place_of(i, wave);
                 }
                 if constexpr (decltype(fast)::value) load_to_lds(base, at, lds);
@@ -657,7 +653,7 @@ __global__ void __launch_bounds__(S::THREADS)
                                 lds);
             };
             run_steps_sharing<T, S, true, A::kLoads + B::kLoads, P::STAGE>(
-                steps, whole, acc, [](auto, int) {}, load, fa, fb, ahead);
+                steps, whole, acc, [](auto, int) {}, load, fa, fb, look, turn);
         } else {
             u32x4 kept_a[2][A::kLoads], kept_b[2][B::kLoads];
             const int left_a = (int)(g.n - n0) * 2 - (int)byte_a;
@@ -675,7 +671,7 @@ __global__ void __launch_bounds__(S::THREADS)
                     else kept_a[kTo][i] = load16<T>(p, left_a);
                 } else {
                     i -= A::kLoads;
-                    const char *p = from_b + (int64_t)row_x(i) * g.ldx;
+                    const char *p = from_b + (int64_t)row_x[i] * g.ldx;
                     if (decltype(fast)::value || full) kept_b[kTo][i] = load_any<u32x4>(p);
                     else kept_b[kTo][i] = load16<T>(p, left_b);
                 }
@@ -696,7 +692,7 @@ __global__ void __launch_bounds__(S::THREADS)
                 [&](auto parity, int i) {
                     fetch(std::false_type(), parity, decltype(parity)::value, i);
                 },
-                load, fa, fb, ahead);
+                load, fa, fb, look, turn);
         }
     }
     store_part<T, S::FM, S::FN>(pipe_lds + wave * (S::FM * S::FN * 512),
