@@ -929,7 +929,14 @@ hist_status_t launch_rows(RowsArgs g, hipStream_t stream)
         // rows: 25 us, with two stages 30)
         if (each >= 80 && tiles(128, 128) >= 128 && tiles(128, 128) <= 256)
             return launch_tiles<T, O, ACROSS, true, Shape<128, 128, 4, 2, 1, 4>>(g, stream);
-        if (each >= 80 && tiles(128, 128) >= 256)
+        // A few tiles more than the 512 that run at one time take as long as a round of them (the
+        // count is an estimate, hence 528): large tiles, if one round of those fills most CUs. 16
+        // experts, 175 rows each, 2688 x 4096: 111 us, with small tiles 147; 32 experts, 138 rows
+        // each, 1344 x 2048: 60 and 75 us, but with 128 rows each, in one round, 59 and 53.
+        const uint64_t small = tiles(128, 128), large = tiles(256, 256);
+        if (each >= 80 && small > 528 && small % 512 < 128 && large >= 160 && large <= 256)
+            return launch_tiles<T, O, ACROSS, true, Shape<256, 256, 2, 4, 1>>(g, stream);
+        if (each >= 80 && small >= 256)
             return launch_tiles<T, O, ACROSS, true, Shape<128, 128, 2, 2, 2>>(g, stream);
         if (each > 40 && tiles(64, 128) >= 256)
             return launch_tiles<T, O, ACROSS, true, Low>(g, stream);
