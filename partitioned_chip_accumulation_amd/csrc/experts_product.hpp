@@ -515,10 +515,12 @@ __global__ void __launch_bounds__(S::THREADS)
                 constexpr int kTo = decltype(parity)::value;
                 if (!decltype(fast)::value && step >= steps) return;
                 const uint32_t from = step * kStepBytes;
-                const bool whole_step = decltype(fast)::value;
+                const bool whole_step = decltype(fast)::value || step < whole;
                 if (i < A::kLoads) {
-                    kept_a[kTo][i] = load16<T>(
-                        from_a[i] + from, whole_step ? 16 : (int)g.bytes - (int)(from + byte_a));
+                    if (whole_step) kept_a[kTo][i] = load_any<u32x4>(from_a[i] + from);
+                    else
+                        kept_a[kTo][i] = load16<T>(
+                            from_a[i] + from, (int)g.bytes - (int)(from + byte_a), g.bytes >= 16);
                 } else {
                     i -= A::kLoads;
                     if constexpr (ACROSS) {
@@ -528,11 +530,12 @@ __global__ void __launch_bounds__(S::THREADS)
                         const char *p =
                             from_b[0] + (int64_t)(whole_step || r <= most ? r : most) * g.ldb;
                         if (whole_step || full) kept_b[kTo][i] = load_any<u32x4>(p);
-                        else kept_b[kTo][i] = load16<T>(p, left_b);
+                        else kept_b[kTo][i] = load16<T>(p, left_b, g.cols >= 8);
+                    } else if (whole_step) {
+                        kept_b[kTo][i] = load_any<u32x4>(from_b[i] + from);
                     } else {
-                        kept_b[kTo][i] =
-                            load16<T>(from_b[i] + from,
-                                      whole_step ? 16 : (int)g.bytes - (int)(from + byte_b));
+                        kept_b[kTo][i] = load16<T>(
+                            from_b[i] + from, (int)g.bytes - (int)(from + byte_b), g.bytes >= 16);
                     }
                 }
             };
@@ -668,12 +671,12 @@ __global__ void __launch_bounds__(S::THREADS)
                     const int r = (int)(step * A::kRows) + i * A::kRowsEach;
                     const char *p = from_a + (int64_t)(decltype(fast)::value || r <= most_a ? r : most_a) * g.lddy;
                     if (decltype(fast)::value || full) kept_a[kTo][i] = load_any<u32x4>(p);
-                    else kept_a[kTo][i] = load16<T>(p, left_a);
+                    else kept_a[kTo][i] = load16<T>(p, left_a, g.n >= 8);
                 } else {
                     i -= A::kLoads;
                     const char *p = from_b + (int64_t)row_x[i] * g.ldx;
                     if (decltype(fast)::value || full) kept_b[kTo][i] = load_any<u32x4>(p);
-                    else kept_b[kTo][i] = load16<T>(p, left_b);
+                    else kept_b[kTo][i] = load16<T>(p, left_b, g.k >= 8);
                 }
             };
             auto load = [&](auto fast, auto parity, uint32_t step, uint32_t lds, int i) {
@@ -745,11 +748,15 @@ __global__ void __launch_bounds__(256) k_rows_thin(RowsArgs g)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint32_t f = from + h * 64;
-                const int left = decltype(whole)::value ? 16 : (int)g.bytes - (int)(f + at);
+                const int left = (int)g.bytes - (int)(f + at);
+                auto one = [&](const char *q) {
+                    if constexpr (decltype(whole)::value) return load_any<u32x4>(q);
+                    else return load16<T>(q, left, g.bytes >= 16);
+                };
 #pragma unroll
-                for (int j = 0; j < FN; ++j) p.b[j][h] = load16<T>(b[j] + f, left);
+                for (int j = 0; j < FN; ++j) p.b[j][h] = one(b[j] + f);
 #pragma unroll
-                for (int i = 0; i < RM; ++i) p.a[i][h] = load16<T>(a[i] + f, left);
+                for (int i = 0; i < RM; ++i) p.a[i][h] = one(a[i] + f);
             }
         };
         auto multiply = [&](const Piece &p) {
@@ -919,11 +926,12 @@ hist_status_t launch_rows(RowsArgs g, hipStream_t stream)
         constexpr int kWm = ACROSS ? 2 : 1, kWn = ACROSS ? 2 : 4;
         typedef Shape<32, 128, kWm, kWn, 2, 4> Lowest;
         typedef Shape<32, 128, kWm, kWn, 4, 2> LowestShort;
-        // a short reduction has no use for stages, but for workgroups
+        // a short reduction has no use for stages, but for workgroups beside it (16384 rows, 8 experts,
+        // 256 -> 2048: 31 us in 128 x 128, 37 in 256 x 256; 1024 -> 2048: 78 and 80)
         const bool brief = g.bytes <= 8 * kStepBytes;
-        if (each >= 224 && g.cols > 128 && tiles(256, 256) >= 256)
+        if (!brief && each >= 224 && g.cols > 128 && tiles(256, 256) >= 256)
             return launch_tiles<T, O, ACROSS, true, Shape<256, 256, 2, 4, 1>>(g, stream);
-        if (each >= 80 && g.cols > 128 && tiles(128, 256) >= 384)
+        if (!brief && each >= 80 && g.cols > 128 && tiles(128, 256) >= 384)
             return launch_tiles<T, O, ACROSS, true, Shape<128, 256, 2, 4, 1, 3>>(g, stream);
         // a workgroup on each CU at most: stages instead of a second one (8 bits, 8192 x 4096, 512
         // rows: 25 us, with two stages 30)
@@ -934,7 +942,7 @@ hist_status_t launch_rows(RowsArgs g, hipStream_t stream)
         // experts, 175 rows each, 2688 x 4096: 111 us, with small tiles 147; 32 experts, 138 rows
         // each, 1344 x 2048: 60 and 75 us, but with 128 rows each, in one round, 59 and 53.
         const uint64_t small = tiles(128, 128), large = tiles(256, 256);
-        if (each >= 80 && small > 528 && small % 512 < 128 && large >= 160 && large <= 256)
+        if (each >= 80 && small > 528 && small % 512 < 128 && large >= 160 && large <= 256 && !brief)
             return launch_tiles<T, O, ACROSS, true, Shape<256, 256, 2, 4, 1>>(g, stream);
         if (each >= 80 && small >= 256)
             return launch_tiles<T, O, ACROSS, true, Shape<128, 128, 2, 2, 2>>(g, stream);
@@ -979,8 +987,10 @@ hist_status_t launch_dw(DwArgs g, hipStream_t stream)
     };
     if (aligned16(g.dy, g.lddy) && aligned16(g.x, g.ldx) && g.n % 8 == 0 && g.k % 8 == 0 &&
         near(64, g.lddy) && near(g.x_rows, g.ldx)) {
-        // large tiles for most of 256 CUs, or small ones
-        return tiles(256, 256) >= 176
+        // Large tiles, if they are enough for most of 256 CUs and not much larger than the weight (32
+        // experts, 1024 rows each, 528 x 288: 53 us, in small ones 34; 1024 x 1024: 98 and 111).
+        const uint64_t area = tiles(256, 256) * 256 * 256;
+        return tiles(256, 256) >= 176 && area * 4 <= tiles(128, 128) * 128 * 128 * 5
                    ? launch_dw_tiles<T, true, Shape<256, 256, 2, 4, 1>>(g, stream)
                    : launch_dw_tiles<T, true, Shape<128, 128, 2, 2, 2>>(g, stream);
     }
