@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(256)
                 for (int i = 0; i < 8; ++i) {
                     const float f = (float)v[i];
                     float m = rintf(f / scale);
-                    // what m leaves of f is exact in 32 bits, so comparing it with half the scale decides
+                    // what m leaves of f is exact in 32 bits: comparing it with half the scale
+                    // decides
                     const float rest = __builtin_fmaf(-m, scale, f);
                     const float twice = 2.f * fabsf(rest);
                     const bool odd = ((int)m & 1) != 0;

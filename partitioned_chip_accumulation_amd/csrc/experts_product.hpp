@@ -168,8 +168,8 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
         if (r < FN) f.b[r] = frag_b(lds, r, kk);
         else f.a[r - FN] = frag_a(lds, r - FN, kk);
     };
-    auto half = [&](auto with_loads, auto fast, auto stage, const Frags &now, Frags &then, const char *lds,
-                    int kk, uint32_t step, uint32_t to) {
+    auto half = [&](auto with_loads, auto fast, auto stage, const Frags &now, Frags &then,
+                    const char *lds, int kk, uint32_t step, uint32_t to) {
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -678,7 +678,8 @@ __global__ void __launch_bounds__(S::THREADS)
                 if (!decltype(fast)::value && step >= steps) return;
                 if (i < A::kLoads) {
                     const int r = (int)(step * A::kRows) + i * A::kRowsEach;
-                    const char *p = from_a + (int64_t)(decltype(fast)::value || r <= most_a ? r : most_a) * g.lddy;
+                    const int row = decltype(fast)::value || r <= most_a ? r : most_a;
+                    const char *p = from_a + (int64_t)row * g.lddy;
                     if (decltype(fast)::value || full) kept_a[kTo][i] = load_any<u32x4>(p);
                     else kept_a[kTo][i] = load16<T>(p, left_a, g.n >= 8);
                 } else {
@@ -1021,8 +1022,8 @@ inline hist_status_t check_sizes(uint64_t rows, uint64_t x_rows, uint32_t top_k,
                                  uint32_t n, uint32_t k)
 {
     if (experts == 0 || n == 0 || k == 0 || top_k == 0) return HIST_ERR_INVALID_ARG;
-    if (experts > EXPERTS_MAX_EXPERTS || top_k > EXPERTS_MAX_TOP_K || n > EXPERTS_MAX_WIDTH || k > EXPERTS_MAX_WIDTH ||
-        rows > EXPERTS_MAX_ROWS || x_rows > EXPERTS_MAX_ROWS)
+    if (experts > EXPERTS_MAX_EXPERTS || top_k > EXPERTS_MAX_TOP_K || n > EXPERTS_MAX_WIDTH ||
+        k > EXPERTS_MAX_WIDTH || rows > EXPERTS_MAX_ROWS || x_rows > EXPERTS_MAX_ROWS)
         return HIST_ERR_UNSUPPORTED;
     return HIST_OK;
 }

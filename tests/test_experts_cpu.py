@@ -90,6 +90,22 @@ def test_argument_errors_before_any_device_call():
     assert lib.experts_combine(P, 64, P, 64, 20, P, P, 2**60, 2, 64, 0, None) == UNSUPPORTED
 
 
+def test_header_is_c(tmp_path):
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("gcc not available")
+    source = tmp_path / "c.c"
+    source.write_text("#include \"experts.h\"\nint main(void) { return experts_quantize_rows(0, 0, 0, "
+                      "0, 0, 0, 0, 0, 0) == HIST_ERR_INVALID_ARG ? EXPERTS_BF16 : 1; }\n")
+    libdir = os.path.dirname(hist.LIBRARY)
+    exe = str(tmp_path / "c")
+    subprocess.run([gcc, "-std=c99", "-Wall", "-Werror", "-D__HIP_PLATFORM_AMD__", "-I",
+                    build.INCLUDE, "-I", "/opt/rocm/include", str(source), "-L", libdir,
+                    "-lpca_hist", f"-Wl,-rpath,{libdir}", "-o", exe], check=True,
+                   capture_output=True)
+    assert subprocess.run([exe], timeout=60).returncode == 0
+
+
 def test_no_device_is_unsupported_not_a_crash():
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")
