@@ -495,10 +495,6 @@ __global__ void __launch_bounds__(S::THREADS)
             };
             if (S::BM == 256 && wm >= high)
                 run_steps_idle<A::kLoads + B::kLoads, P::STAGE>(steps, load);
-            else if constexpr (ACROSS && S::FM * S::FN == 32)
-                run_steps_sharing<T, S, true, A::kLoads + B::kLoads, P::STAGE>(
-                    steps, whole, acc, [](auto, int) {}, load, fa, fb, [](uint32_t) {},
-                    [](uint32_t) {});
             else
                 run_steps<T, S, true, A::kLoads + B::kLoads, P::STAGE>(
                     steps, whole, acc, [](auto, int) {}, load, fa, fb);
