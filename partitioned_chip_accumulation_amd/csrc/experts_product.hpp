@@ -266,6 +266,14 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
     constexpr int kReads = (FM + FN + FM - kWait - 1) / (FM - kWait);
     constexpr int kLoads = (LOADS + FM - kWait - 1) / (FM - kWait);
     static_assert(kWait > 0 && FN <= FM, "rows to spread the reads over");
+    constexpr bool kUsedUp = [] {  // a fragment of A is only read after its row's products
+        for (int i = kWait; i < FM; ++i) {
+            const int past = (i - kWait + 1) * kReads;
+            if ((past < FM + FN ? past : FM + FN) - 1 - FN > i) return false;
+        }
+        return true;
+    }();
+    static_assert(kUsedUp, "reads that are not ahead of the products");
     typename Mma<T>::Frag a[FM], b[2][FN];
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)pipe_lds;
     auto products = [&](int i, const typename Mma<T>::Frag (&with)[FN]) {
