@@ -5,7 +5,8 @@ A router gives each token ``top_k`` expert ids. ``group_rows`` counts the
 sorted rows by their experts' weights (``matmul_dx`` and ``matmul_dw`` are its
 gradients, ``int8_matmul`` its 8-bit form); ``combine`` adds the results back
 to their tokens (``combine_backward``: its gradients). ``linear`` and
-``merge`` are the product and the sum for torch's autograd.
+``merge`` are the product and the sum for torch's autograd, with gradients of the
+first order (a gradient of a gradient raises RuntimeError).
 
 ::
 
@@ -313,6 +314,26 @@ def _plain_rows(t: torch.Tensor) -> torch.Tensor:
     return t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
 
 
+class _FirstOrder(torch.autograd.Function):
+    """A gradient that a kernel computed, tied to what it depends on: a second backward pass
+    raises where it would have taken the gradient for a constant."""
+    @staticmethod
+    def forward(ctx, grad, *_):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("experts.linear and experts.merge have gradients of the first order "
+                           "only")
+
+
+def _first_order(grad: torch.Tensor, *depends_on: torch.Tensor) -> torch.Tensor:
+    # (torch's once_differentiable looks at the incoming gradients alone, not at what was saved)
+    if torch.is_grad_enabled() and any(t.requires_grad for t in depends_on):
+        return _FirstOrder.apply(grad, *depends_on)
+    return grad
+
+
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, gather, *g):
@@ -330,8 +351,9 @@ class _Linear(torch.autograd.Function):
             dx = matmul_dx(dy, w, g)
             if ctx.gather:
                 dx = combine(dx, g)
+            dx = _first_order(dx, dy, w)
         if ctx.needs_input_grad[1]:
-            dw = matmul_dw(dy, x, g, ctx.gather)
+            dw = _first_order(matmul_dw(dy, x, g, ctx.gather), dy, x)
         return (dx, dw, None) + (None,) * len(g)
 
 
@@ -345,6 +367,7 @@ class _Merge(torch.autograd.Function):
     def backward(ctx, dout):
         y, weights, *g = ctx.saved_tensors
         dy, dweights = combine_backward(_plain_rows(dout), y, Groups(*g), weights)
+        dy, dweights = _first_order(dy, dout, weights), _first_order(dweights, dout, y)
         return (dy, dweights) + (None,) * len(g)
 
 
