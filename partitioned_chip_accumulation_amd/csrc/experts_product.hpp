@@ -69,6 +69,24 @@ __device__ __forceinline__ void store_part(char *lds, O *out, int64_t ld_bytes, 
     }
 }
 
+// A scale of the 8-bit product, as a fraction of [0.5, 1) and a power of two (zero, infinity and NaN
+// are their own fractions). A whole-number sum times a row's scale can pass the range of 32 bits where
+// the column's scale would bring it back (a row with 3e38 in it), so the fractions are multiplied
+// first, which rounds as the scales would, and the powers come last.
+struct Scale {
+    float part;
+    int power;
+    static __device__ __forceinline__ Scale of(float s)
+    {
+        return {__builtin_amdgcn_frexp_mantf(s), __builtin_amdgcn_frexp_expf(s)};
+    }
+};
+
+__device__ __forceinline__ float scaled(int32_t sum, const Scale &a, const Scale &b)
+{
+    return __builtin_amdgcn_ldexpf((float)sum * a.part * b.part, a.power + b.power);
+}
+
 // The part of a product of rows: `real` is false for rows past the last kept one.
 template <class T, class O, int FM, int FN, class Acc>
 __device__ __forceinline__ void store_rows(const RowsArgs &g, char *lds, const Tile &t,
@@ -78,8 +96,7 @@ __device__ __forceinline__ void store_rows(const RowsArgs &g, char *lds, const T
     O *out = (O *)(g.out + (int64_t)row * g.ldo) + col;
     if constexpr (sizeof(T) == 1) {
         const uint32_t lane = threadIdx.x % 64;
-        f32x4 sb[FN] = {};
-        float sa[FM] = {};
+        Scale sb[FN][4] = {}, sa[FM] = {};
         if (real) {
             const float *from = g.sb + (uint64_t)t.group * g.cols + col;
 #pragma unroll
@@ -87,18 +104,18 @@ __device__ __forceinline__ void store_rows(const RowsArgs &g, char *lds, const T
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int c = j * 16 + lane / 16 * 4 + q;
-                    sb[j][q] = c < wide ? from[c] : 0.f;
+                    sb[j][q] = Scale::of(c < wide ? from[c] : 0.f);
                 }
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 const int r = i * 16 + lane % 16;
-                sa[i] = r < high ? g.sa[source_row(g, row + r)] : 0.f;
+                sa[i] = Scale::of(r < high ? g.sa[source_row(g, row + r)] : 0.f);
             }
         }
         store_part<O, FM, FN>(lds, out, g.ldo, high, wide, [&](int i, int j) {
             f32x4 v;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = (float)acc[i][j][q] * sa[i] * sb[j][q];
+            for (int q = 0; q < 4; ++q) v[q] = scaled(acc[i][j][q], sa[i], sb[j][q]);
             return v;
         });
     } else {
@@ -825,11 +842,12 @@ __global__ void __launch_bounds__(256) k_rows_thin(RowsArgs g)
         typedef O O4 __attribute__((ext_vector_type(4)));
         float v[4];
         if constexpr (sizeof(T) == 1) {
-            const float sa = real ? g.sa[source_row(g, m0 + r)] : 0.f;
+            const Scale sa = Scale::of(real ? g.sa[source_row(g, m0 + r)] : 0.f);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 v[q] = real && q < left
-                           ? (float)s[q] * sa * g.sb[(uint64_t)t.group * g.cols + n0 + c + q]
+                           ? scaled(s[q], sa,
+                                    Scale::of(g.sb[(uint64_t)t.group * g.cols + n0 + c + q]))
                            : 0.f;
         } else {
 #pragma unroll
