@@ -82,9 +82,19 @@ struct Scale {
     }
 };
 
+// The widest reduction, EXPERTS_MAX_WIDTH products of -128 and -128, sums to 2^31 and wraps to
+// -2^31, which is no other sum: the least real one is 2^17 * -128 * 127.
 __device__ __forceinline__ float scaled(int32_t sum, const Scale &a, const Scale &b)
 {
-    return __builtin_amdgcn_ldexpf((float)sum * a.part * b.part, a.power + b.power);
+    const float f = (float)sum, s = sum == INT32_MIN ? -f : f;
+    return __builtin_amdgcn_ldexpf(s * a.part * b.part, a.power + b.power);
+}
+
+__device__ __forceinline__ f32x4 plus(f32x4 a, f32x4 b) { return a + b; }
+__device__ __forceinline__ s32x4 plus(s32x4 a, s32x4 b)  // wraps, see scaled()
+{
+    return __builtin_bit_cast(s32x4,
+                              __builtin_bit_cast(u32x4, a) + __builtin_bit_cast(u32x4, b));
 }
 
 // The part of a product of rows: `real` is false for rows past the last kept one.
@@ -835,7 +845,7 @@ __global__ void __launch_bounds__(256) k_rows_thin(RowsArgs g)
     for (uint32_t f = wave; f < RM * FN; f += 4) {
         Acc s = sums[0][f][lane];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) s += sums[w][f][lane];
+        for (int w = 1; w < 4; ++w) s = plus(s, sums[w][f][lane]);
         const uint32_t r = f / FN * 16 + lane % 16, c = f % FN * 16 + lane / 16 * 4;
         if (r >= high || c >= wide) continue;
         const int left = (int)(wide - c);

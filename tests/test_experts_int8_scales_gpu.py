@@ -64,3 +64,19 @@ def test_scales_that_are_zero_subnormal_or_not_finite(rows, n):
         assert torch.equal(y.isnan(), want.isnan())
         ok = ~want.isnan()
         assert torch.equal(y[ok], want[ok])
+
+
+@pytest.mark.parametrize("rows,n", [(1, 20), (40, 300), (300, 4100)])
+def test_the_largest_sums_of_the_widest_reduction(rows, n):
+    """k = 131072: -128 throughout sums to 2^31, -128 times 127 to its opposite less 2^24."""
+    k = 2**17
+    xq = torch.full((rows, k), -128, dtype=torch.int8, device="cuda")
+    wq = torch.full((n, k), -128, dtype=torch.int8, device="cuda")
+    wq[1] = 127
+    wq[2, 5] = -127
+    wq[3, k // 2:] = 127
+    one = torch.ones(max(rows, n), device="cuda")
+    y = experts.int8_matmul(xq, one[:rows], wq, one[:n])
+    sums = xq[:1].double() @ wq.double().t().contiguous()
+    assert int(sums[0, 0]) == 2**31
+    assert_int8(y, sums.expand(rows, n), one[:rows].view(-1, 1), one[:n].view(1, -1))
