@@ -366,8 +366,12 @@ class _Merge(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         y, weights, *g = ctx.saved_tensors
-        dy, dweights = combine_backward(_plain_rows(dout), y, Groups(*g), weights)
-        dy, dweights = _first_order(dy, dout, weights), _first_order(dweights, dout, y)
+        g = Groups(*g)
+        by = weights if weights is not None else torch.ones(
+            g.place.shape, dtype=torch.float32, device=y.device)
+        dy, dweights = combine_backward(_plain_rows(dout), y, g, by)
+        dy = _first_order(dy, dout, by)
+        dweights = None if weights is None else _first_order(dweights, dout, y)
         return (dy, dweights) + (None,) * len(g)
 
 
@@ -376,6 +380,6 @@ def linear(x: torch.Tensor, w: torch.Tensor, g: Groups, gather: bool = False) ->
     return _Linear.apply(x, w, gather, *g)
 
 
-def merge(y: torch.Tensor, g: Groups, weights: torch.Tensor) -> torch.Tensor:
-    """``combine`` with gradients for y and the weights."""
+def merge(y: torch.Tensor, g: Groups, weights: torch.Tensor | None) -> torch.Tensor:
+    """``combine`` with gradients for y and the weights (if there are any)."""
     return _Merge.apply(y, weights, *g)

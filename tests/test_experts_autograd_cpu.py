@@ -127,3 +127,15 @@ def test_a_gradient_that_depends_on_no_leaf_stays_a_constant(opaque):
     y = plain_matmul(x, w, g, True).detach().requires_grad_()
     grad, = torch.autograd.grad(experts.merge(y, g, weights.detach()).sum(), y, create_graph=True)
     assert not grad.requires_grad
+
+
+def test_merge_without_weights_adds_the_rows(opaque):
+    """As combine does without weights; the rows' gradients are the tokens'."""
+    g, x, w, _ = inputs()
+    y = plain_matmul(x, w, g, True).detach().requires_grad_()
+    out = experts.merge(y, g, None)
+    want = plain_combine(y, g)
+    torch.testing.assert_close(out, want, rtol=1e-12, atol=1e-12)
+    seed = torch.randn(*out.shape, dtype=out.dtype)
+    for a, b in zip(torch.autograd.grad(out, y, seed), torch.autograd.grad(want, y, seed)):
+        torch.testing.assert_close(a, b, rtol=1e-12, atol=1e-12)
