@@ -61,12 +61,15 @@ _raw_stream = torch._C._cuda_getCurrentRawStream  # 0.1 us; current_stream().cud
 
 
 def _library():
+    global _functions
     lib = hist.library()
     if not _functions:
+        bound = {}
         for name, args in _SIGNATURES.items():
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = _i32, args
-            _functions[name] = fn
+            bound[name] = fn
+        _functions = bound  # whole at once: another thread sees none of them or all
     return lib
 
 
@@ -164,8 +167,9 @@ def group_rows(ids: torch.Tensor, experts: int) -> Groups:
     pairs, work = tokens * top_k, 0
     if pairs > _ONE_WORKGROUP:
         need = _u64()
-        status = _library().experts_group_workspace_size(tokens, top_k, experts,
-                                                         ctypes.byref(need))
+        _library()
+        status = _functions["experts_group_workspace_size"](tokens, top_k, experts,
+                                                            ctypes.byref(need))
         if status:
             raise hist.HistError(status, "experts_group_workspace_size")
         work = need.value // 4
