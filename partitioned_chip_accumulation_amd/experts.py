@@ -57,7 +57,9 @@ _SIGNATURES = {
                             _u32, _u32, _u32, _u32, _i32, _vp],
 }
 _functions: dict = {}
-_raw_stream = torch._C._cuda_getCurrentRawStream  # 0.1 us; current_stream().cuda_stream takes 2.8
+# 0.1 us; current_stream().cuda_stream takes 2.8. (A torch build for the host alone does not have it; no
+# tensor gets as far as a call there.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _library():

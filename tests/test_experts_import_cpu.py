@@ -57,3 +57,27 @@ def test_two_threads_in_their_first_call(monkeypatch):
     assert not first.is_alive() and not second.is_alive()
     assert not failed
     assert set(experts._functions) == set(experts._SIGNATURES)
+
+
+def test_import_without_a_gpu_runtime():
+    """A torch build for the host alone lacks the GPU's entry points; the package imports there, and
+    what needs no GPU works."""
+    code = ("import torch\n"
+            "for name in [n for n in dir(torch._C) if n.startswith('_cuda_getCurrent')]:\n"
+            "    delattr(torch._C, name)\n"
+            "import partitioned_chip_accumulation_amd as p\n"
+            "from partitioned_chip_accumulation_amd import experts, hist\n"
+            "assert hist.library() and p.experts is experts\n"
+            "try:\n"
+            "    experts.quantize_rows(torch.zeros(2, 8, dtype=torch.bfloat16))\n"
+            "except ValueError:\n"
+            "    print('refused')\n")
+    run = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
+                         timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
+    assert run.stdout.strip() == "refused"
+
+
+def test_binding_exists_without_a_gpu():
+    size = ctypes.c_uint64(0)
+    assert experts._library().experts_group_workspace_size(8, 2, 4, ctypes.byref(size)) == 0
