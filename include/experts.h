@@ -33,8 +33,8 @@
  * calls only queue kernels on `stream` (no allocation, memset or
  * synchronisation, so they can be captured into a HIP graph), inputs and
  * outputs must not overlap, statuses are hist_status_t and come before any
- * work is queued. Sizes whose launch would take 2^32 threads or more give
- * HIST_ERR_UNSUPPORTED. Device-side indexes (offsets, order, place) are clamped or
+ * work is queued. Products whose launch would take 2^32 threads or more (some
+ * 2^37 results) give HIST_ERR_UNSUPPORTED. Device-side indexes (offsets, order, place) are clamped or
  * skipped when out of range; they never lead outside the buffers.
  */
 #ifndef PCA_EXPERTS_H

@@ -70,11 +70,11 @@ __global__ void __launch_bounds__(kThreads)
                        const T *__restrict__ dout, int64_t lddout, const T *__restrict__ y,
                        int64_t ldy, const int32_t *__restrict__ order,
                        const int32_t *__restrict__ place, const float *__restrict__ weights,
-                       uint32_t pairs, uint32_t top_k, uint32_t n)
+                       uint32_t first, uint32_t pairs, uint32_t top_k, uint32_t n)
 {
     typedef typename Vec8<T>::type V;
-    const uint32_t i = __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) +
-                                                      threadIdx.x / 64);
+    const uint32_t i = first + __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) +
+                                                              threadIdx.x / 64);
     if (i >= pairs) return;
     const uint32_t lane = threadIdx.x % 64;
     if ((uint32_t)order[i] >= pairs) {
@@ -111,6 +111,48 @@ __global__ void __launch_bounds__(kThreads)
 
 using namespace pca_experts;
 
+template <class T>
+static hist_status_t launch_combine(void *out, int64_t ldo, const void *y, int64_t ldy,
+                                    uint32_t rows, const int32_t *place, const float *weights,
+                                    uint64_t tokens, uint32_t top_k, uint32_t n,
+                                    hipStream_t stream)
+{
+    uint32_t lanes_log2 = 4;
+    while (lanes_log2 < 6 && (kCols << lanes_log2) < n) ++lanes_log2;
+    const uint32_t parts = (n + (kCols << lanes_log2) - 1) / (kCols << lanes_log2);
+    const uint64_t most = (most_of(kThreads, kThreads) >> lanes_log2) / parts;
+    hist_status_t st = HIST_OK;
+    for (uint64_t t = 0; t < tokens && st == HIST_OK; t += most) {
+        const uint64_t some = tokens - t < most ? tokens - t : most;
+        const uint64_t blocks = (((some * parts) << lanes_log2) + kThreads - 1) / kThreads;
+        st = launch(k_combine<T>, blocks, kThreads, 0, stream, (T *)out + t * ldo, ldo,
+                    (const T *)y, ldy, rows, place + t * top_k,
+                    weights ? weights + t * top_k : nullptr, (uint32_t)some, top_k, n, lanes_log2,
+                    parts);
+    }
+    return st;
+}
+
+template <class T>
+static hist_status_t launch_combine_backward(void *dy, int64_t lddy, float *dweights,
+                                             const void *dout, int64_t lddout, const void *y,
+                                             int64_t ldy, const int32_t *order,
+                                             const int32_t *place, const float *weights,
+                                             uint32_t pairs, uint32_t top_k, uint32_t n,
+                                             hipStream_t stream)
+{
+    constexpr uint32_t kEach = kThreads / 64;
+    const uint64_t most = most_of(kEach, kThreads);
+    hist_status_t st = HIST_OK;
+    for (uint64_t first = 0; first < pairs && st == HIST_OK; first += most) {
+        const uint64_t some = pairs - first < most ? pairs - first : most;
+        st = launch(k_combine_backward<T>, (some + kEach - 1) / kEach, kThreads, 0, stream, (T *)dy,
+                    lddy, dweights, (const T *)dout, lddout, (const T *)y, ldy, order, place,
+                    weights, (uint32_t)first, pairs, top_k, n);
+    }
+    return st;
+}
+
 static hist_status_t check_rows(uint64_t tokens, uint32_t top_k, uint32_t n, int32_t dtype)
 {
     if (!dtype_ok(dtype) || top_k == 0 || n == 0) return HIST_ERR_INVALID_ARG;
@@ -134,17 +176,8 @@ extern "C" hist_status_t experts_combine(void *out, int64_t ldo, const void *y, 
         return HIST_ERR_INVALID_ARG;
     st = device_status();
     if (st != HIST_OK || tokens == 0) return st;
-    uint32_t lanes_log2 = 4;
-    while (lanes_log2 < 6 && (kCols << lanes_log2) < n) ++lanes_log2;
-    const uint32_t parts = (n + (kCols << lanes_log2) - 1) / (kCols << lanes_log2);
-    const uint64_t blocks = (((tokens * parts) << lanes_log2) + kThreads - 1) / kThreads;
-    if (dtype == EXPERTS_BF16)
-        return launch(k_combine<__bf16>, blocks, kThreads, 0, stream, (__bf16 *)out, ldo,
-                      (const __bf16 *)y, ldy, (uint32_t)rows, place, weights, (uint32_t)tokens,
-                      top_k, n, lanes_log2, parts);
-    return launch(k_combine<_Float16>, blocks, kThreads, 0, stream, (_Float16 *)out, ldo,
-                  (const _Float16 *)y, ldy, (uint32_t)rows, place, weights, (uint32_t)tokens, top_k,
-                  n, lanes_log2, parts);
+    return (dtype == EXPERTS_BF16 ? launch_combine<__bf16> : launch_combine<_Float16>)(
+        out, ldo, y, ldy, (uint32_t)rows, place, weights, tokens, top_k, n, stream);
 }
 
 extern "C" hist_status_t experts_combine_backward(void *dy, int64_t lddy, float *dweights,
@@ -164,13 +197,8 @@ extern "C" hist_status_t experts_combine_backward(void *dy, int64_t lddy, float 
         return HIST_ERR_INVALID_ARG;
     st = device_status();
     if (st != HIST_OK || tokens == 0) return st;
-    const uint32_t pairs = (uint32_t)(tokens * top_k);
-    const uint32_t blocks = (pairs + kThreads / 64 - 1) / (kThreads / 64);
-    if (dtype == EXPERTS_BF16)
-        return launch(k_combine_backward<__bf16>, blocks, kThreads, 0, stream, (__bf16 *)dy, lddy,
-                      dweights, (const __bf16 *)dout, lddout, (const __bf16 *)y, ldy, order, place,
-                      weights, pairs, top_k, n);
-    return launch(k_combine_backward<_Float16>, blocks, kThreads, 0, stream, (_Float16 *)dy, lddy,
-                  dweights, (const _Float16 *)dout, lddout, (const _Float16 *)y, ldy, order, place,
-                  weights, pairs, top_k, n);
+    return (dtype == EXPERTS_BF16 ? launch_combine_backward<__bf16>
+                                  : launch_combine_backward<_Float16>)(
+        dy, lddy, dweights, dout, lddout, y, ldy, order, place, weights,
+        (uint32_t)(tokens * top_k), top_k, n, stream);
 }

@@ -99,7 +99,11 @@ inline hist_status_t device_status()
     return pca_host::device_supported(dev);
 }
 
-// Queues a kernel. A launch is limited to 2^32 - 1 threads.
+// What one launch takes at `each` a workgroup: it is limited to 2^32 - 1 threads. The operators whose
+// rows are their own work queue as many launches as that needs.
+inline uint64_t most_of(uint64_t each, uint32_t threads) { return UINT32_MAX / threads * each; }
+
+// Queues a kernel.
 template <class... P, class... A>
 hist_status_t launch(void (*kernel)(P...), uint64_t blocks, uint32_t threads, uint32_t lds,
                      hipStream_t stream, A... args)

@@ -112,11 +112,19 @@ template <class T>
 hist_status_t launch_quantize(int8_t *xq, int64_t ldq, float *sx, const void *x, int64_t ldx,
                               uint32_t rows, uint32_t k, hipStream_t stream)
 {
-    if (k <= 1024)
-        return launch(k_quantize<T, 64, 2>, (rows + 3) / 4, 256, 0, stream, xq, ldq, sx,
-                      (const T *)x, ldx, rows, k);
-    return launch(k_quantize<T, 256, 4>, rows, 256, 0, stream, xq, ldq, sx, (const T *)x, ldx, rows,
-                  k);
+    const bool narrow = k <= 1024;
+    const uint64_t most = most_of(narrow ? 4 : 1, 256);
+    hist_status_t st = HIST_OK;
+    for (uint64_t r = 0; r < rows && st == HIST_OK; r += most) {
+        const uint32_t high = (uint32_t)(rows - r < most ? rows - r : most);
+        int8_t *to = xq + r * ldq;
+        const T *from = (const T *)x + r * ldx;
+        st = narrow ? launch(k_quantize<T, 64, 2>, (high + 3) / 4, 256, 0, stream, to, ldq, sx + r,
+                             from, ldx, high, k)
+                    : launch(k_quantize<T, 256, 4>, high, 256, 0, stream, to, ldq, sx + r, from,
+                             ldx, high, k);
+    }
+    return st;
 }
 
 }  // namespace pca_experts
