@@ -8,7 +8,8 @@
 
 namespace pca_experts {
 
-constexpr uint32_t kCus = 256;  // of the device
+constexpr uint32_t kCus = 256;           // of the device
+constexpr uint32_t kLdsOfCu = 160 << 10;  // bytes
 
 struct RowsArgs {
     char *out;
@@ -904,13 +905,15 @@ inline bool aligned16(const void *p, int64_t ld_bytes)
 template <class T, class O, bool ACROSS, bool DIRECT, class S>
 hist_status_t launch_tiles(RowsArgs g, hipStream_t stream)
 {
+    constexpr uint32_t kLds = S::STAGES * RowsParts<T, S, ACROSS>::STAGE;
+    static_assert(S::PER_CU * kLds <= kLdsOfCu, "workgroups that a CU holds at one time");
+    static_assert(S::BM * S::BN * sizeof(O) <= kLds, "results on their way to memory");
     g.n_tiles = (g.cols + S::BN - 1) / S::BN;
     const uint64_t tiles =
         most_row_tiles(g.rows, g.offsets ? g.experts + 1 : 1, S::BM) * g.n_tiles;
     // (and a workgroup more for each tile of a last round that is at most half full)
     const uint64_t blocks = blocks_for(tiles + (S::BM == 256 ? kCus / 2 : 0), &g.span);
-    return launch(k_rows<T, O, S, ACROSS, DIRECT>, blocks, S::THREADS,
-                  S::STAGES * RowsParts<T, S, ACROSS>::STAGE, stream, g);
+    return launch(k_rows<T, O, S, ACROSS, DIRECT>, blocks, S::THREADS, kLds, stream, g);
 }
 
 // Whether `rows` rows from one base lie within 32-bit offsets.
@@ -966,9 +969,14 @@ hist_status_t launch_rows(RowsArgs g, hipStream_t stream)
         g.bytes % 16 == 0 && (!ACROSS || g.cols % 8 == 0) &&
         near(g.order ? g.a_rows : 256, g.lda) && near(256, g.ldb)) {
         typedef Shape<64, 128, 2, 2, 2, 3> Low;
-        constexpr int kWm = ACROSS ? 2 : 1, kWn = ACROSS ? 2 : 4;
-        typedef Shape<32, 128, kWm, kWn, 2, 4> Lowest;
-        typedef Shape<32, 128, kWm, kWn, 4, 2> LowestShort;
+        // A stage with weights across the reduction takes 21 KiB of LDS, along it 20, so the gradient of
+        // the rows has a stage, or a workgroup, less (32 experts, 2560 -> 2048: 2 to 32 rows an expert
+        // 62-64 us, 5.2-5.4 TB/s of weights, 40 rows 78; a fourth stage, which leaves one workgroup on
+        // a CU, 62-66 and 82; 1344 -> 2048: 33-34 and 34-36. 64 rows, 64 x 128: 67 us).
+        typedef typename std::conditional<ACROSS, Shape<32, 128, 2, 2, 2, 3>,
+                                          Shape<32, 128, 1, 4, 2, 4>>::type Lowest;
+        typedef typename std::conditional<ACROSS, Shape<32, 128, 2, 2, 3>,
+                                          Shape<32, 128, 1, 4, 4>>::type LowestShort;
         // a short reduction has no use for stages, but for workgroups beside it (16384 rows, 8 experts,
         // 256 -> 2048: 31 us in 128 x 128, 37 in 256 x 256; 1024 -> 2048: 78 and 80)
         const bool brief = g.bytes <= 8 * kStepBytes;
@@ -1016,10 +1024,13 @@ hist_status_t launch_rows(RowsArgs g, hipStream_t stream)
 template <class T, bool DIRECT, class S>
 hist_status_t launch_dw_tiles(DwArgs g, hipStream_t stream)
 {
+    constexpr uint32_t kLds = 2 * DwParts<T, S>::STAGE;
+    static_assert(S::PER_CU * kLds <= kLdsOfCu, "workgroups that a CU holds at one time");
+    static_assert(S::BM * S::BN * sizeof(T) <= kLds, "results on their way to memory");
     g.n_tiles = (g.n + S::BM - 1) / S::BM;
     g.k_tiles = (g.k + S::BN - 1) / S::BN;
     const uint64_t blocks = blocks_for((uint64_t)g.n_tiles * g.k_tiles * g.experts, &g.span);
-    return launch(k_dw<T, S, DIRECT>, blocks, S::THREADS, 2 * DwParts<T, S>::STAGE, stream, g);
+    return launch(k_dw<T, S, DIRECT>, blocks, S::THREADS, kLds, stream, g);
 }
 
 template <class T>
