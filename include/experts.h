@@ -126,6 +126,32 @@ hist_status_t experts_int8_matmul(void *y, int64_t ldy, const int8_t *xq, int64_
                                   uint32_t experts, uint32_t n, uint32_t k, int32_t dtype,
                                   hipStream_t stream);
 
+typedef enum {
+    EXPERTS_MATMUL = 0,
+    EXPERTS_MATMUL_DX = 1,
+    EXPERTS_MATMUL_DW = 2,
+    EXPERTS_INT8_MATMUL = 3
+} experts_product_t;
+
+typedef struct {
+    uint32_t rows, cols; /* of the results that one workgroup computes */
+    uint32_t threads;    /* of a workgroup */
+    uint32_t stages;     /* steps of the reduction in LDS; 0: operands in registers, and the
+                            reduction divided among the workgroup's waves */
+    uint32_t per_cu;     /* workgroups on a CU at one time (0 where stages is) */
+    uint32_t direct;     /* 1: operands go straight from memory to LDS */
+} experts_kernel_t;
+
+/* The kernel that a product of these sizes takes, computed on the host with no
+ * device present, for tests of the rules. x_rows: rows of a gathered x, 0 if
+ * order is NULL. experts 0: the dense 8-bit product. lda, ldb: the leading
+ * dimensions of x and w (matmul, int8_matmul), dy and w (dx), dy and x (dw).
+ * alignment: of the operands' addresses in bytes, a power of two; the experts'
+ * weights follow one another. rows must be positive. */
+hist_status_t experts_product_preview(int32_t product, uint64_t rows, uint64_t x_rows,
+                                      uint32_t experts, uint32_t n, uint32_t k, int64_t lda,
+                                      int64_t ldb, uint32_t alignment, experts_kernel_t *kernel);
+
 #ifdef __cplusplus
 }
 #endif

@@ -49,3 +49,37 @@ extern "C" hist_status_t experts_matmul_dx(void *dx, int64_t lddx, const void *d
                ? launch_rows<__bf16, __bf16, true>(g, stream)
                : launch_rows<_Float16, _Float16, true>(g, stream);
 }
+
+// The rules read the operands' addresses, so the preview makes up addresses as aligned as it is told.
+extern "C" hist_status_t experts_product_preview(int32_t product, uint64_t rows, uint64_t x_rows,
+                                                 uint32_t experts, uint32_t n, uint32_t k,
+                                                 int64_t lda, int64_t ldb, uint32_t alignment,
+                                                 experts_kernel_t *kernel)
+{
+    const bool dense = product == EXPERTS_INT8_MATMUL && experts == 0, gather = x_rows != 0;
+    if (!kernel || product < EXPERTS_MATMUL || product > EXPERTS_INT8_MATMUL || alignment == 0 ||
+        (alignment & (alignment - 1)) || (gather && (dense || product == EXPERTS_MATMUL_DX)))
+        return HIST_ERR_INVALID_ARG;
+    const uint32_t groups = dense ? 1 : experts;
+    const hist_status_t st = check_sizes(rows, x_rows, 1, groups, n, k);
+    if (st != HIST_OK) return st;
+    const bool dx = product == EXPERTS_MATMUL_DX, dw = product == EXPERTS_MATMUL_DW;
+    if (lda < (int64_t)(dx || dw ? n : k) || ldb < (int64_t)k || rows == 0)
+        return HIST_ERR_INVALID_ARG;
+    char *const at = (char *)(uintptr_t)alignment;
+    const int32_t *const list = (const int32_t *)at;  // not read here
+    const int64_t size = product == EXPERTS_INT8_MATMUL ? 1 : 2;
+    const uint32_t a_rows = (uint32_t)(gather ? x_rows : rows);
+    if (dw) {
+        const DwArgs g = {at, at, at, lda * size, ldb * size, list, gather ? list : nullptr,
+                          (uint32_t)rows, a_rows, groups, n, k, 0, 0, 0, Divide::by(1)};
+        return with_dw_kernel(dw_kernel(g), DescribeKernel{kernel});
+    }
+    const uint32_t reduction = dx ? n : k;
+    const RowsArgs g = {at, at, at, 0, lda * size, ldb * size, ldb * size * n,
+                        dense ? nullptr : list, gather ? list : nullptr, nullptr, nullptr,
+                        (uint32_t)rows, a_rows, groups, dx ? k : n, (uint32_t)(reduction * size), 0,
+                        0, Divide::by(1)};
+    return dx ? with_rows_kernel<true>(rows_kernel<true>(g), DescribeKernel{kernel})
+              : with_rows_kernel<false>(rows_kernel<false>(g), DescribeKernel{kernel});
+}

@@ -950,9 +950,16 @@ hist_status_t launch_thin(RowsArgs g, hipStream_t stream)
 // workgroups a CU). Few tiles, a dense weight of 8192 x 4096 in 8 bits (64x64, 64x128, 128x128,
 // 256x256): rows 256: 20.0, 19.3, 27.6, 38.8; rows 512: 32.5, 28.7, 30.1, 40.0; rows 1024: 54.8,
 // 47.9, 40.0, 43.5; and thin 32 x 64 against 64 x 64: rows 32: 18.6, 20.5; rows 64: 18.9, 20.8.
-template <class T, class O, bool ACROSS>
-hist_status_t launch_rows(RowsArgs g, hipStream_t stream)
+enum class RowsKernel {
+    kThin16, kThin32,                                                           // divided reduction
+    k256x256, k128x256, k128x128Alone, k128x128, k64x128, k32x128, k32x128Short, k64x64,  // direct
+    kVia256x128, kVia128x128, kVia64x64, kVia32x128                             // through registers
+};
+
+template <bool ACROSS>
+RowsKernel rows_kernel(const RowsArgs &g)
 {
+    typedef RowsKernel K;
     const uint64_t groups = g.offsets ? g.experts : 1, each = g.rows / groups;
     // about so many: half a tile of each group is empty
     auto tiles = [&](uint32_t bm, uint32_t bn) {
@@ -961,64 +968,103 @@ hist_status_t launch_rows(RowsArgs g, hipStream_t stream)
     };
     // The thin kernels divide the reduction among waves, the others do not, so the choice between
     // them does not depend on alignment: a product's bits are the same at every address.
-    if constexpr (!ACROSS) {
-        if (each <= 6) return launch_thin<T, O, 1, 1, 4>(g, stream);
-        if (tiles(64, 64) < (each <= 64 ? 256 : 128)) return launch_thin<T, O, 2, 4, 2>(g, stream);
+    if (!ACROSS) {
+        if (each <= 6) return K::kThin16;
+        if (tiles(64, 64) < (each <= 64 ? 256 : 128)) return K::kThin32;
     }
     if (aligned16(g.a, g.lda) && aligned16(g.b, g.ldb) && g.b_stride % 16 == 0 &&
         g.bytes % 16 == 0 && (!ACROSS || g.cols % 8 == 0) &&
         near(g.order ? g.a_rows : 256, g.lda) && near(256, g.ldb)) {
-        typedef Shape<64, 128, 2, 2, 2, 3> Low;
-        // A stage with weights across the reduction takes 21 KiB of LDS, along it 20, so the gradient of
-        // the rows has a stage, or a workgroup, less (32 experts, 2560 -> 2048: 2 to 32 rows an expert
-        // 62-64 us, 5.2-5.4 TB/s of weights, 40 rows 78; a fourth stage, which leaves one workgroup on
-        // a CU, 62-66 and 82; 1344 -> 2048: 33-34 and 34-36. 64 rows, 64 x 128: 67 us).
-        typedef typename std::conditional<ACROSS, Shape<32, 128, 2, 2, 2, 3>,
-                                          Shape<32, 128, 1, 4, 2, 4>>::type Lowest;
-        typedef typename std::conditional<ACROSS, Shape<32, 128, 2, 2, 3>,
-                                          Shape<32, 128, 1, 4, 4>>::type LowestShort;
         // a short reduction has no use for stages, but for workgroups beside it (16384 rows, 8 experts,
         // 256 -> 2048: 31 us in 128 x 128, 37 in 256 x 256; 1024 -> 2048: 78 and 80)
         const bool brief = g.bytes <= 8 * kStepBytes;
-        if (!brief && each >= 224 && g.cols > 128 && tiles(256, 256) >= 256)
-            return launch_tiles<T, O, ACROSS, true, Shape<256, 256, 2, 4, 1>>(g, stream);
-        if (!brief && each >= 80 && g.cols > 128 && tiles(128, 256) >= 384)
-            return launch_tiles<T, O, ACROSS, true, Shape<128, 256, 2, 4, 1, 3>>(g, stream);
+        if (!brief && each >= 224 && g.cols > 128 && tiles(256, 256) >= 256) return K::k256x256;
+        if (!brief && each >= 80 && g.cols > 128 && tiles(128, 256) >= 384) return K::k128x256;
         // a workgroup on each CU at most: stages instead of a second one (8 bits, 8192 x 4096, 512
         // rows: 25 us, with two stages 30)
-        if (each >= 80 && tiles(128, 128) >= 128 && tiles(128, 128) <= 256)
-            return launch_tiles<T, O, ACROSS, true, Shape<128, 128, 4, 2, 1, 4>>(g, stream);
+        const uint64_t small = tiles(128, 128), large = tiles(256, 256);
+        if (each >= 80 && small >= 128 && small <= 256) return K::k128x128Alone;
         // A few tiles more than the 512 that run at one time take as long as a round of them (the
         // count is an estimate, hence 528): large tiles, if one round of those fills most CUs. 16
         // experts, 175 rows each, 2688 x 4096: 111 us, with small tiles 147; 32 experts, 138 rows
         // each, 1344 x 2048: 60 and 75 us, but with 128 rows each, in one round, 59 and 53.
-        const uint64_t small = tiles(128, 128), large = tiles(256, 256);
         if (each >= 80 && small > 528 && small % 512 < 128 && large >= 160 && large <= 256 && !brief)
-            return launch_tiles<T, O, ACROSS, true, Shape<256, 256, 2, 4, 1>>(g, stream);
-        if (each >= 80 && small >= 256)
-            return launch_tiles<T, O, ACROSS, true, Shape<128, 128, 2, 2, 2>>(g, stream);
-        if (each > 40 && tiles(64, 128) >= 256)
-            return launch_tiles<T, O, ACROSS, true, Low>(g, stream);
-        if constexpr (ACROSS) {
-            if (each > 40) return launch_tiles<T, O, ACROSS, true, Low>(g, stream);
-            return brief ? launch_tiles<T, O, ACROSS, true, LowestShort>(g, stream)
-                         : launch_tiles<T, O, ACROSS, true, Lowest>(g, stream);
-        } else {
-            if (each <= 40 && tiles(32, 128) >= 256)
-                return brief ? launch_tiles<T, O, ACROSS, true, LowestShort>(g, stream)
-                             : launch_tiles<T, O, ACROSS, true, Lowest>(g, stream);
-            return launch_tiles<T, O, ACROSS, true, Shape<64, 64, 2, 2, 3, 3>>(g, stream);
-        }
+            return K::k256x256;
+        if (each >= 80 && small >= 256) return K::k128x128;
+        if (each > 40 && (ACROSS || tiles(64, 128) >= 256)) return K::k64x128;
+        if (ACROSS || (each <= 40 && tiles(32, 128) >= 256))
+            return brief ? K::k32x128Short : K::k32x128;
+        return K::k64x64;
     }
     // Through registers. A load that is not aligned takes the CU's path to its cache twice, so a tile
     // that loads less for its products counts for more: 16 experts of 1024 rows on average, 2560 x
     // 2053, 256 x 128 against 128 x 128: 286 and 302 us, the gradient of the rows 231 and 267.
-    if (each >= 192 && tiles(256, 128) >= 256)
-        return launch_tiles<T, O, ACROSS, false, Shape<256, 128, 4, 2, 1>>(g, stream);
-    if (each >= 80 && tiles(128, 128) >= 256)
-        return launch_tiles<T, O, ACROSS, false, Shape<128, 128, 2, 2, 2>>(g, stream);
-    if constexpr (ACROSS) return launch_tiles<T, O, ACROSS, false, Shape<32, 128, 2, 2, 3>>(g, stream);
-    else return launch_tiles<T, O, ACROSS, false, Shape<64, 64, 2, 2, 3>>(g, stream);
+    if (each >= 192 && tiles(256, 128) >= 256) return K::kVia256x128;
+    if (each >= 80 && tiles(128, 128) >= 256) return K::kVia128x128;
+    return ACROSS ? K::kVia32x128 : K::kVia64x64;
+}
+
+// What a kernel is made for: a shape of tiles, or the thin kernel's parameters.
+template <class S, bool DIRECT> struct Tiles {};
+template <int RM, int FN, int DEEP> struct Thin {};
+
+// Calls f with what the kernel is made for.
+template <bool ACROSS, class F>
+hist_status_t with_rows_kernel(RowsKernel kernel, const F &f)
+{
+    typedef RowsKernel K;
+    // A stage with weights across the reduction takes 21 KiB of LDS, along it 20, so the gradient of
+    // the rows has a stage, or a workgroup, less (32 experts, 2560 -> 2048: 2 to 32 rows an expert
+    // 62-64 us, 5.2-5.4 TB/s of weights, 40 rows 78; a fourth stage, which leaves one workgroup on
+    // a CU, 62-66 and 82; 1344 -> 2048: 33-34 and 34-36. 64 rows, 64 x 128: 67 us).
+    typedef typename std::conditional<ACROSS, Shape<32, 128, 2, 2, 2, 3>,
+                                      Shape<32, 128, 1, 4, 2, 4>>::type Lowest;
+    typedef typename std::conditional<ACROSS, Shape<32, 128, 2, 2, 3>,
+                                      Shape<32, 128, 1, 4, 4>>::type LowestShort;
+    switch (kernel) {
+    case K::k256x256: return f(Tiles<Shape<256, 256, 2, 4, 1>, true>());
+    case K::k128x256: return f(Tiles<Shape<128, 256, 2, 4, 1, 3>, true>());
+    case K::k128x128Alone: return f(Tiles<Shape<128, 128, 4, 2, 1, 4>, true>());
+    case K::k128x128: return f(Tiles<Shape<128, 128, 2, 2, 2>, true>());
+    case K::k64x128: return f(Tiles<Shape<64, 128, 2, 2, 2, 3>, true>());
+    case K::k32x128: return f(Tiles<Lowest, true>());
+    case K::k32x128Short: return f(Tiles<LowestShort, true>());
+    case K::kVia256x128: return f(Tiles<Shape<256, 128, 4, 2, 1>, false>());
+    case K::kVia128x128: return f(Tiles<Shape<128, 128, 2, 2, 2>, false>());
+    default: break;
+    }
+    if constexpr (ACROSS) {
+        return f(Tiles<Shape<32, 128, 2, 2, 3>, false>());
+    } else {
+        switch (kernel) {
+        case K::kThin16: return f(Thin<1, 1, 4>());
+        case K::kThin32: return f(Thin<2, 4, 2>());
+        case K::k64x64: return f(Tiles<Shape<64, 64, 2, 2, 3, 3>, true>());
+        default: return f(Tiles<Shape<64, 64, 2, 2, 3>, false>());
+        }
+    }
+}
+
+template <class T, class O, bool ACROSS>
+struct LaunchRows {
+    const RowsArgs &g;
+    hipStream_t stream;
+    template <class S, bool DIRECT>
+    hist_status_t operator()(Tiles<S, DIRECT>) const
+    {
+        return launch_tiles<T, O, ACROSS, DIRECT, S>(g, stream);
+    }
+    template <int RM, int FN, int DEEP>
+    hist_status_t operator()(Thin<RM, FN, DEEP>) const
+    {
+        return launch_thin<T, O, RM, FN, DEEP>(g, stream);
+    }
+};
+
+template <class T, class O, bool ACROSS>
+hist_status_t launch_rows(const RowsArgs &g, hipStream_t stream)
+{
+    return with_rows_kernel<ACROSS>(rows_kernel<ACROSS>(g), LaunchRows<T, O, ACROSS>{g, stream});
 }
 
 template <class T, bool DIRECT, class S>
@@ -1033,9 +1079,11 @@ hist_status_t launch_dw_tiles(DwArgs g, hipStream_t stream)
     return launch(k_dw<T, S, DIRECT>, blocks, S::THREADS, kLds, stream, g);
 }
 
-template <class T>
-hist_status_t launch_dw(DwArgs g, hipStream_t stream)
+enum class DwKernel { k256x256, k128x128, kVia256x128, kVia128x128 };
+
+inline DwKernel dw_kernel(const DwArgs &g)
 {
+    typedef DwKernel K;
     auto tiles = [&](uint32_t bm, uint32_t bn) {
         return (uint64_t)g.experts * ((g.n + bm - 1) / bm) * ((g.k + bn - 1) / bn);
     };
@@ -1044,15 +1092,57 @@ hist_status_t launch_dw(DwArgs g, hipStream_t stream)
         // Large tiles, if they are enough for most of 256 CUs and not much larger than the weight (32
         // experts, 1024 rows each, 528 x 288: 53 us, in small ones 34; 1024 x 1024: 98 and 111).
         const uint64_t area = tiles(256, 256) * 256 * 256;
-        return tiles(256, 256) >= 176 && area * 4 <= tiles(128, 128) * 128 * 128 * 5
-                   ? launch_dw_tiles<T, true, Shape<256, 256, 2, 4, 1>>(g, stream)
-                   : launch_dw_tiles<T, true, Shape<128, 128, 2, 2, 2>>(g, stream);
+        return tiles(256, 256) >= 176 && area * 4 <= tiles(128, 128) * 128 * 128 * 5 ? K::k256x256
+                                                                                    : K::k128x128;
     }
     // (the same sizes: 404 and 516 us)
-    return tiles(256, 128) >= 256
-               ? launch_dw_tiles<T, false, Shape<256, 128, 4, 2, 1>>(g, stream)
-               : launch_dw_tiles<T, false, Shape<128, 128, 2, 2, 2>>(g, stream);
+    return tiles(256, 128) >= 256 ? K::kVia256x128 : K::kVia128x128;
 }
+
+template <class F>
+hist_status_t with_dw_kernel(DwKernel kernel, const F &f)
+{
+    switch (kernel) {
+    case DwKernel::k256x256: return f(Tiles<Shape<256, 256, 2, 4, 1>, true>());
+    case DwKernel::k128x128: return f(Tiles<Shape<128, 128, 2, 2, 2>, true>());
+    case DwKernel::kVia256x128: return f(Tiles<Shape<256, 128, 4, 2, 1>, false>());
+    default: return f(Tiles<Shape<128, 128, 2, 2, 2>, false>());
+    }
+}
+
+template <class T>
+struct LaunchDw {
+    const DwArgs &g;
+    hipStream_t stream;
+    template <class S, bool DIRECT>
+    hist_status_t operator()(Tiles<S, DIRECT>) const
+    {
+        return launch_dw_tiles<T, DIRECT, S>(g, stream);
+    }
+};
+
+template <class T>
+hist_status_t launch_dw(const DwArgs &g, hipStream_t stream)
+{
+    return with_dw_kernel(dw_kernel(g), LaunchDw<T>{g, stream});
+}
+
+// Fills in the answer of experts_product_preview.
+struct DescribeKernel {
+    experts_kernel_t *kernel;
+    template <class S, bool DIRECT>
+    hist_status_t operator()(Tiles<S, DIRECT>) const
+    {
+        *kernel = {S::BM, S::BN, S::THREADS, S::STAGES, S::PER_CU, DIRECT};
+        return HIST_OK;
+    }
+    template <int RM, int FN, int DEEP>
+    hist_status_t operator()(Thin<RM, FN, DEEP>) const
+    {
+        *kernel = {16 * RM, 16 * FN, 256, 0, 0, 0};
+        return HIST_OK;
+    }
+};
 
 // Checks that the products share. `unit`: bytes of an element of the result
 // of a leading dimension.

@@ -56,6 +56,17 @@ _SIGNATURES = {
     "experts_int8_matmul": [_vp, _i64, _vp, _i64, _u64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _u64,
                             _u32, _u32, _u32, _u32, _i32, _vp],
 }
+PRODUCTS = {"matmul": 0, "matmul_dx": 1, "matmul_dw": 2, "int8_matmul": 3}
+
+
+class Kernel(ctypes.Structure):
+    """The kernel of a product (``preview``)."""
+    _fields_ = [("rows", _u32), ("cols", _u32), ("threads", _u32), ("stages", _u32),
+                ("per_cu", _u32), ("direct", _u32)]
+
+
+_SIGNATURES["experts_product_preview"] = [_i32, _u64, _u64, _u32, _u32, _u32, _i64, _i64, _u32,
+                                          ctypes.POINTER(Kernel)]
 _functions: dict = {}
 # 0.1 us; current_stream().cuda_stream takes 2.8. (A torch build for the host alone does not have it; no
 # tensor gets as far as a call there.)
@@ -313,6 +324,22 @@ def int8_matmul(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: torch.
           sx.data_ptr(), wq.data_ptr(), ldw, stride, sw.data_ptr(), offsets, order, pairs, top_k,
           experts, n, k, _DTYPES[out_dtype])
     return y
+
+
+def preview(product: str, rows: int, experts: int, n: int, k: int, x_rows: int = 0,
+            lda: int | None = None, ldb: int | None = None, alignment: int = 16) -> Kernel:
+    """The kernel that ``product`` (a key of PRODUCTS) takes for ``rows`` sorted pairs and weights
+    [experts, n, k] (experts 0: the dense 8-bit product); ``x_rows``: rows of a gathered x. Needs
+    no GPU. The leading dimensions default to those of contiguous operands."""
+    kernel = Kernel()
+    first = n if product in ("matmul_dx", "matmul_dw") else k
+    _library()
+    status = _functions["experts_product_preview"](
+        PRODUCTS[product], rows, x_rows, experts, n, k, first if lda is None else lda,
+        k if ldb is None else ldb, alignment, ctypes.byref(kernel))
+    if status:
+        raise hist.HistError(status, "experts_product_preview")
+    return kernel
 
 
 def _plain_rows(t: torch.Tensor) -> torch.Tensor:
