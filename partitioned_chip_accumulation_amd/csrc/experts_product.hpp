@@ -70,29 +70,33 @@ __device__ __forceinline__ void store_part(char *lds, O *out, int64_t ld_bytes, 
     }
 }
 
-// A scale of the 8-bit product, as a fraction of [0.5, 1) and a power of two (zero, infinity and NaN
-// are their own fractions). A whole-number sum times a row's scale can pass the range of 32 bits where
-// the column's scale would bring it back (a row with 3e38 in it), so the fractions are multiplied
-// first, which rounds as the scales would, and the powers come last.
-struct Scale {
-    float part;
-    int power;
-    static __device__ __forceinline__ Scale of(float s)
+// A row's scale of the 8-bit product. A whole-number sum times the scale can pass the range of 32 bits
+// where the column's scale would bring it back (a row with 3e38 in it), so a large scale is taken 2^64
+// times smaller, and the result 2^64 times larger again. Both are exact, and nothing between them is too
+// small: sum * scale is 2^32 or more (or 0), times the least column's scale 2^-117.
+struct RowScale {
+    float by, back;
+    static __device__ __forceinline__ RowScale of(float s)
     {
-        return {__builtin_amdgcn_frexp_mantf(s), __builtin_amdgcn_frexp_expf(s)};
+        const bool large = fabsf(s) >= 0x1p96f;
+        return {large ? s * 0x1p-64f : s, large ? 0x1p64f : 1.f};
+    }
+    __device__ __forceinline__ float operator()(int32_t sum, float column) const
+    {
+        return (float)sum * by * column * back;
     }
 };
 
 // The widest reduction, EXPERTS_MAX_WIDTH products of -128 and -128, sums to 2^31 and wraps to
-// -2^31, which is no other sum: the least real one is 2^17 * -128 * 127.
-__device__ __forceinline__ float scaled(int32_t sum, const Scale &a, const Scale &b)
+// -2^31, which is no other sum: the least real one is 2^17 * -128 * 127. 2^31 - 1 becomes 2^31 as a float.
+__device__ __forceinline__ void unwrap(s32x4 &sums)
 {
-    const float f = (float)sum, s = sum == INT32_MIN ? -f : f;
-    return __builtin_amdgcn_ldexpf(s * a.part * b.part, a.power + b.power);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sums[q] = sums[q] == INT32_MIN ? INT32_MAX : sums[q];
 }
 
 __device__ __forceinline__ f32x4 plus(f32x4 a, f32x4 b) { return a + b; }
-__device__ __forceinline__ s32x4 plus(s32x4 a, s32x4 b)  // wraps, see scaled()
+__device__ __forceinline__ s32x4 plus(s32x4 a, s32x4 b)  // wraps, see unwrap()
 {
     return __builtin_bit_cast(s32x4,
                               __builtin_bit_cast(u32x4, a) + __builtin_bit_cast(u32x4, b));
@@ -101,13 +105,14 @@ __device__ __forceinline__ s32x4 plus(s32x4 a, s32x4 b)  // wraps, see scaled()
 // The part of a product of rows: `real` is false for rows past the last kept one.
 template <class T, class O, int FM, int FN, class Acc>
 __device__ __forceinline__ void store_rows(const RowsArgs &g, char *lds, const Tile &t,
-                                           const Acc (&acc)[FM][FN], bool real, uint32_t row,
+                                           Acc (&acc)[FM][FN], bool real, uint32_t row,
                                            uint32_t col, int high, int wide)
 {
     O *out = (O *)(g.out + (int64_t)row * g.ldo) + col;
     if constexpr (sizeof(T) == 1) {
         const uint32_t lane = threadIdx.x % 64;
-        Scale sb[FN][4] = {}, sa[FM] = {};
+        f32x4 sb[FN] = {};
+        RowScale sa[FM] = {};
         if (real) {
             const float *from = g.sb + (uint64_t)t.group * g.cols + col;
 #pragma unroll
@@ -115,18 +120,23 @@ __device__ __forceinline__ void store_rows(const RowsArgs &g, char *lds, const T
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int c = j * 16 + lane / 16 * 4 + q;
-                    sb[j][q] = Scale::of(c < wide ? from[c] : 0.f);
+                    sb[j][q] = c < wide ? from[c] : 0.f;
                 }
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
                 const int r = i * 16 + lane % 16;
-                sa[i] = Scale::of(r < high ? g.sa[source_row(g, row + r)] : 0.f);
+                sa[i] = RowScale::of(r < high ? g.sa[source_row(g, row + r)] : 0.f);
             }
         }
+        if (g.bytes == EXPERTS_MAX_WIDTH)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FN; ++j) unwrap(acc[i][j]);
         store_part<O, FM, FN>(lds, out, g.ldo, high, wide, [&](int i, int j) {
             f32x4 v;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] = scaled(acc[i][j][q], sa[i], sb[j][q]);
+            for (int q = 0; q < 4; ++q) v[q] = sa[i](acc[i][j][q], sb[j][q]);
             return v;
         });
     } else {
@@ -853,12 +863,12 @@ __global__ void __launch_bounds__(256) k_rows_thin(RowsArgs g)
         typedef O O4 __attribute__((ext_vector_type(4)));
         float v[4];
         if constexpr (sizeof(T) == 1) {
-            const Scale sa = Scale::of(real ? g.sa[source_row(g, m0 + r)] : 0.f);
+            const RowScale sa = RowScale::of(real ? g.sa[source_row(g, m0 + r)] : 0.f);
+            if (g.bytes == EXPERTS_MAX_WIDTH) unwrap(s);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 v[q] = real && q < left
-                           ? scaled(s[q], sa,
-                                    Scale::of(g.sb[(uint64_t)t.group * g.cols + n0 + c + q]))
+                           ? sa(s[q], g.sb[(uint64_t)t.group * g.cols + n0 + c + q])
                            : 0.f;
         } else {
 #pragma unroll
