@@ -25,7 +25,7 @@
  * Types: 16-bit elements are EXPERTS_BF16 or EXPERTS_FP16; sums are held in 32
  * bits and rounded once, to nearest even, when the result is stored. (The 8-bit
  * product's are whole numbers; as 32-bit floats they are multiplied by the two
- * scales, three roundings of 2^-24, before that.) Leading dimensions (ld*) are in elements, rows have
+ * scales, three roundings of 2^-24 each, before that.) Leading dimensions (ld*) are in elements, rows have
  * unit stride; any alignment of the element type works (rows of 16-byte
  * aligned addresses and leading dimensions load fastest).
  *

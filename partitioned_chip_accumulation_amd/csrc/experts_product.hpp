@@ -437,9 +437,9 @@ struct DwParts {
 };
 
 // Rows times their experts' weights, or the gradient of the rows. Bound by the matrix cores
-// where groups are long: 32768 pairs, 4096 x 4096, bf16 in 256 x 256 tiles take 880 us, 1.25
+// where groups are long: 32768 pairs, 4096 x 4096, bf16 in 256 x 256 tiles take 880-925 us, 1.19 to 1.25
 // PFLOP/s, with the matrix cores busy 70% of the cycles (a dense product of the
-// same rows 810 us; the library's reaches 1.6 PFLOP/s); by reading the weights where they are short
+// same rows 824 us, the library's 735); by reading the weights where they are short
 // (launch_rows has the figures).
 // T: element of the operands; O: of the result; ACROSS: the weights lie across the
 // reduction; DIRECT: every row at a multiple of 16 bytes, and all rows that a tile can take within
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(S::THREADS)
 }
 
 // The gradient of the weights: a tile of one expert's, its rows the reduction. 16384 pairs of 32
-// skewed experts, 2560 x 2048, fp16: 265 us, 0.64 PFLOP/s and 1.7 TB/s; the steps are few (8 of 64 rows
+// skewed experts, 2560 x 2048, fp16: 264-287 us, 0.60 to 0.64 PFLOP/s and 1.6-1.7 TB/s; the steps are few (8 of 64 rows
 // on average), so the time is half tile starts and the 128 KiB that each tile stores; with 2048 rows
 // an expert it reaches 1.02 PFLOP/s.
 template <class T, class S, bool DIRECT>
@@ -997,7 +997,8 @@ RowsKernel rows_kernel(const RowsArgs &g)
         // A few tiles more than the 512 that run at one time take as long as a round of them (the
         // count is an estimate, hence 528): large tiles, if one round of those fills most CUs. 16
         // experts, 175 rows each, 2688 x 4096: 111 us, with small tiles 147; 32 experts, 138 rows
-        // each, 1344 x 2048: 60 and 75 us, but with 128 rows each, in one round, 59 and 53.
+        // each, 1344 x 2048: 60 and 75 us, but with 128 rows each, in one round, 59 and 53. (The host
+        // does not know the routing, so sizes near the edge fall on either side of a round.)
         if (each >= 80 && small > 528 && small % 512 < 128 && large >= 160 && large <= 256 && !brief)
             return K::k256x256;
         if (each >= 80 && small >= 256) return K::k128x128;
@@ -1099,7 +1100,8 @@ inline DwKernel dw_kernel(const DwArgs &g)
     };
     if (aligned16(g.dy, g.lddy) && aligned16(g.x, g.ldx) && g.n % 8 == 0 && g.k % 8 == 0 &&
         near(64, g.lddy) && near(g.x_rows, g.ldx)) {
-        // Large tiles, if they are enough for most of 256 CUs and not much larger than the weight (32
+        // Large tiles, if they are enough for most of 256 CUs and not much larger than the weight,
+        // whatever the rows an expert, for which there are no measurements (32
         // experts, 1024 rows each, 528 x 288: 53 us, in small ones 34; 1024 x 1024: 98 and 111).
         const uint64_t area = tiles(256, 256) * 256 * 256;
         return tiles(256, 256) >= 176 && area * 4 <= tiles(128, 128) * 128 * 128 * 5 ? K::k256x256

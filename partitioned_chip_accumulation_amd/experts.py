@@ -383,6 +383,9 @@ class _Linear(torch.autograd.Function):
         if ctx.needs_input_grad[0]:
             dx = matmul_dx(dy, w, g)
             if ctx.gather:
+                # Each pair's row is rounded to 16 bits before the sum over a token's pairs, whose
+                # sums are 32-bit and rounded once more: rows of 32 bits would be twice the bytes to
+                # write and to read again.
                 dx = combine(dx, g)
             dx = _first_order(dx, dy, w)
         if ctx.needs_input_grad[1]:
@@ -409,7 +412,8 @@ class _Merge(torch.autograd.Function):
 
 
 def linear(x: torch.Tensor, w: torch.Tensor, g: Groups, gather: bool = False) -> torch.Tensor:
-    """``matmul`` with gradients for x and w."""
+    """``matmul`` with gradients for x and w. With ``gather``, x's gradient is the sum of its pairs'
+    16-bit gradients: off by half a step of each of them, at most, and half a step of the sum."""
     return _Linear.apply(x, w, gather, *g)
 
 
