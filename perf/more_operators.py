@@ -15,6 +15,7 @@
 The 4-bit form: a block's power of two is 2^(floor(log2 max |x|) - 2), and each value of it, divided by
 that, the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with its sign, ties to the even code, beyond 6 it is 6.
 Two values share a byte, the first one in its lower half; a power of two is a byte, its exponent plus 127.
+A row's powers of two start at a multiple of 16 bytes.
 
 A pair whose expert id lies outside [0, experts) is dropped: it adds nothing. ``own`` selects between
 the plain form below and the library's calls.
@@ -174,10 +175,11 @@ def _stack(case, g, kind, rows, k):
         scale = torch.rand(*shape[:-1], generator=g, device="cuda") + 0.5
         return q, scale / (40 * k ** 0.5)
     if kind == "mx4":
-        if not case["experts"]:
-            return _quantized_mx4(normal(*shape) * k ** -0.5)[1:]
-        each = [_quantized_mx4(normal(rows, k) * k ** -0.5)[1:] for _ in range(shape[0])]
-        return tuple(torch.stack(t) for t in zip(*each))
+        each = [_quantized_mx4(normal(rows, k) * k ** -0.5)[1:]
+                for _ in range(max(1, case["experts"]))]
+        codes, powers = (torch.stack(t) if case["experts"] else t[0] for t in zip(*each))
+        blocks = powers.shape[-1]
+        return codes, torch.nn.functional.pad(powers, (0, -blocks % 16))[..., :blocks]
     return (normal(*shape) * k ** -0.5).to(DTYPES[case["dtype"]])
 
 
