@@ -15,6 +15,13 @@
  *   experts_quantize_rows   8-bit rows with one scale each
  *   experts_int8_matmul     the product of 8-bit rows and 8-bit weights, by
  *                           expert or dense
+ *   experts_quantize_mx4    4-bit rows, a power of two for 32 values
+ *   experts_mx4_matmul      the product of 4-bit rows and 4-bit weights, by
+ *                           expert or dense
+ *   experts_rms_norm        the norm before the layer, with the residual's
+ *                           addition, in 16 bits or (experts_rms_norm_int8) in
+ *                           8 as experts_int8_matmul takes them
+ *   experts_rms_norm_backward  its gradients
  *
  * Pairs are numbered twice: i in the order of the tokens, p in the order of
  * the experts. order[p] = i and place[i] = p. A pair whose id lies outside
@@ -126,11 +133,69 @@ hist_status_t experts_int8_matmul(void *y, int64_t ldy, const int8_t *xq, int64_
                                   uint32_t experts, uint32_t n, uint32_t k, int32_t dtype,
                                   hipStream_t stream);
 
+/* 4-bit rows: blocks of 32 values with a power of two each, ceil(k / 32) blocks
+ * a row. A block's power is 2^(floor(log2 max |x|) - 2), at least 2^-127,
+ * stored as the exponent plus 127 in a byte of xs [rows][blocks]. A value is x
+ * divided by it, to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4 and 6 with its sign
+ * (ties to the even code, beyond 6 it is 6): a 4-bit code of one sign, two
+ * exponent and one fraction bit. xq [rows][16 blocks] holds two codes a byte,
+ * the first one in the lower half; past k they are 0. A block with an infinity
+ * or a NaN has power 255 and codes 0, and its products are NaN. */
+hist_status_t experts_quantize_mx4(uint8_t *xq, int64_t ldq, uint8_t *xs, int64_t ldxs,
+                                   const void *x, int64_t ldx, uint64_t rows, uint32_t k,
+                                   int32_t dtype, hipStream_t stream);
+
+/* y [rows][n] = xq wq^T, each value times its block's power. wq [experts][n][16
+ * blocks] and ws [experts][n][blocks] (w_stride and ws_stride bytes from one
+ * expert to the next); all leading dimensions but ldy in bytes. offsets, order
+ * and the rows of xq and xs as in experts_int8_matmul. The products are exact,
+ * sums are held in 32 bits. Powers whose rows start at multiples of 4 bytes load
+ * fastest. */
+hist_status_t experts_mx4_matmul(void *y, int64_t ldy, const uint8_t *xq, int64_t ldq,
+                                 const uint8_t *xs, int64_t ldxs, uint64_t x_rows,
+                                 const uint8_t *wq, int64_t ldw, int64_t w_stride,
+                                 const uint8_t *ws, int64_t ldws, int64_t ws_stride,
+                                 const int32_t *offsets, const int32_t *order, uint64_t rows,
+                                 uint32_t top_k, uint32_t experts, uint32_t n, uint32_t blocks,
+                                 int32_t dtype, hipStream_t stream);
+
+/* h = x + residual, rounded to the type (residual NULL: h is x, and the argument
+ * h is not used), and y = h (mean h^2 + eps)^-1/2 weight, row by row, in 32 bits
+ * and rounded once. x, residual, h, y [rows][n], weight [n]. eps: 1e-30 or
+ * more. */
+hist_status_t experts_rms_norm(void *y, int64_t ldy, void *h, int64_t ldh, const void *x,
+                               int64_t ldx, const void *residual, int64_t ldr,
+                               const void *weight, uint64_t rows, uint32_t n, float eps,
+                               int32_t dtype, hipStream_t stream);
+
+/* The same with y as 32-bit values rounded to 8 bits: sx[r] = max |y[r]| / 127,
+ * xq[r] = y[r] / sx[r] to the nearest whole number. Rows of zeros, infinities
+ * and NaN as in experts_quantize_rows. */
+hist_status_t experts_rms_norm_int8(int8_t *xq, int64_t ldq, float *sx, void *h, int64_t ldh,
+                                    const void *x, int64_t ldx, const void *residual,
+                                    int64_t ldr, const void *weight, uint64_t rows, uint32_t n,
+                                    float eps, int32_t dtype, hipStream_t stream);
+
+/* Bytes of workspace experts_rms_norm_backward needs. */
+hist_status_t experts_rms_norm_backward_workspace_size(uint64_t rows, uint32_t n,
+                                                       uint64_t *bytes);
+
+/* dx [rows][n], the gradient of x and of the residual alike, and dweight [n],
+ * from dy, the gradient of y, and dh, that of h beyond its part in y (NULL:
+ * none). Sums in 32 bits and in a fixed order, rounded once. workspace: 16-byte
+ * aligned, not read before it is written. */
+hist_status_t experts_rms_norm_backward(void *dx, int64_t lddx, void *dweight, const void *dy,
+                                        int64_t lddy, const void *h, int64_t ldh, const void *dh,
+                                        int64_t lddh, const void *weight, uint64_t rows,
+                                        uint32_t n, float eps, int32_t dtype, void *workspace,
+                                        uint64_t workspace_bytes, hipStream_t stream);
+
 typedef enum {
     EXPERTS_MATMUL = 0,
     EXPERTS_MATMUL_DX = 1,
     EXPERTS_MATMUL_DW = 2,
-    EXPERTS_INT8_MATMUL = 3
+    EXPERTS_INT8_MATMUL = 3,
+    EXPERTS_MX4_MATMUL = 4
 } experts_product_t;
 
 typedef struct {
@@ -144,8 +209,10 @@ typedef struct {
 
 /* The kernel that a product of these sizes takes, computed on the host with no
  * device present, for tests of the rules. x_rows: rows of a gathered x, 0 if
- * order is NULL. experts 0: the dense 8-bit product. lda, ldb: the leading
- * dimensions of x and w (matmul, int8_matmul), dy and w (dx), dy and x (dw).
+ * order is NULL. experts 0: the dense 8-bit or 4-bit product. lda, ldb: the leading
+ * dimensions of x and w (matmul, int8_matmul), dy and w (dx), dy and x (dw), in
+ * elements; of the codes in bytes (mx4_matmul, whose powers of two start each row
+ * at a multiple of 16 bytes from the first one). k: elements.
  * alignment: of the operands' addresses in bytes, a power of two; the experts'
  * weights follow one another. rows must be positive. */
 hist_status_t experts_product_preview(int32_t product, uint64_t rows, uint64_t x_rows,

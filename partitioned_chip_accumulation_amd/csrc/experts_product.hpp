@@ -4,7 +4,7 @@
 
 #include "experts_tile.hpp"
 
-#include <type_traits>
+#include <cstddef>
 
 namespace pca_experts {
 
@@ -24,6 +24,8 @@ struct RowsArgs {
     uint32_t bytes;  // of the reduction
     uint32_t n_tiles, span;
     Divide divide;  // by top_k
+    const uint8_t *pa = nullptr, *pb = nullptr;  // 4-bit operands' powers of two
+    int64_t ldpa = 0, ldpb = 0, pb_stride = 0;
 };
 
 // The row of a that sorted row p reads; a bad index reads row 0 (the row's
@@ -109,7 +111,7 @@ __device__ __forceinline__ void store_rows(const RowsArgs &g, char *lds, const T
                                            uint32_t col, int high, int wide)
 {
     O *out = (O *)(g.out + (int64_t)row * g.ldo) + col;
-    if constexpr (sizeof(T) == 1) {
+    if constexpr (std::is_same<T, int8_t>::value) {
         const uint32_t lane = threadIdx.x % 64;
         f32x4 sb[FN] = {};
         RowScale sa[FM] = {};
@@ -174,7 +176,8 @@ extern __shared__ __align__(16) char pipe_lds[];
 // (fast: a whole one, of which there are `whole`; parity: the step's). Where it is not
 // DIRECT, it puts the piece, which is in registers by then, and fetches that of two steps later,
 // and first(parity, i) fetches those of steps 0 and 1.
-// frag_a and frag_b read the fragments of half a step.
+// frag_a and frag_b read the fragments of half a step, power_a and power_b (4-bit operands) the powers of
+// two of four of them.
 //
 // A step is two halves. At its top the first half's fragments are in registers (or
 // on their way), and the next step's pieces are. While the first half is multiplied
@@ -183,19 +186,22 @@ extern __shared__ __align__(16) char pipe_lds[];
 // first fragments are read. So there is one barrier a step, loads have a step to
 // arrive, and all reads and loads are issued between products.
 template <class T, class S, bool DIRECT, int LOADS, uint32_t STAGE, class F, class L, class FA,
-          class FB>
+          class FB, class PA, class PB>
 __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
                                           typename Mma<T>::Acc (&acc)[S::FM][S::FN], F first, L load,
-                                          FA frag_a, FB frag_b)
+                                          FA frag_a, FB frag_b, PA power_a, PB power_b)
 {
     constexpr int FM = S::FM, FN = S::FN;
     constexpr int N = S::STAGES;
     static_assert(DIRECT || N == 2, "pieces in registers alternate");
     constexpr uint32_t kAhead = DIRECT ? N : 4;  // steps from a step to what it fetches
+    constexpr bool kPowers = std::is_same<T, Mx4>::value;
+    constexpr int kPowersA = (FM + 3) / 4, kPowersB = (FN + 3) / 4;  // registers
     struct Frags {
         typename Mma<T>::Frag a[FM], b[FN];
+        uint32_t pa[kPowersA], pb[kPowersB];
     };
-    constexpr int kReads = FM + FN;
+    constexpr int kReads = FM + FN + (kPowers ? kPowersA + kPowersB : 0);
     constexpr int kParts = FM * 3 / 4 > 0 ? FM * 3 / 4 : 1;
     // reads after a product, over the first three quarters of the rows; loads over all of them
     constexpr int kSlots = kParts * FN, kReadsEach = (kReads + kSlots - 1) / kSlots;
@@ -204,7 +210,12 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
     constexpr int kLoadGap = FM * FN / LOADS > 0 ? FM * FN / LOADS : 1;
     auto read = [&](const char *lds, Frags &f, int kk, int r) {
         if (r < FN) f.b[r] = frag_b(lds, r, kk);
-        else f.a[r - FN] = frag_a(lds, r - FN, kk);
+        else if (r < FN + FM) f.a[r - FN] = frag_a(lds, r - FN, kk);
+        else if constexpr (kPowers) {
+            r -= FN + FM;
+            if (r < kPowersB) f.pb[r] = power_b(lds, r, kk);
+            else f.pa[r - kPowersB] = power_a(lds, r - kPowersB, kk);
+        }
     };
     auto half = [&](auto with_loads, auto fast, auto stage, const Frags &now, Frags &then,
                     const char *lds, int kk, uint32_t step, uint32_t to) {
@@ -212,7 +223,11 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
         for (int i = 0; i < FM; ++i) {
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                acc[i][j] = Mma<T>::run(now.b[j], now.a[i], acc[i][j]);
+                if constexpr (kPowers)
+                    Mma<T>::add(now.b[j], now.a[i], acc[i][j], now.pb[j / 4], now.pa[i / 4],
+                                j % 4, i % 4);
+                else
+                    acc[i][j] = Mma<T>::run(now.b[j], now.a[i], acc[i][j]);
                 const int slot = i * FN + j;
                 if (slot % kReadGap == 0)
 #pragma unroll
@@ -261,9 +276,8 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
     if constexpr (DIRECT) {
         if (steps >= N) wait_loads<LOADS *(N - 1)>();
         else wait_loads<0>();
-    } else {
-        __builtin_amdgcn_s_waitcnt(0xc07f);
     }
+    if constexpr (!DIRECT || kPowers) __builtin_amdgcn_s_waitcnt(0xc07f);  // what it put there itself
     block_barrier();
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(pipe_lds, f[0], 0, r);
@@ -284,21 +298,25 @@ __device__ __forceinline__ void run_steps(uint32_t steps, uint32_t whole,
         if constexpr (N > 3)
             if (k + 3 < steps) step(std::false_type(), Fourth(), k + 3);
     }
+    if constexpr (kPowers) sums_done(acc);
     block_barrier();
 }
 
 // The same where two sets of fragments do not fit beside the sums, as with two
-// operands across the reduction: a fragment of A takes the registers of the one that has just
+// operands across the reduction, or with the powers of two of 4-bit ones in the largest tiles: a fragment of A takes the registers of the one that has just
 // been used up (those of B alternate), so the reads of the second half end with the first
 // half's products, and the barrier comes a few rows of products into the second. look(step)
 // asks for what the loads of that step need (row numbers), turn(step) makes addresses of it.
 template <class T, class S, bool DIRECT, int LOADS, uint32_t STAGE, class F, class L, class FA,
-          class FB, class K, class U>
+          class FB, class K, class U, class PA = std::nullptr_t, class PB = std::nullptr_t>
 __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole,
                                           typename Mma<T>::Acc (&acc)[S::FM][S::FN], F first, L load,
-                                          FA frag_a, FB frag_b, K look, U turn)
+                                          FA frag_a, FB frag_b, K look, U turn,
+                                          PA power_a = PA(), PB power_b = PB())
 {
     constexpr int FM = S::FM, FN = S::FN;
+    constexpr bool kPowers = std::is_same<T, Mx4>::value;
+    constexpr int kPowersA = (FM + 3) / 4, kPowersB = (FN + 3) / 4;  // registers
     constexpr uint32_t kAhead = DIRECT ? 2 : 4;  // steps from a step to what it fetches
     constexpr int kWait = FM / 4;  // rows of the second half before the barrier
     constexpr int kReads = (FM + FN + FM - kWait - 1) / (FM - kWait);
@@ -313,25 +331,40 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
     }();
     static_assert(kUsedUp, "reads that are not ahead of the products");
     typename Mma<T>::Frag a[FM], b[2][FN];
+    uint32_t pa[2][kPowersA], pb[2][kPowersB];
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)pipe_lds;
-    auto products = [&](int i, const typename Mma<T>::Frag (&with)[FN]) {
+    auto products = [&](int i, int half) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) Mma<T>::add(with[j], a[i], acc[i][j]);
+        for (int j = 0; j < FN; ++j) {
+            if constexpr (kPowers)
+                Mma<T>::add(b[half][j], a[i], acc[i][j], pb[half][j / 4], pa[half][i / 4], j % 4,
+                            i % 4);
+            else
+                Mma<T>::add(b[half][j], a[i], acc[i][j]);
+        }
         __builtin_amdgcn_sched_barrier(0);
+    };
+    // the powers of two of half a step, i of them at a time
+    auto powers = [&](const char *lds, int i, int half) {
+        if constexpr (kPowers) {
+            if (i < kPowersA) pa[half][i] = power_a(lds, i, half);
+            if (i < kPowersB) pb[half][i] = power_b(lds, i, half);
+        }
     };
     auto step = [&](auto fast, auto stage, uint32_t k) {
         constexpr uint32_t kHere = decltype(stage)::value * STAGE;
         constexpr uint32_t kThere = STAGE - kHere;
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
-            products(i, b[0]);
+            products(i, 0);
             if (i < FN) b[1][i] = frag_b(pipe_lds + kHere, i, 1);
             a[i] = frag_a(pipe_lds + kHere, i, 1);
+            powers(pipe_lds + kHere, i, 1);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
-            products(i, b[1]);
+            products(i, 1);
             if (i == kWait - 1) {
                 __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): this wave has left the stage
                 if constexpr (DIRECT) wait_loads<0>();
@@ -344,6 +377,7 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
                     if (r < FN) b[0][r] = frag_b(pipe_lds + kThere, r, 0);
                     else if (r < FM + FN) a[r - FN] = frag_a(pipe_lds + kThere, r - FN, 0);
                 }
+                powers(pipe_lds + kThere, i - kWait, 0);
 #pragma unroll
                 for (int p = (i - kWait) * kLoads; p < (i - kWait + 1) * kLoads; ++p)
                     if (p < LOADS) load(fast, stage, k + 2, base + kHere, p);
@@ -375,15 +409,17 @@ __device__ __forceinline__ void run_steps_sharing(uint32_t steps, uint32_t whole
     if constexpr (DIRECT) {
         if (steps > 1) wait_loads<LOADS>();
         else wait_loads<0>();
-    } else {
-        __builtin_amdgcn_s_waitcnt(0xc07f);
     }
+    if constexpr (!DIRECT || kPowers) __builtin_amdgcn_s_waitcnt(0xc07f);
     look(kAhead);
     block_barrier();
 #pragma unroll
     for (int j = 0; j < FN; ++j) b[0][j] = frag_b(pipe_lds, j, 0);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) a[i] = frag_a(pipe_lds, i, 0);
+    for (int i = 0; i < FM; ++i) {
+        a[i] = frag_a(pipe_lds, i, 0);
+        powers(pipe_lds, i, 0);
+    }
     uint32_t k = 0;
     for (; k + kAhead + 1 < whole; k += 2) {
         step(std::true_type(), Even(), k);
@@ -408,9 +444,11 @@ __device__ __forceinline__ void run_steps_idle(uint32_t steps, L load)
         for (int i = 0; i < LOADS; ++i) load(std::false_type(), Any(), s, base + s * STAGE, i);
     if (steps > 1) wait_loads<LOADS>();
     else wait_loads<0>();
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): powers of two that it put there itself
     block_barrier();
     for (uint32_t k = 0; k < steps; ++k) {
         wait_loads<0>();
+        __builtin_amdgcn_s_waitcnt(0xc07f);
         block_barrier();
 #pragma unroll
         for (int i = 0; i < LOADS; ++i)
@@ -426,7 +464,16 @@ struct RowsParts {
     typedef Along<T, S::BM, S::THREADS> A;
     typedef typename std::conditional<ACROSS, Across<T, S::BN, S::THREADS>,
                                       Along<T, S::BN, S::THREADS>>::type B;
-    static constexpr uint32_t STAGE = A::kBytes + B::kBytes;
+    // The powers of two of 4-bit operands: A's rows, in groups of 64, then B's, and B's last one
+    // again in what the waves' last loads have left.
+    static constexpr bool kPowers = std::is_same<T, Mx4>::value;
+    static constexpr int kWaves = S::THREADS / 64;
+    static constexpr uint32_t kPowerRows = (S::BM + 63) / 64 * 64;  // of A
+    static constexpr int kPowerLoads =
+        kPowers ? ((kPowerRows + S::BN) / 32 + kWaves - 1) / kWaves : 0;
+    static constexpr uint32_t kPowersAt = A::kBytes + B::kBytes;
+    static constexpr uint32_t STAGE = kPowersAt + kPowerLoads * kWaves * 256;
+    static constexpr int kLoads = A::kLoads + B::kLoads + kPowerLoads;
 };
 template <class T, class S>
 struct DwParts {
@@ -502,7 +549,44 @@ __global__ void __launch_bounds__(S::THREADS)
         auto fb = [&](const char *lds, int j, int kk) {
             return B::frag(lds + A::kBytes, wn, j, kk);
         };
+        // the powers of four fragments, or as many as there are
+        auto pa = [&](const char *lds, int i, int kk) {
+            return Powers::read<S::FM < 4 ? S::FM : 4>(lds + P::kPowersAt, wm + i * 64, kk);
+        };
+        auto pb = [&](const char *lds, int j, int kk) {
+            return Powers::read<S::FN < 4 ? S::FN : 4>(
+                lds + P::kPowersAt + P::kPowerRows * kStepPowers, wn + j * 64, kk);
+        };
         const uint32_t byte_a = A::byte(), byte_b = B::byte();
+        // This thread's powers of two of a step: four bytes of a row, two threads a row.
+        typedef typename std::conditional<DIRECT, uint32_t, int64_t>::type Ld;
+        Ld at_p[P::kPowerLoads + 1];
+        const uint32_t byte_p = Powers::half_of() * 4, blocks = g.bytes / 16;
+        const char *powers_a = (const char *)g.pa + (g.order ? 0 : (int64_t)m0 * g.ldpa);
+        const char *powers_b = (const char *)g.pb + (int64_t)t.group * g.pb_stride +
+                               (int64_t)n0 * g.ldpb;
+        auto powers_of = [&](int i) {  // the wave's
+            return (i * P::kWaves + wave) * 32 < P::kPowerRows ? powers_a : powers_b;
+        };
+        if constexpr (P::kPowers) {
+#pragma unroll
+            for (int i = 0; i < P::kPowerLoads; ++i) {
+                uint32_t r = Powers::row_of(i * P::kWaves + wave);
+                if ((i * P::kWaves + wave) * 32 < P::kPowerRows) {
+                    r = r < high ? r : high - 1;
+                    at_p[i] = (g.order ? source_row(g, m0 + r) : r) * (Ld)g.ldpa + byte_p;
+                } else {
+                    r -= P::kPowerRows;
+                    at_p[i] = (r < wide ? r : wide - 1) * (Ld)g.ldpb + byte_p;
+                }
+            }
+        }
+        // The four bytes at a row's end, of which `left` (1 to 3) are its own; the others read 0.
+        auto last_powers = [&](const char *p, int left) {
+            const uint8_t *q = (const uint8_t *)p;
+            const uint32_t v = q[0], second = q[left > 1], third = q[left > 2 ? 2 : 0];
+            return v | (left > 1 ? second << 8 : 0) | (left > 2 ? third << 16 : 0);
+        };
         if constexpr (DIRECT) {
             uint32_t at_a[A::kLoads], at_b[ACROSS ? 1 : B::kLoads];
 #pragma unroll
@@ -520,6 +604,26 @@ __global__ void __launch_bounds__(S::THREADS)
                 const char *base;
                 uint32_t at;
                 bool in = true;
+                if (P::kPowers && i >= A::kLoads + B::kLoads) {
+                    i -= A::kLoads + B::kLoads;
+                    lds += P::kPowersAt + (i * P::kWaves + wave) * 256;
+                    // (addresses computed ahead for every load did not fit beside the sums)
+                    if constexpr (!decltype(fast)::value) asm volatile("" : "+v"(at_p[i]));
+                    base = powers_of(i) + step * kStepPowers;
+                    if constexpr (decltype(fast)::value) {
+                        load4_to_lds(base, at_p[i], lds);
+                        return;
+                    }
+                    int left = (int)blocks - (int)(step * kStepPowers + byte_p);
+                    asm volatile("" : "+v"(left));
+                    // Of a wave's lanes one half has the row's last four bytes, if they are not whole,
+                    // so some lane always loads, and the count of the loads in flight stays true.
+                    if (left >= 4 || left <= 0)
+                        load4_to_lds(left > 0 ? base + at_p[i] : (const char *)&kZeros, lds);
+                    else
+                        put_in_lds(last_powers(base + at_p[i], left), lds);
+                    return;
+                }
                 if (i < A::kLoads) {
                     base = rows + from, at = at_a[i], lds += A::place_of(i, wave);
                     if constexpr (!decltype(fast)::value) in = from + byte_a < g.bytes;
@@ -536,17 +640,23 @@ __global__ void __launch_bounds__(S::THREADS)
                         if constexpr (!decltype(fast)::value) in = from + byte_b < g.bytes;
                     }
                 }
+                if constexpr (P::kPowers && !decltype(fast)::value) asm volatile("" : "+v"(at));
                 if constexpr (decltype(fast)::value) load_to_lds(base, at, lds);
                 else load_to_lds(in ? base + at : (const char *)&kZeros, lds);
             };
             if (S::BM == 256 && wm >= high)
-                run_steps_idle<A::kLoads + B::kLoads, P::STAGE>(steps, load);
+                run_steps_idle<P::kLoads, P::STAGE>(steps, load);
+            else if constexpr (P::kPowers && S::FM * S::FN >= 32)
+                run_steps_sharing<T, S, true, P::kLoads, P::STAGE>(
+                    steps, whole, acc, [](auto, int) {}, load, fa, fb, [](uint32_t) {},
+                    [](uint32_t) {}, pa, pb);
             else
-                run_steps<T, S, true, A::kLoads + B::kLoads, P::STAGE>(
-                    steps, whole, acc, [](auto, int) {}, load, fa, fb);
+                run_steps<T, S, true, P::kLoads, P::STAGE>(
+                    steps, whole, acc, [](auto, int) {}, load, fa, fb, pa, pb);
         } else {
             const char *from_a[A::kLoads], *from_b[ACROSS ? 1 : B::kLoads];
             u32x4 kept_a[2][A::kLoads], kept_b[2][B::kLoads];
+            uint32_t kept_p[2][P::kPowerLoads + 1];
 #pragma unroll
             for (int i = 0; i < A::kLoads; ++i) from_a[i] = rows + (int64_t)row_a(i) * g.lda + byte_a;
             if constexpr (ACROSS) {
@@ -563,7 +673,15 @@ __global__ void __launch_bounds__(S::THREADS)
                 if (!decltype(fast)::value && step >= steps) return;
                 const uint32_t from = step * kStepBytes;
                 const bool whole_step = decltype(fast)::value || step < whole;
-                if (i < A::kLoads) {
+                if (P::kPowers && i >= A::kLoads + B::kLoads) {
+                    i -= A::kLoads + B::kLoads;
+                    const char *p = powers_of(i) + step * kStepPowers + at_p[i];
+                    const int left = (int)blocks - (int)(step * kStepPowers + byte_p);
+                    uint32_t &to = kept_p[kTo][i];
+                    if (whole_step) to = load_any<uint32_t>(p);
+                    else if (left >= 4) to = load_any<uint32_t>(p);
+                    else to = left > 0 ? last_powers(p, left) : 0;
+                } else if (i < A::kLoads) {
                     if (whole_step) kept_a[kTo][i] = load_any<u32x4>(from_a[i] + from);
                     else
                         kept_a[kTo][i] = load16<T>(
@@ -588,7 +706,11 @@ __global__ void __launch_bounds__(S::THREADS)
             };
             auto load = [&](auto fast, auto parity, uint32_t step, uint32_t lds, int i) {
                 if (!decltype(fast)::value && step >= steps) return;
-                if (i < A::kLoads) {
+                if (P::kPowers && i >= A::kLoads + B::kLoads) {
+                    const int j = i - A::kLoads - B::kLoads;
+                    put_in_lds(kept_p[decltype(parity)::value][j],
+                               lds + P::kPowersAt + (j * P::kWaves + wave) * 256);
+                } else if (i < A::kLoads) {
                     put_in_lds(kept_a[decltype(parity)::value][i], lds + A::place_of(i, wave));
                 } else {
                     const int j = i - A::kLoads;
@@ -604,11 +726,12 @@ __global__ void __launch_bounds__(S::THREADS)
                 fetch(std::false_type(), parity, decltype(parity)::value, i);
             };
             if constexpr (S::FM >= 4)
-                run_steps_sharing<T, S, false, A::kLoads + B::kLoads, P::STAGE>(
-                    steps, whole, acc, first, load, fa, fb, [](uint32_t) {}, [](uint32_t) {});
+                run_steps_sharing<T, S, false, P::kLoads, P::STAGE>(
+                    steps, whole, acc, first, load, fa, fb, [](uint32_t) {}, [](uint32_t) {}, pa,
+                    pb);
             else
-                run_steps<T, S, false, A::kLoads + B::kLoads, P::STAGE>(
-                    steps, whole, acc, first, load, fa, fb);
+                run_steps<T, S, false, P::kLoads, P::STAGE>(
+                    steps, whole, acc, first, load, fa, fb, pa, pb);
         }
     }
     store_rows<T, O>(g, pipe_lds + wave * (S::FM * S::FN * 512), t, acc, real, m0 + wm, n0 + wn,
@@ -793,8 +916,24 @@ __global__ void __launch_bounds__(256) k_rows_thin(RowsArgs g)
             b[j] = g.b + (int64_t)t.group * g.b_stride +
                    (int64_t)(n0 + (c < wide ? c : wide - 1)) * g.ldb + at;
         }
+        constexpr bool kPowers = std::is_same<T, Mx4>::value;
+        const uint8_t *pa[RM], *pb[FN];  // a row's eight powers of two go with a piece
+        if constexpr (kPowers) {
+#pragma unroll
+            for (int i = 0; i < RM; ++i) {
+                const uint32_t r = i * 16 + lane % 16;
+                pa[i] = g.pa + (int64_t)source_row(g, m0 + (r < high ? r : high - 1)) * g.ldpa;
+            }
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const uint32_t c = j * 16 + lane % 16;
+                pb[j] = g.pb + (int64_t)t.group * g.pb_stride +
+                        (int64_t)(n0 + (c < wide ? c : wide - 1)) * g.ldpb;
+            }
+        }
         struct Piece {
             u32x4 a[RM][2], b[FN][2];
+            uint32_t pa[kPowers ? RM : 1][2], pb[kPowers ? FN : 1][2];
         };
         // whole: the piece's 128 bytes lie in the rows
         auto fetch = [&](Piece &p, uint32_t from, auto whole) {
@@ -810,6 +949,18 @@ __global__ void __launch_bounds__(256) k_rows_thin(RowsArgs g)
                 for (int j = 0; j < FN; ++j) p.b[j][h] = one(b[j] + f);
 #pragma unroll
                 for (int i = 0; i < RM; ++i) p.a[i][h] = one(a[i] + f);
+                if constexpr (kPowers) {
+                    // this lane's block is number lane / 16 of four
+                    const uint32_t block = f / 16 + lane / 16;
+                    auto power = [&](const uint8_t *q) -> uint32_t {
+                        if constexpr (decltype(whole)::value) return q[block];
+                        else return left > 0 ? q[block] : 0;
+                    };
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) p.pb[j][h] = power(pb[j]);
+#pragma unroll
+                    for (int i = 0; i < RM; ++i) p.pa[i][h] = power(pa[i]);
+                }
             }
         };
         auto multiply = [&](const Piece &p) {
@@ -819,8 +970,14 @@ __global__ void __launch_bounds__(256) k_rows_thin(RowsArgs g)
                 for (int i = 0; i < RM; ++i)
 #pragma unroll
                     for (int j = 0; j < FN; ++j)
-                        acc[i][j] = Mma<T>::run(__builtin_bit_cast(Frag, p.b[j][h]),
-                                                __builtin_bit_cast(Frag, p.a[i][h]), acc[i][j]);
+                        if constexpr (kPowers)
+                            acc[i][j] = Mma<T>::run(__builtin_bit_cast(Frag, p.b[j][h]),
+                                                    __builtin_bit_cast(Frag, p.a[i][h]),
+                                                    acc[i][j], p.pb[j][h], p.pa[i][h]);
+                        else
+                            acc[i][j] = Mma<T>::run(__builtin_bit_cast(Frag, p.b[j][h]),
+                                                    __builtin_bit_cast(Frag, p.a[i][h]),
+                                                    acc[i][j]);
         };
         constexpr uint32_t kTurn = 4 * kStepBytes;
         uint32_t from = wave * kStepBytes;
@@ -862,7 +1019,7 @@ __global__ void __launch_bounds__(256) k_rows_thin(RowsArgs g)
         const int left = (int)(wide - c);
         typedef O O4 __attribute__((ext_vector_type(4)));
         float v[4];
-        if constexpr (sizeof(T) == 1) {
+        if constexpr (std::is_same<T, int8_t>::value) {
             const RowScale sa = RowScale::of(real ? g.sa[source_row(g, m0 + r)] : 0.f);
             if (g.bytes == EXPERTS_MAX_WIDTH) unwrap(s);
 #pragma unroll
@@ -984,7 +1141,10 @@ RowsKernel rows_kernel(const RowsArgs &g)
     }
     if (aligned16(g.a, g.lda) && aligned16(g.b, g.ldb) && g.b_stride % 16 == 0 &&
         g.bytes % 16 == 0 && (!ACROSS || g.cols % 8 == 0) &&
-        near(g.order ? g.a_rows : 256, g.lda) && near(256, g.ldb)) {
+        near(g.order ? g.a_rows : 256, g.lda) && near(256, g.ldb) &&
+        near(g.order ? g.a_rows : 256, g.ldpa) && near(256, g.ldpb) &&
+        !misaligned(g.pa, 4) && !misaligned(g.pb, 4) &&
+        ((g.ldpa | g.ldpb | g.pb_stride) & 3) == 0) {
         // a short reduction has no use for stages, but for workgroups beside it (16384 rows, 8 experts,
         // 256 -> 2048: 31 us in 128 x 128, 37 in 256 x 256; 1024 -> 2048: 78 and 80)
         const bool brief = g.bytes <= 8 * kStepBytes;
@@ -1020,7 +1180,8 @@ template <class S, bool DIRECT> struct Tiles {};
 template <int RM, int FN, int DEEP> struct Thin {};
 
 // Calls f with what the kernel is made for.
-template <bool ACROSS, class F>
+// POWERS: 4-bit operands, whose powers of two take another tenth of a stage.
+template <bool ACROSS, bool POWERS = false, class F>
 hist_status_t with_rows_kernel(RowsKernel kernel, const F &f)
 {
     typedef RowsKernel K;
@@ -1028,10 +1189,18 @@ hist_status_t with_rows_kernel(RowsKernel kernel, const F &f)
     // the rows has a stage, or a workgroup, less (32 experts, 2560 -> 2048: 2 to 32 rows an expert
     // 62-64 us, 5.2-5.4 TB/s of weights, 40 rows 78; a fourth stage, which leaves one workgroup on
     // a CU, 62-66 and 82; 1344 -> 2048: 33-34 and 34-36. 64 rows, 64 x 128: 67 us).
-    typedef typename std::conditional<ACROSS, Shape<32, 128, 2, 2, 2, 3>,
-                                      Shape<32, 128, 1, 4, 2, 4>>::type Lowest;
-    typedef typename std::conditional<ACROSS, Shape<32, 128, 2, 2, 3>,
-                                      Shape<32, 128, 1, 4, 4>>::type LowestShort;
+    typedef typename std::conditional<
+        ACROSS, Shape<32, 128, 2, 2, 2, 3>,
+        typename std::conditional<POWERS, Shape<32, 128, 1, 4, 2, 3>,
+                                  Shape<32, 128, 1, 4, 2, 4>>::type>::type Lowest;
+    // (through registers, with 4-bit operands, larger tiles or fewer waves do not fit the registers)
+    typedef typename std::conditional<POWERS, Shape<128, 128, 4, 2, 1>,
+                                      Shape<128, 128, 2, 2, 2>>::type Via128;
+    typedef typename std::conditional<POWERS, Via128, Shape<256, 128, 4, 2, 1>>::type Via256;
+    typedef typename std::conditional<
+        ACROSS, Shape<32, 128, 2, 2, 3>,
+        typename std::conditional<POWERS, Shape<32, 128, 1, 4, 3>,
+                                  Shape<32, 128, 1, 4, 4>>::type>::type LowestShort;
     switch (kernel) {
     case K::k256x256: return f(Tiles<Shape<256, 256, 2, 4, 1>, true>());
     case K::k128x256: return f(Tiles<Shape<128, 256, 2, 4, 1, 3>, true>());
@@ -1040,8 +1209,8 @@ hist_status_t with_rows_kernel(RowsKernel kernel, const F &f)
     case K::k64x128: return f(Tiles<Shape<64, 128, 2, 2, 2, 3>, true>());
     case K::k32x128: return f(Tiles<Lowest, true>());
     case K::k32x128Short: return f(Tiles<LowestShort, true>());
-    case K::kVia256x128: return f(Tiles<Shape<256, 128, 4, 2, 1>, false>());
-    case K::kVia128x128: return f(Tiles<Shape<128, 128, 2, 2, 2>, false>());
+    case K::kVia256x128: return f(Tiles<Via256, false>());
+    case K::kVia128x128: return f(Tiles<Via128, false>());
     default: break;
     }
     if constexpr (ACROSS) {
@@ -1075,7 +1244,8 @@ struct LaunchRows {
 template <class T, class O, bool ACROSS>
 hist_status_t launch_rows(const RowsArgs &g, hipStream_t stream)
 {
-    return with_rows_kernel<ACROSS>(rows_kernel<ACROSS>(g), LaunchRows<T, O, ACROSS>{g, stream});
+    return with_rows_kernel<ACROSS, std::is_same<T, Mx4>::value>(
+        rows_kernel<ACROSS>(g), LaunchRows<T, O, ACROSS>{g, stream});
 }
 
 template <class T, bool DIRECT, class S>

@@ -13,13 +13,20 @@
 //
 // The fragments go to the matrix instruction with B first, so that a lane
 // holds four consecutive columns n of one row m of the result.
+//
+// 4-bit operands (Mx4) lie along the reduction, two elements a byte, and are loaded and read like 8-bit
+// ones: a lane's 16 bytes are one block of 32 elements, which has a power of two of its own. Those
+// of a step, 8 bytes a row, follow the operands in LDS.
 #pragma once
 
 #include "experts_common.hpp"
 
+#include <type_traits>
+
 namespace pca_experts {
 
 constexpr uint32_t kStepBytes = 128;
+constexpr uint32_t kStepPowers = kStepBytes / 16;  // bytes of powers of two that go with them
 
 // What one matrix instruction takes and gives, by element type. add() keeps the sum
 // in its registers: the compiler's own form names other ones for the result, and in the
@@ -61,6 +68,51 @@ template <> struct Mma<int8_t> {
     static __device__ __forceinline__ void add(Frag a, Frag b, Acc &c)
     {
         asm("s_nop 1\n\tv_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+    }
+};
+
+struct Mx4 {
+    uint8_t two;
+};
+template <> struct Mma<Mx4> {
+    typedef s32x4 Frag;
+    typedef f32x4 Acc;
+    typedef int s32x8 __attribute__((ext_vector_type(8)));
+    // The lowest bytes of pa and pb: the exponents plus 127 (255: NaN) of the lane's blocks.
+    static __device__ __forceinline__ Acc run(Frag a, Frag b, Acc c, uint32_t pa, uint32_t pb)
+    {
+        const s32x8 x = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+        const s32x8 y = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
+        // (4: four bits, of one sign, two exponent and one fraction bit)
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, (int)pa, 0,
+                                                                (int)pb);
+    }
+    // The same with byte A of pa and byte B of pb.
+    template <int A, int B>
+    static __device__ __forceinline__ void add(Frag a, Frag b, Acc &c, uint32_t pa, uint32_t pb)
+    {
+        asm("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 "
+            "op_sel:[%5,%6,0] op_sel_hi:[%7,%8,0] cbsz:4 blgp:4"
+            : "+v"(c)
+            : "v"(a), "v"(b), "v"(pa), "v"(pb), "n"(A & 1), "n"(B & 1), "n"(A >> 1), "n"(B >> 1));
+    }
+    // With bytes that the compiler knows once it has unrolled the loops around.
+    template <int A>
+    static __device__ __forceinline__ void add(Frag a, Frag b, Acc &c, uint32_t pa, uint32_t pb,
+                                               int at_b)
+    {
+        if (at_b == 0) add<A, 0>(a, b, c, pa, pb);
+        else if (at_b == 1) add<A, 1>(a, b, c, pa, pb);
+        else if (at_b == 2) add<A, 2>(a, b, c, pa, pb);
+        else add<A, 3>(a, b, c, pa, pb);
+    }
+    static __device__ __forceinline__ void add(Frag a, Frag b, Acc &c, uint32_t pa, uint32_t pb,
+                                               int at_a, int at_b)
+    {
+        if (at_a == 0) add<0>(a, b, c, pa, pb, at_b);
+        else if (at_a == 1) add<1>(a, b, c, pa, pb, at_b);
+        else if (at_a == 2) add<2>(a, b, c, pa, pb, at_b);
+        else add<3>(a, b, c, pa, pb, at_b);
     }
 };
 
@@ -151,6 +203,39 @@ struct Along {
     }
 };
 
+// The powers of two of 4-bit operands in LDS: 8 bytes a row and step, four for each half. Those of
+// rows r, r + 16, r + 32 and r + 48 lie together, so that one read of a lane has what four
+// fragments need, and one register takes it. A load of a wave is 32 rows: its lane is four bytes of row
+// row_of(load), half half_of().
+struct Powers {
+    static __device__ __forceinline__ uint32_t row_of(uint32_t load)
+    {
+        const uint32_t lane = threadIdx.x % 64;
+        return load / 2 * 64 + lane % 4 * 16 + load % 2 * 8 + lane / 8;
+    }
+    static __device__ __forceinline__ uint32_t half_of() { return threadIdx.x / 4 % 2; }
+    // Byte i: the power of this lane's block of fragment i, N of them (1, 2 or 4) from row first on.
+    template <int N>
+    static __device__ __forceinline__ uint32_t read(const char *lds, uint32_t first, int kk)
+    {
+        const uint32_t lane = threadIdx.x % 64, at = lane / 16;
+        const char *p = lds + first / 64 * 512 + lane % 16 * 32 + kk * 16 + first / 16 % 4 * 4;
+        if constexpr (N == 1) {
+            return *(const uint32_t *)p >> at * 8;
+        } else if constexpr (N == 2) {
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            const u32x2 v = *(const u32x2 *)p;
+            return __builtin_amdgcn_perm(v[1], v[0], at | (at + 4) << 8);
+        } else {
+            const u32x4 v = *(const u32x4 *)p;
+            const uint32_t pick = at | (at + 4) << 8;
+            const uint32_t low = __builtin_amdgcn_perm(v[1], v[0], pick);
+            const uint32_t high = __builtin_amdgcn_perm(v[3], v[2], pick);
+            return __builtin_amdgcn_perm(high, low, 0x05040100);
+        }
+    }
+};
+
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
@@ -238,11 +323,26 @@ __device__ __forceinline__ void load_to_lds(const char *base, uint32_t offset, u
                  : "s"(lds), "v"(offset), "s"(base));
 }
 
-// The way through registers: a lane's piece to LDS.
-__device__ __forceinline__ void put_in_lds(u32x4 v, uint32_t lds)
+// Four bytes a lane, to LDS at lds + 4 * lane; of lanes that are not active, nothing.
+__device__ __forceinline__ void load4_to_lds(const char *p, uint32_t lds)
 {
-    typedef __attribute__((address_space(3))) u32x4 Piece;
-    *(Piece *)(uintptr_t)(lds + threadIdx.x % 64 * 16) = v;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+                 :
+                 : "s"(lds), "v"(p));
+}
+__device__ __forceinline__ void load4_to_lds(const char *base, uint32_t offset, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                 :
+                 : "s"(lds), "v"(offset), "s"(base));
+}
+
+// The way through registers: a lane's piece to LDS.
+template <class V>
+__device__ __forceinline__ void put_in_lds(V v, uint32_t lds)
+{
+    typedef __attribute__((address_space(3))) V Piece;
+    *(Piece *)(uintptr_t)(lds + threadIdx.x % 64 * sizeof(V)) = v;
 }
 
 // Until at most N of the wave's loads are in flight.

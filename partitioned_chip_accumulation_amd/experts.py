@@ -40,6 +40,7 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 _vp, _u32, _u64, _i32, _i64 = (ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int32,
                                ctypes.c_int64)
+_f32 = ctypes.c_float
 _SIGNATURES = {
     "experts_group_workspace_size": [_u64, _u32, _u32, ctypes.POINTER(_u64)],
     "experts_group": [_vp, _i32, _u64, _u32, _u32, _vp, _vp, _vp, _vp, _vp, _u64, _vp],
@@ -55,8 +56,18 @@ _SIGNATURES = {
     "experts_quantize_rows": [_vp, _i64, _vp, _vp, _i64, _u64, _u32, _i32, _vp],
     "experts_int8_matmul": [_vp, _i64, _vp, _i64, _u64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _u64,
                             _u32, _u32, _u32, _u32, _i32, _vp],
+    "experts_quantize_mx4": [_vp, _i64, _vp, _i64, _vp, _i64, _u64, _u32, _i32, _vp],
+    "experts_mx4_matmul": [_vp, _i64, _vp, _i64, _vp, _i64, _u64, _vp, _i64, _i64, _vp, _i64, _i64,
+                           _vp, _vp, _u64, _u32, _u32, _u32, _u32, _i32, _vp],
+    "experts_rms_norm": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _u64, _u32, _f32, _i32,
+                         _vp],
+    "experts_rms_norm_int8": [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _u64, _u32,
+                              _f32, _i32, _vp],
+    "experts_rms_norm_backward_workspace_size": [_u64, _u32, ctypes.POINTER(_u64)],
+    "experts_rms_norm_backward": [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _u64, _u32,
+                                  _f32, _i32, _vp, _u64, _vp],
 }
-PRODUCTS = {"matmul": 0, "matmul_dx": 1, "matmul_dw": 2, "int8_matmul": 3}
+PRODUCTS = {"matmul": 0, "matmul_dx": 1, "matmul_dw": 2, "int8_matmul": 3, "mx4_matmul": 4}
 
 
 class Kernel(ctypes.Structure):
@@ -326,17 +337,145 @@ def int8_matmul(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: torch.
     return y
 
 
+def _powers(s: torch.Tensor, q: torch.Tensor, name: str) -> int:
+    """Checks the powers of two of 4-bit rows and returns their leading dimension."""
+    ld = _matrix(s, name, (torch.uint8,), q.dim())
+    if s.device != q.device or s.shape[:-1] != q.shape[:-1] or s.shape[-1] * 16 != q.shape[-1]:
+        raise ValueError(f"{name} must have one byte for 16 of the codes, on their device")
+    return ld
+
+
+def quantize_mx4(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+    """4-bit rows: xq uint8 [rows, 16 blocks] and xs uint8 [rows, blocks] with blocks = ceil(k / 32).
+    A block of 32 values has a power of two, 2^(xs - 127) = 2^(floor(log2 max |x|) - 2), and each
+    value divided by it is the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with its sign (6 beyond that), two
+    of them a byte, the first one in the lower half, zeros past the row's end. xs' rows start at
+    multiples of 16 bytes (its stride can exceed its width)."""
+    ldx = _matrix(x, "x")
+    rows, k = x.shape
+    blocks = (k + 31) // 32
+    lds = (blocks + 15) // 16 * 16
+    xq = torch.empty(rows, 16 * blocks, dtype=torch.uint8, device=x.device)
+    xs = torch.empty(rows, lds, dtype=torch.uint8, device=x.device)
+    _call("experts_quantize_mx4", x.device, xq.data_ptr(), 16 * blocks, xs.data_ptr(), lds,
+          x.data_ptr(), ldx, rows, k, _DTYPES[x.dtype])
+    return xq, (xs if lds == blocks else xs[:, :blocks])
+
+
+def mx4_matmul(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.Tensor,
+               g: Groups | None = None, gather: bool = False,
+               out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The product of 4-bit rows and 4-bit weights, both as ``quantize_mx4`` makes them. Dense without
+    ``g``: wq is [n, 16 blocks], ws [n, blocks]. By expert with it: [experts, n, ...], and xq and xs
+    are per token with ``gather``, else per pair."""
+    if out_dtype not in _DTYPES:
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float16")
+    ldq = _matrix(xq, "xq", (torch.uint8,))
+    device, x_rows = xq.device, xq.shape[0]
+    ldxs = _powers(xs, xq, "xs")
+    if g is None:
+        if gather:
+            raise ValueError("gather needs the groups")
+        ldw, stride, ws_stride = _matrix(wq, "wq", (torch.uint8,)), 0, 0
+        if wq.device != device or wq.shape[0] == 0:
+            raise ValueError(f"wq must have rows and be on {device}")
+        experts, pairs, top_k, offsets, order = 1, x_rows, 1, None, None
+    else:
+        experts, pairs, top_k = _groups(g, device)
+        ldw, stride = _weights(wq, experts, device, torch.uint8)
+        ws_stride = ws.stride(0) if experts > 1 and ws.dim() == 3 else 0
+        _rows(xq, g, pairs, gather, "xq")
+        offsets, order = g.offsets.data_ptr(), g.order.data_ptr() if gather else None
+    ldws = _powers(ws, wq, "ws")
+    n = wq.shape[-2]
+    _same(xq.shape[1], wq.shape[-1], "the last dimensions of xq and wq")
+    y = torch.empty(pairs, n, dtype=out_dtype, device=device)
+    _call("experts_mx4_matmul", device, y.data_ptr(), n, xq.data_ptr(), ldq, xs.data_ptr(), ldxs,
+          x_rows, wq.data_ptr(), ldw, stride, ws.data_ptr(), ldws, ws_stride, offsets, order, pairs,
+          top_k, experts, n, xs.shape[1], _DTYPES[out_dtype])
+    return y
+
+
+def _norm_inputs(x: torch.Tensor, weight: torch.Tensor, other: torch.Tensor | None, name: str,
+                 eps: float) -> tuple[int, int]:
+    """Checks what the norm takes; the leading dimensions of x and of a second matrix like it."""
+    ldx = _matrix(x, "x" if name == "residual" else "dy")
+    _vector(weight, "weight", x.dtype, x.shape[1:], x.device)
+    if not 1e-30 <= eps < float("inf"):
+        raise ValueError("eps must be 1e-30 or more, and finite")
+    if other is None:
+        return ldx, 0
+    ld = _matrix(other, name, (x.dtype,))
+    if other.shape != x.shape or other.device != x.device:
+        raise ValueError(f"{name} must have the shape {tuple(x.shape)} and be on {x.device}")
+    return ldx, ld
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+             eps: float = 1e-6) -> tuple[torch.Tensor, torch.Tensor]:
+    """(y, h): h = x + residual in x's type (x itself without a residual), y = h / sqrt(mean h^2 + eps)
+    times weight, row by row. weight is [n], of x's type."""
+    ldx, ldr = _norm_inputs(x, weight, residual, "residual", eps)
+    rows, n = x.shape
+    y = torch.empty(rows, n, dtype=x.dtype, device=x.device)
+    h = x if residual is None else torch.empty(rows, n, dtype=x.dtype, device=x.device)
+    _call("experts_rms_norm", x.device, y.data_ptr(), n, h.data_ptr(), n, x.data_ptr(), ldx,
+          None if residual is None else residual.data_ptr(), ldr, weight.data_ptr(), rows, n, eps,
+          _DTYPES[x.dtype])
+    return y, h
+
+
+def rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                  eps: float = 1e-6) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(xq, sx, h): ``rms_norm`` with y in 8 bits and float32 scales of its rows, as ``int8_matmul``
+    takes them. y is not rounded to x's type before."""
+    ldx, ldr = _norm_inputs(x, weight, residual, "residual", eps)
+    rows, n = x.shape
+    ldq = (n + 15) // 16 * 16
+    xq = torch.empty(rows, ldq, dtype=torch.int8, device=x.device)
+    sx = torch.empty(rows, dtype=torch.float32, device=x.device)
+    h = x if residual is None else torch.empty(rows, n, dtype=x.dtype, device=x.device)
+    _call("experts_rms_norm_int8", x.device, xq.data_ptr(), ldq, sx.data_ptr(), h.data_ptr(), n,
+          x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
+          weight.data_ptr(), rows, n, eps, _DTYPES[x.dtype])
+    return (xq if ldq == n else xq[:, :n]), sx, h
+
+
+def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                      dh: torch.Tensor | None = None,
+                      eps: float = 1e-6) -> tuple[torch.Tensor, torch.Tensor]:
+    """``rms_norm``'s gradients from dy, its h and the gradient dh that h gets from elsewhere:
+    (dx, dweight). dx is the gradient of x and of the residual alike."""
+    lddy, ldh = _norm_inputs(dy, weight, h, "h", eps)
+    lddh = 0 if dh is None else _norm_inputs(dy, weight, dh, "dh", eps)[1]
+    rows, n = dy.shape
+    need = _u64()
+    _library()
+    status = _functions["experts_rms_norm_backward_workspace_size"](rows, n, ctypes.byref(need))
+    if status:
+        raise hist.HistError(status, "experts_rms_norm_backward_workspace_size")
+    dx = torch.empty(rows, n, dtype=dy.dtype, device=dy.device)
+    dweight = torch.empty(n, dtype=dy.dtype, device=dy.device)
+    work = torch.empty(need.value, dtype=torch.uint8, device=dy.device)
+    _call("experts_rms_norm_backward", dy.device, dx.data_ptr(), n, dweight.data_ptr(),
+          dy.data_ptr(), lddy, h.data_ptr(), ldh, None if dh is None else dh.data_ptr(), lddh,
+          weight.data_ptr(), rows, n, eps, _DTYPES[dy.dtype], work.data_ptr(), need.value)
+    return dx, dweight
+
+
 def preview(product: str, rows: int, experts: int, n: int, k: int, x_rows: int = 0,
             lda: int | None = None, ldb: int | None = None, alignment: int = 16) -> Kernel:
     """The kernel that ``product`` (a key of PRODUCTS) takes for ``rows`` sorted pairs and weights
-    [experts, n, k] (experts 0: the dense 8-bit product); ``x_rows``: rows of a gathered x. Needs
+    [experts, n, k] (experts 0: the dense 8-bit or 4-bit product); ``x_rows``: rows of a gathered x. Needs
     no GPU. The leading dimensions default to those of contiguous operands."""
     kernel = Kernel()
-    first = n if product in ("matmul_dx", "matmul_dw") else k
+    first, second = n if product in ("matmul_dx", "matmul_dw") else k, k
+    if product == "mx4_matmul":
+        first = second = (k + 31) // 32 * 16
     _library()
     status = _functions["experts_product_preview"](
         PRODUCTS[product], rows, x_rows, experts, n, k, first if lda is None else lda,
-        k if ldb is None else ldb, alignment, ctypes.byref(kernel))
+        second if ldb is None else ldb, alignment, ctypes.byref(kernel))
     if status:
         raise hist.HistError(status, "experts_product_preview")
     return kernel
@@ -356,8 +495,8 @@ class _FirstOrder(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, _):
-        raise RuntimeError("experts.linear and experts.merge have gradients of the first order "
-                           "only")
+        raise RuntimeError("experts.linear, experts.merge and experts.norm have gradients of the first "
+                           "order only")
 
 
 def _first_order(grad: torch.Tensor, *depends_on: torch.Tensor) -> torch.Tensor:
@@ -420,3 +559,34 @@ def linear(x: torch.Tensor, w: torch.Tensor, g: Groups, gather: bool = False) ->
 def merge(y: torch.Tensor, g: Groups, weights: torch.Tensor | None) -> torch.Tensor:
     """``combine`` with gradients for y and the weights (if there are any)."""
     return _Merge.apply(y, weights, *g)
+
+
+class _Norm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        y, h = rms_norm(x, weight, residual, eps)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(h, weight)
+        ctx.eps, ctx.added = eps, residual is not None
+        return (y, h) if ctx.added else y
+
+    @staticmethod
+    def backward(ctx, dy, dh=None):
+        h, weight = ctx.saved_tensors
+        if dy is None:  # only h was used, or nothing
+            return dh, None, dh if ctx.added else None, None
+        if dh is not None:
+            dh = _plain_rows(dh)
+        dx, dweight = rms_norm_backward(_plain_rows(dy), h, weight, dh, ctx.eps)
+        depends = [t for t in (dy, h, weight, dh) if t is not None]
+        dx, dweight = _first_order(dx, *depends), _first_order(dweight, *depends)
+        return dx, dweight, dx if ctx.added else None, None
+
+
+def norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+         eps: float = 1e-6) -> tuple[torch.Tensor, torch.Tensor]:
+    """``rms_norm`` with gradients for x, the weight and the residual. The gradient that h gets from
+    what follows is added to the norm's before the one rounding."""
+    if residual is None:
+        return _Norm.apply(x, weight, None, eps), x
+    return _Norm.apply(x, weight, residual, eps)

@@ -1,0 +1,230 @@
+"""4-bit rows and their product against their definitions (tolerances as in test_experts_gpu: products of
+two 4-bit values and their powers are exact in 32 bits)."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import mx4_reference
+from partitioned_chip_accumulation_amd import experts
+from test_experts_gpu import assert_close, groups, normal, product, route, spans, token_rows
+from test_experts_kernels_gpu import ROWS, names, pairs_of
+
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.bfloat16, torch.float16]
+
+# through registers: rows whose addresses are off 16 bytes, or powers off 4
+VIA = [
+    ("128 x 128", (1500, 2, 5601, 777), (128, 128, 2, 0), None),
+    ("128 x 128, ragged groups", (1000, 8, 4001, 777), (128, 128, 2, 0), None),
+    ("64 x 64", (200, 2, 2603, 781), (64, 64, 2, 0), None),
+]
+
+
+def expected(kernel):
+    """The kernel of the 4-bit product where the others take this one."""
+    return (32, 128, 3, 1) if kernel == (32, 128, 4, 1) else kernel
+
+
+def check_quantized(x):
+    xq, xs = experts.quantize_mx4(x)
+    codes, powers = mx4_reference.quantize(x.float().cpu().numpy())
+    assert xs.stride(0) % 16 == 0 or x.shape[0] == 1
+    assert np.array_equal(xs.cpu().numpy(), powers)
+    assert np.array_equal(xq.cpu().numpy(), codes)
+
+
+@pytest.mark.parametrize("rows,k", [(1, 1), (3, 31), (2, 32), (5, 33), (7, 100), (4, 2048),
+                                    (3, 2049), (2, 5000), (300, 77)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_quantize(rows, k, dtype):
+    scale = 2.0 ** torch.linspace(-12, 12, rows).view(-1, 1).cuda()
+    check_quantized((normal(rows * k, rows, k) * scale).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_quantize_every_value(dtype):
+    """All finite 16-bit values, each in blocks of its own size and in blocks of larger ones."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    x = bits.view(dtype)
+    x = x[torch.isfinite(x.float())]
+    x = x[: x.numel() // 32 * 32]
+    order = torch.argsort(x.float().abs(), stable=True)
+    mixed = torch.randperm(x.numel(), generator=torch.Generator().manual_seed(1))
+    for at in (order, mixed):
+        check_quantized(x[at].view(-1, 32).cuda())
+        check_quantized(x[at].view(1, -1).cuda())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_quantize_infinities_nan_and_zeros(dtype):
+    x = normal(3, 6, 96, dtype=dtype)
+    x[0, 5], x[1, 40], x[2, 95] = float("inf"), float("-inf"), float("nan")
+    x[3, 32:64] = 0
+    x[4] = -0.0
+    check_quantized(x)
+    _, xs = experts.quantize_mx4(x)
+    assert xs[0].tolist()[0] == xs[1].tolist()[1] == xs[2].tolist()[2] == 255
+    assert (xs[:3] == 255).sum() == 3
+
+
+def test_quantize_views_and_no_rows():
+    x = normal(4, 40, 70, dtype=torch.bfloat16)
+    wide = torch.full((40, 91), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 3:73] = x
+    for a, b in zip(experts.quantize_mx4(wide[:, 3:73]), experts.quantize_mx4(x)):
+        assert torch.equal(a, b)
+    xq, xs = experts.quantize_mx4(x[:0])
+    assert xq.shape == (0, 48) and xs.shape == (0, 3)
+
+
+def weights(seed, num, n, k):
+    """Codes and powers [num, n, ...] as quantize_mx4 lays them out, and their values in 64 bits."""
+    w = normal(seed, num * n, k, dtype=torch.bfloat16, scale=k**-0.5)
+    wq, ws = experts.quantize_mx4(w)
+    wq, ws = wq.view(num, n, -1), ws.view(num, n, -1)
+    return wq, ws, exact(wq, ws)
+
+
+def exact(q, s):
+    return torch.from_numpy(mx4_reference.values(q.cpu().numpy(), s.cpu().numpy())).cuda()
+
+
+def check(y, xv, wv, g, gather):
+    """xv: the rows' values in 64 bits; wv: the weights'."""
+    for e, a, b in spans(g):
+        want, magnitude = product(token_rows(xv, g, a, b, gather), wv[e])
+        assert_close(y[a:b], want, magnitude, xv.shape[1])
+    assert not y[int(g.offsets[-1]):].any()
+
+
+@pytest.mark.parametrize("size", [c[1] for c in ROWS], ids=names(ROWS))
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_every_kernel(size, dtype):
+    tokens, num, n, k = size
+    g = pairs_of(tokens, num)
+    x = normal(1, tokens, 4 * k, dtype=dtype)
+    wq, ws, wv = weights(2, num, n, 4 * k)
+    xq, xs = experts.quantize_mx4(x)
+    xv = exact(xq, xs)
+    y = experts.mx4_matmul(xq, xs, wq, ws, g, gather=True, out_dtype=dtype)
+    assert y.dtype == dtype
+    check(y, xv, wv, g, True)
+
+
+def shifted(t, by):
+    longer = torch.full((*t.shape[:-1], t.shape[-1] + 2 * by + 3), 255, dtype=t.dtype,
+                        device=t.device)
+    view = longer[..., by:by + t.shape[-1]]
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("size", [c[1] for c in ROWS + VIA],
+                         ids=names(ROWS) + [n + "_through_registers" for n in names(VIA)])
+@pytest.mark.parametrize("codes,powers", [(1, 0), (0, 1), (0, 4), (6, 2)])
+def test_bits_do_not_depend_on_addresses(size, codes, powers):
+    """Rows off 16 bytes, powers off 4 and powers at odd multiples of 4, other operands' bytes of 255
+    around them: the same bits as contiguous ones."""
+    tokens, num, n, k = size
+    g = pairs_of(tokens, num)
+    xq, xs = experts.quantize_mx4(normal(1, tokens, 4 * k, dtype=torch.bfloat16))
+    wq, ws, _ = weights(2, num, n, 4 * k)
+    want = experts.mx4_matmul(xq, xs, wq, ws, g, gather=True)
+    got = experts.mx4_matmul(shifted(xq, codes), shifted(xs, powers), shifted(wq, codes),
+                             shifted(ws, powers), g, gather=True)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("blocks", [1, 2, 3, 4, 5, 7, 8, 9, 11, 12, 16, 17, 24, 31, 33, 63])
+@pytest.mark.parametrize("rows,n", [(3, 40), (70, 2600), (1000, 2000), (2100, 8200)])
+def test_ragged_reductions(blocks, rows, n):
+    """Every remainder of a step, dense: few rows, tiles with stages, large tiles. The bytes after the
+    rows' own powers are 255, which would make a product NaN."""
+    k = blocks * 32
+    xq, xs = experts.quantize_mx4(normal(blocks, rows, k, dtype=torch.bfloat16))
+    wq, ws, wv = weights(blocks + 1, 1, n, k)
+    padded = torch.full((n, (blocks + 3) // 4 * 4 + 4), 255, dtype=torch.uint8, device="cuda")
+    padded[:, :blocks] = ws[0]
+    longer = torch.full((rows, (blocks + 3) // 4 * 4), 255, dtype=torch.uint8, device="cuda")
+    longer[:, :blocks] = xs
+    y = experts.mx4_matmul(xq, longer[:, :blocks], wq[0], padded[:, :blocks])
+    want, magnitude = product(exact(xq, xs), wv[0])
+    assert_close(y, want, magnitude, k)
+
+
+@pytest.mark.parametrize("tokens,num,n,k,gather", [
+    (1, 1, 1, 1, True), (1, 8, 16, 32, True), (7, 3, 5, 33, False), (50, 5, 130, 200, True),
+    (300, 4, 257, 1000, False), (2000, 4, 300, 288, True)])
+@pytest.mark.parametrize("kind", ["mixed", "one", "none"])
+def test_groups(tokens, num, n, k, gather, kind):
+    top_k = min(num, 2)
+    g = groups(route(tokens, tokens, top_k, num, kind), num)
+    x = normal(1, tokens if gather else tokens * top_k, k, dtype=torch.float16)
+    wq, ws, wv = weights(2, num, n, k)
+    xq, xs = experts.quantize_mx4(x)
+    check(experts.mx4_matmul(xq, xs, wq, ws, g, gather=gather, out_dtype=torch.float16),
+          exact(xq, xs), wv, g, gather)
+
+
+@pytest.mark.parametrize("rows,n", [(5, 100), (600, 2600)])
+def test_infinities_and_extreme_powers(rows, n):
+    """A row or a column with a power of 255 is NaN and keeps it to itself; the least and greatest powers
+    multiply to ordinary values."""
+    k = 544
+    xq, xs = experts.quantize_mx4(normal(1, rows, k, dtype=torch.bfloat16))
+    wq, ws, _ = weights(2, 1, n, k)
+    wq, ws = wq[0].contiguous(), ws[0].contiguous()
+    xs, ws = xs.contiguous(), ws.contiguous()
+    xs[2], ws[3] = 0, 254
+    xs[1, 5], ws[7, 16] = 255, 255
+    y = experts.mx4_matmul(xq, xs, wq, ws)
+    want, magnitude = product(exact(xq, xs), exact(wq, ws))
+    # (the partial sums of magnitudes past 2^128 = 3.4e38, column 3 of most rows, leave the range of 32
+    # bits, and two of different signs make a NaN: there the 32-bit sum has no value to compare)
+    held = ~(magnitude >= 2.0**128)
+    assert torch.equal(torch.isnan(y[held]), torch.isnan(want[held]))
+    assert held[2].all() and held[:, 4:].all()
+    assert torch.isnan(y[1]).all() and torch.isnan(y[:, 7]).all()
+    fine = torch.isfinite(want) & (magnitude < 1e38) & (magnitude > 1e-30)
+    assert fine[2, 3] and fine.any(1).sum() == rows - 1
+    assert_close(y[fine], want[fine], magnitude[fine], k)
+
+
+def test_empty_and_refused():
+    xq, xs = experts.quantize_mx4(normal(1, 4, 64, dtype=torch.bfloat16))
+    assert experts.mx4_matmul(xq[:0], xs[:0], xq, xs).shape == (0, 4)
+    for bad in (lambda: experts.mx4_matmul(xq, xs[:, :1], xq, xs),
+                lambda: experts.mx4_matmul(xq, xs[:3], xq, xs),
+                lambda: experts.mx4_matmul(xq, xs, xq[:, :16], xs[:, :1]),
+                lambda: experts.mx4_matmul(xq, xs, xq, xs, gather=True),
+                lambda: experts.mx4_matmul(xq, xs, xq, xs, out_dtype=torch.float32),
+                lambda: experts.mx4_matmul(xq.int(), xs, xq, xs),
+                lambda: experts.mx4_matmul(xq, xs.cpu(), xq, xs),
+                lambda: experts.quantize_mx4(torch.zeros(4, 64, device="cuda")),
+                lambda: experts.quantize_mx4(torch.zeros(4, 64, dtype=torch.float16,
+                                                         device="cuda")[:, ::2])):
+        with pytest.raises(ValueError):
+            bad()
+
+
+def test_captured_twice():
+    """Two captured graphs of one product, replayed in turn with eager calls between."""
+    g = pairs_of(1000, 8)
+    xq, xs = experts.quantize_mx4(normal(1, 1000, 2080, dtype=torch.bfloat16))
+    wq, ws, _ = weights(2, 8, 4008, 2080)
+    want = experts.mx4_matmul(xq, xs, wq, ws, g, gather=True)
+    torch.cuda.synchronize()
+    captured = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = experts.mx4_matmul(xq, xs, wq, ws, g, gather=True)
+        captured.append((graph, out))
+    for _ in range(3):
+        for graph, out in captured:
+            out.zero_()
+            graph.replay()
+            assert torch.equal(out, want)
+        assert torch.equal(experts.mx4_matmul(xq, xs, wq, ws, g, gather=True), want)
