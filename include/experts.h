@@ -22,6 +22,7 @@
  *                           addition, in 16 bits or (experts_rms_norm_int8) in
  *                           8 as experts_int8_matmul takes them
  *   experts_rms_norm_backward  its gradients
+ *   experts_few_tokens      the whole layer for up to EXPERTS_MAX_FEW tokens
  *
  * Pairs are numbered twice: i in the order of the tokens, p in the order of
  * the experts. order[p] = i and place[i] = p. A pair whose id lies outside
@@ -189,6 +190,50 @@ hist_status_t experts_rms_norm_backward(void *dx, int64_t lddx, void *dweight, c
                                         int64_t lddh, const void *weight, uint64_t rows,
                                         uint32_t n, float eps, int32_t dtype, void *workspace,
                                         uint64_t workspace_bytes, hipStream_t stream);
+
+/* Experts' weights [experts][rows][k]: 16-bit elements of the tokens' type, or
+ * 8-bit whole numbers with scales (float [experts][rows]), or 4-bit codes with
+ * powers of two as experts_quantize_mx4 makes them. Leading dimensions, and
+ * strides from one expert to the next, are in elements (of codes: bytes). */
+typedef enum {
+    EXPERTS_WEIGHT_16 = 0,
+    EXPERTS_WEIGHT_INT8 = 1,
+    EXPERTS_WEIGHT_MX4 = 2
+} experts_weight_kind_t;
+
+typedef struct {
+    const void *data;
+    int64_t ld, stride;
+    const void *scales;    /* NULL for EXPERTS_WEIGHT_16 */
+    int64_t ld_scales;     /* of powers of two; not used otherwise */
+    int64_t scales_stride; /* of scales or powers */
+    int32_t kind;
+} experts_weight_t;
+
+/* Tokens that experts_few_tokens takes. */
+#define EXPERTS_MAX_FEW 64u
+
+/* Bytes of workspace experts_few_tokens needs; down_kind: of the second weight. */
+hist_status_t experts_few_tokens_workspace_size(uint64_t tokens, uint32_t top_k,
+                                                uint32_t experts, uint32_t hidden, uint32_t n,
+                                                int32_t down_kind, uint64_t *bytes);
+
+/* A whole expert layer for a few tokens. out [tokens][n], x [tokens][width]:
+ *   out[t] = sum_j weights[t][j] h down[e]^T, e = ids[t][j], a = x[t] up[e]^T,
+ *   h = silu(a) (gated 0), or (gated 1) silu of a's first half times its second.
+ * up [experts][hidden or 2 hidden][width], down [experts][n][hidden]. ids: int32
+ * or int64 (id_bits) [tokens][top_k]; an id outside [0, experts) adds nothing.
+ * silu(a) = a / (1 + e^-a). Sums are held in 32 bits; h is rounded to the type
+ * once, the result once. Weights of an expert without a token are not read.
+ * workspace: 16-byte aligned, not read before it is written; calls that may run
+ * at one time need one each. */
+hist_status_t experts_few_tokens(void *out, int64_t ldo, const void *x, int64_t ldx,
+                                 const experts_weight_t *up, const experts_weight_t *down,
+                                 const void *ids, int32_t id_bits, const float *weights,
+                                 uint64_t tokens, uint32_t top_k, uint32_t experts,
+                                 uint32_t width, uint32_t hidden, uint32_t n, int32_t gated,
+                                 int32_t dtype, void *workspace, uint64_t workspace_bytes,
+                                 hipStream_t stream);
 
 typedef enum {
     EXPERTS_MATMUL = 0,

@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libpca_hist.so")
 SOURCES = ["hist_api.hip", "hist_bench.hip", "hist_tune.hip", "hist_static.hip",
            "hist_model.hip", "experts_group.hip", "experts_combine.hip", "experts_matmul.hip",
-           "experts_dw.hip", "experts_int8.hip", "experts_norm.hip", "experts_mx4.hip"]
+           "experts_dw.hip", "experts_int8.hip", "experts_norm.hip", "experts_mx4.hip",
+           "experts_few.hip", "experts_few_bf16.hip"]
 JOBS = 6  # compilers at one time
 
 HIPCC_FLAGS = [

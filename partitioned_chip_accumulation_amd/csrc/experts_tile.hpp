@@ -132,6 +132,20 @@ __device__ __forceinline__ void sums_done(Acc (&acc)[FM][FN])
         for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
 }
 
+// Of 16 bytes that end with a row, the last `left` (any number), followed by zeros.
+__device__ __forceinline__ u32x4 drop16(u32x4 v, int left)
+{
+    const uint32_t s = left >= 16 ? 0 : left > 0 ? 16 - left : 16;  // bytes to drop
+    const bool eight = s & 8, four = s & 4;
+    const uint32_t a0 = eight ? v[2] : v[0], a1 = eight ? v[3] : v[1];
+    const uint32_t a2 = eight ? 0 : v[2], a3 = eight ? 0 : v[3];
+    const uint32_t b0 = four ? a1 : a0, b1 = four ? a2 : a1, b2 = four ? a3 : a2;
+    const uint32_t b3 = four ? 0 : a3;
+    const u32x4 r = {__builtin_amdgcn_alignbyte(b1, b0, s), __builtin_amdgcn_alignbyte(b2, b1, s),
+                     __builtin_amdgcn_alignbyte(b3, b2, s), __builtin_amdgcn_alignbyte(0, b3, s)};
+    return s == 16 ? u32x4{0, 0, 0, 0} : r;
+}
+
 // 16 bytes at p, of which only the first `left` (any number) belong to the row; the others
 // read 0. Any alignment of T. Where the row has 16 bytes (`roomy`, the same for the wave), the 16 that
 // end with it are read and shifted (a product of 16384 rows and 2048 columns with a reduction of
@@ -139,18 +153,7 @@ __device__ __forceinline__ void sums_done(Acc (&acc)[FM][FN])
 template <class T>
 __device__ __forceinline__ u32x4 load16(const char *p, int left, bool roomy)
 {
-    if (roomy) {
-        const u32x4 v = load_any<u32x4>(p + (left < 16 ? left : 16) - 16);
-        const uint32_t s = left >= 16 ? 0 : left > 0 ? 16 - left : 16;  // bytes to drop
-        const bool eight = s & 8, four = s & 4;
-        const uint32_t a0 = eight ? v[2] : v[0], a1 = eight ? v[3] : v[1];
-        const uint32_t a2 = eight ? 0 : v[2], a3 = eight ? 0 : v[3];
-        const uint32_t b0 = four ? a1 : a0, b1 = four ? a2 : a1, b2 = four ? a3 : a2;
-        const uint32_t b3 = four ? 0 : a3;
-        const u32x4 r = {__builtin_amdgcn_alignbyte(b1, b0, s), __builtin_amdgcn_alignbyte(b2, b1, s),
-                         __builtin_amdgcn_alignbyte(b3, b2, s), __builtin_amdgcn_alignbyte(0, b3, s)};
-        return s == 16 ? u32x4{0, 0, 0, 0} : r;
-    }
+    if (roomy) return drop16(load_any<u32x4>(p + (left < 16 ? left : 16) - 16), left);
     u32x4 v = {0, 0, 0, 0};
     constexpr int kEach = 16 / sizeof(T);
 #pragma unroll

@@ -35,6 +35,7 @@ from . import hist
 
 MAX_EXPERTS = 1024
 MAX_TOP_K = 64
+MAX_FEW = 64  # tokens of few_tokens
 _ONE_WORKGROUP = 8192  # pairs that experts_group sorts without a workspace
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
@@ -66,8 +67,17 @@ _SIGNATURES = {
     "experts_rms_norm_backward_workspace_size": [_u64, _u32, ctypes.POINTER(_u64)],
     "experts_rms_norm_backward": [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _u64, _u32,
                                   _f32, _i32, _vp, _u64, _vp],
+    "experts_few_tokens_workspace_size": [_u64, _u32, _u32, _u32, _u32, _i32, ctypes.POINTER(_u64)],
+    "experts_few_tokens": [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _u64, _u32, _u32, _u32,
+                           _u32, _u32, _i32, _i32, _vp, _u64, _vp],
 }
 PRODUCTS = {"matmul": 0, "matmul_dx": 1, "matmul_dw": 2, "int8_matmul": 3, "mx4_matmul": 4}
+
+
+class _Weight(ctypes.Structure):
+    """The experts' weights as ``experts_few_tokens`` takes them."""
+    _fields_ = [("data", _vp), ("ld", _i64), ("stride", _i64), ("scales", _vp), ("ld_scales", _i64),
+                ("scales_stride", _i64), ("kind", _i32)]
 
 
 class Kernel(ctypes.Structure):
@@ -461,6 +471,76 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
           dy.data_ptr(), lddy, h.data_ptr(), ldh, None if dh is None else dh.data_ptr(), lddh,
           weight.data_ptr(), rows, n, eps, _DTYPES[dy.dtype], work.data_ptr(), need.value)
     return dx, dweight
+
+
+def _stack(w, name: str, k: int, x: torch.Tensor) -> tuple[_Weight, tuple]:
+    """The weights of ``few_tokens`` for rows of k values like x's, and the shape of their data."""
+    if isinstance(w, torch.Tensor):
+        data, scales = w, None
+        ld = _matrix(data, name, (x.dtype,), 3)
+        kind, width, ld_scales, scales_stride = 0, k, 0, 0
+    else:
+        data, scales = w
+        mx4 = isinstance(data, torch.Tensor) and data.dtype == torch.uint8
+        ld = _matrix(data, name, (torch.uint8 if mx4 else torch.int8,), 3)
+        if mx4:
+            kind, width = 2, (k + 31) // 32 * 16
+            ld_scales = _powers(scales, data, f"the powers of two of {name}")
+            scales_stride = scales.stride(0) if scales.shape[0] > 1 else 0
+        else:
+            kind, width, ld_scales, scales_stride = 1, k, 0, data.shape[1]
+            _vector(scales, f"the scales of {name}", torch.float32, data.shape[:-1], data.device)
+    shape = data.shape
+    if data.device != x.device or shape[0] == 0 or shape[1] == 0 or shape[2] != width:
+        raise ValueError(f"{name} must hold the weights [experts, rows, {width}] of an expert or more "
+                         f"on {x.device}")
+    return _Weight(data.data_ptr(), ld, data.stride(0) if shape[0] > 1 else 0,
+                   None if scales is None else scales.data_ptr(), ld_scales, scales_stride,
+                   kind), shape
+
+
+def few_tokens(x: torch.Tensor, up, down, ids: torch.Tensor, weights: torch.Tensor,
+               gated: bool = True) -> torch.Tensor:
+    """A whole expert layer for up to MAX_FEW tokens: out[t] = sum over j of weights[t, j] h down[e]^T
+    with e = ids[t, j], h = silu(a) for a = x[t] up[e]^T, or with ``gated`` silu of a's first half times
+    its second half.
+
+    up is [experts, hidden (gated: 2 hidden), width] and down [experts, n, hidden]: a tensor of x's type,
+    or a pair of int8 values and float32 scales [experts, rows], or a pair of 4-bit codes and powers of
+    two as ``quantize_mx4`` makes them. ids (int32 or int64) and weights (float32) are [tokens, top_k]; an
+    id outside [0, experts) adds nothing. Weights of experts without a token are not read."""
+    ldx = _matrix(x, "x")
+    tokens, width = x.shape
+    device = x.device
+    if not (isinstance(ids, torch.Tensor) and ids.device == device and ids.dim() == 2 and
+            ids.dtype in (torch.int32, torch.int64) and ids.is_contiguous() and
+            ids.shape[0] == tokens):
+        raise ValueError(f"ids must be a contiguous int32 or int64 tensor of shape [{tokens}, top_k] "
+                         f"on {device}")
+    top_k = ids.shape[1]
+    _vector(weights, "weights", torch.float32, ids.shape, device)
+    if tokens > MAX_FEW:
+        raise ValueError(f"few_tokens takes {MAX_FEW} tokens at most: group_rows, linear and merge take "
+                         f"any number")
+    first, (experts, rows, _) = _stack(up, "up", width, x)
+    if gated and rows % 2:
+        raise ValueError("up must have an even number of rows, a gate's and as many others")
+    hidden = rows // 2 if gated else rows
+    second, (others, n, _) = _stack(down, "down", hidden, x)
+    _same(experts, others, "the numbers of up's and down's experts")
+    need = _u64()
+    _library()
+    status = _functions["experts_few_tokens_workspace_size"](tokens, top_k, experts, hidden, n,
+                                                             second.kind, ctypes.byref(need))
+    if status:
+        raise hist.HistError(status, "experts_few_tokens_workspace_size")
+    out = torch.empty(tokens, n, dtype=x.dtype, device=device)
+    work = torch.empty(need.value, dtype=torch.uint8, device=device)
+    _call("experts_few_tokens", device, out.data_ptr(), n, x.data_ptr(), ldx, ctypes.addressof(first),
+          ctypes.addressof(second), ids.data_ptr(), ids.element_size() * 8, weights.data_ptr(), tokens,
+          top_k, experts, width, hidden, n, bool(gated), _DTYPES[x.dtype], work.data_ptr(),
+          need.value)
+    return out
 
 
 def preview(product: str, rows: int, experts: int, n: int, k: int, x_rows: int = 0,
