@@ -225,6 +225,9 @@ hist_status_t experts_few_tokens_workspace_size(uint64_t tokens, uint32_t top_k,
  * or int64 (id_bits) [tokens][top_k]; an id outside [0, experts) adds nothing.
  * silu(a) = a / (1 + e^-a). Sums are held in 32 bits; h is rounded to the type
  * once, the result once. Weights of an expert without a token are not read.
+ * width and hidden are 8 or more, 16 for 8-bit weights; 64 of x's rows, and an
+ * expert's rows of powers of two, lie within 2^31 bytes, and the weights' leading
+ * dimensions are 2^25 at most (HIST_ERR_UNSUPPORTED otherwise).
  * workspace: 16-byte aligned, not read before it is written; calls that may run
  * at one time need one each. */
 hist_status_t experts_few_tokens(void *out, int64_t ldo, const void *x, int64_t ldx,

@@ -17,7 +17,7 @@ inline hist_status_t check_few(uint64_t tokens, uint32_t top_k, uint32_t experts
 }
 
 // A weight [experts][rows][k] of a kind, in bytes; false if it cannot be one.
-inline bool few_weight(FewWeight &w, const experts_weight_t *from, uint32_t k)
+inline bool few_weight(FewWeight &w, const experts_weight_t *from, uint32_t rows, uint32_t k)
 {
     if (!from || from->kind < EXPERTS_WEIGHT_16 || from->kind > EXPERTS_WEIGHT_MX4 || !from->data ||
         from->stride < 0)
@@ -26,7 +26,8 @@ inline bool few_weight(FewWeight &w, const experts_weight_t *from, uint32_t k)
     const int64_t size = wide ? 2 : 1, scale = mx4 ? 1 : 4;
     const int64_t blocks = (k + 31) / 32;
     w = {(const char *)from->data, (const char *)from->scales, from->ld * size, from->stride * size,
-         mx4 ? from->ld_scales : 0, from->scales_stride * scale};
+         mx4 ? from->ld_scales : 0, from->scales_stride * scale,
+         mx4 ? (uint32_t)((rows - 1) * from->ld_scales + blocks) : 0};
     if (from->ld < (mx4 ? blocks * 16 : (int64_t)k) || misaligned(w.data, size)) return false;
     if (wide) return true;
     return w.scales && from->scales_stride >= 0 && !misaligned(w.scales, scale) &&
@@ -69,13 +70,26 @@ extern "C" hist_status_t experts_few_tokens(void *out, int64_t ldo, const void *
         return HIST_ERR_INVALID_ARG;
     hist_status_t st = check_few(tokens, top_k, experts, hidden, n, down->kind);
     if (st != HIST_OK) return st;
-    if (width > EXPERTS_MAX_WIDTH) return HIST_ERR_UNSUPPORTED;
+    // (rows of 16 bytes: no load is shorter)
+    if (width > EXPERTS_MAX_WIDTH || width < (up->kind == EXPERTS_WEIGHT_INT8 ? 16u : 8u) ||
+        hidden < (down->kind == EXPERTS_WEIGHT_INT8 ? 16u : 8u))
+        return HIST_ERR_UNSUPPORTED;
     FewArgs g = {};
-    if (!few_weight(g.up, up, width) || !few_weight(g.down, down, hidden) || ldo < (int64_t)n ||
+    const uint32_t up_rows = gated ? 2 * hidden : hidden;
+    if (!few_weight(g.up, up, up_rows, width) || !few_weight(g.down, down, n, hidden) || ldo < (int64_t)n ||
         ldx < (int64_t)width || misaligned(out, 2) || misaligned(x, 2) ||
         misaligned(ids, id_bits / 8) || misaligned(weights, 4) ||
         (tokens && (!out || !x || !ids || !weights)))
         return HIST_ERR_INVALID_ARG;
+    // (32-bit places in x, in h, in 32 rows of a weight and in an expert's powers of two)
+    auto near = [](uint64_t rows, int64_t ld) { return rows * ld <= Window::kMost; };
+    if (ldx > (1 << 30) || !near(EXPERTS_MAX_FEW, ldx * 2) || up->ld > (1 << 25) ||
+        down->ld > (1 << 25) ||
+        (up->kind == EXPERTS_WEIGHT_MX4 &&
+         (up->ld_scales > (1 << 30) || !near(up_rows, up->ld_scales))) ||
+        (down->kind == EXPERTS_WEIGHT_MX4 &&
+         (down->ld_scales > (1 << 30) || !near(n, down->ld_scales))))
+        return HIST_ERR_UNSUPPORTED;
     const FewPlan p = few_plan(tokens ? tokens : 1, top_k, experts, hidden, n, down->kind);
     if (tokens && (!workspace || misaligned(workspace, 16) || workspace_bytes < p.bytes))
         return HIST_ERR_WORKSPACE;
@@ -90,7 +104,7 @@ extern "C" hist_status_t experts_few_tokens(void *out, int64_t ldo, const void *
     g.by = weights;
     g.ldo = ldo * 2;
     g.ldx = ldx * 2;
-    g.ldh = (hidden + 7) / 8 * 16;
+    g.ldh = h_bytes(hidden, down->kind);
     g.ids64 = id_bits == 64;
     g.tokens = (uint32_t)tokens;
     g.top_k = top_k;

@@ -20,19 +20,19 @@ namespace pca_experts {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-constexpr uint32_t kMostFew = EXPERTS_MAX_FEW;  // tokens
-constexpr uint32_t kTurn = 64;                  // bytes of a row that a wave takes in one step
+constexpr uint32_t kHalf = 64;  // bytes of a row that one load of a wave takes
 
 struct FewWeight {
     const char *data;
     const char *scales;  // float [experts][rows], or powers of two
     int64_t ld, stride, ld_scales, scales_stride;  // bytes
+    uint32_t window;                               // bytes of an expert's powers of two
 };
 
 struct FewArgs {
     char *out;
     const char *x;
-    char *h;            // [pairs][ldh]: row t * top_k + j, j the first of t's choices of its expert
+    char *h;            // [pairs][ldh]
     uint32_t *arrived;  // [tiles of the result]
     uint32_t *partial;
     FewWeight up, down;
@@ -40,7 +40,7 @@ struct FewArgs {
     const float *by;
     int64_t ldo, ldx, ldh;  // bytes
     uint32_t ids64, gated, tokens, top_k, experts, width, hidden, n;
-    uint32_t tiles, splits;
+    uint32_t tiles, splits;  // of the result
 };
 
 // How weights of type W go with tokens of type T: C fragments of a lane's 16 bytes.
@@ -119,136 +119,332 @@ __device__ __host__ __forceinline__ uint32_t row_bytes(uint32_t k)
 }
 
 // ---------------------------------------------------------------------------
-// The routing in LDS: the ids, and the experts that have a token in the order of their numbers.
+// The routing. A slot is what there is to do for one expert and up to kRows pairs of it, in their order.
+// Up to 64 pairs are a wave's registers: every wave finds its slots by itself, without LDS and barriers,
+// in the order of the experts' first pairs. More pairs go through LDS, where the slots come in the order of
+// the experts' numbers.
 struct Routes {
-    uint32_t mask[EXPERTS_MAX_EXPERTS / 32];
+    uint32_t many[EXPERTS_MAX_EXPERTS];  // pairs of each expert
     uint32_t count;
-    int16_t list[EXPERTS_MAX_EXPERTS];
+    // expert, and which kRows of its pairs << 16 (there are as many as experts, and one more for each 16 of
+    // the other pairs)
+    uint32_t list[EXPERTS_MAX_EXPERTS + EXPERTS_MAX_FEW * EXPERTS_MAX_TOP_K / 16];
 };
-extern __shared__ __align__(16) char few_lds[];  // int16_t ids[pairs], float by[pairs]
+extern __shared__ __align__(16) char few_lds[];  // int16_t ids[pairs], float by[pairs], then the sums
 
-__device__ __forceinline__ int16_t *lds_ids() { return (int16_t *)few_lds; }
-__device__ __forceinline__ float *lds_by(uint32_t pairs)
+__device__ __host__ __forceinline__ uint32_t ids_bytes(uint32_t pairs)
 {
-    return (float *)(few_lds + (pairs * 2 + 15) / 16 * 16);
+    return (pairs * 2 + 15) / 16 * 16;
+}
+__device__ __host__ __forceinline__ uint32_t by_bytes(uint32_t pairs)
+{
+    return (pairs * 4 + 15) / 16 * 16;
 }
 
-template <bool BY>
-__device__ __forceinline__ void find_routes(const FewArgs &g, Routes &routes)
-{
-    const uint32_t pairs = g.tokens * g.top_k;
-    if (threadIdx.x < EXPERTS_MAX_EXPERTS / 32) routes.mask[threadIdx.x] = 0;
-    __syncthreads();
-    for (uint32_t i = threadIdx.x; i < pairs; i += blockDim.x) {
-        const int64_t id = g.ids64 ? ((const int64_t *)g.ids)[i] : ((const int32_t *)g.ids)[i];
-        const bool valid = (uint64_t)id < g.experts;
-        lds_ids()[i] = valid ? (int16_t)id : -1;
-        if constexpr (BY) lds_by(pairs)[i] = g.by[i];
-        if (valid)
-            __hip_atomic_fetch_or(&routes.mask[id / 32], 1u << id % 32, __ATOMIC_RELAXED,
-                                  __HIP_MEMORY_SCOPE_WORKGROUP);
+template <uint32_t kRows, bool BY>
+struct Router {
+    Routes &routes;
+    const uint32_t pairs;
+    uint32_t count;  // slots
+    // of pair number lane, of up to 64
+    int id;
+    float by;
+    uint32_t rank;    // pairs of the expert before it
+    uint64_t same;    // its pairs
+    uint64_t starts;  // the lanes that a slot begins with, the same for all
+
+    __device__ __forceinline__ int16_t *lds_ids() const { return (int16_t *)few_lds; }
+    __device__ __forceinline__ float *lds_by() const { return (float *)(few_lds + ids_bytes(pairs)); }
+
+    __device__ __forceinline__ Router(const FewArgs &g, Routes &r)
+        : routes(r), pairs(g.tokens * g.top_k)
+    {
+        auto id_of = [&](uint32_t i) {
+            const int64_t id = g.ids64 ? ((const int64_t *)g.ids)[i] : ((const int32_t *)g.ids)[i];
+            return (uint64_t)id < g.experts ? (int)id : -1;
+        };
+        const uint32_t lane = threadIdx.x % 64;
+        if (pairs <= 64) {
+            id = lane < pairs ? id_of(lane) : -1;
+            by = BY && lane < pairs ? g.by[lane] : 0.f;
+            same = __ballot(id >= 0);
+#pragma unroll
+            for (int bit = 0; (1u << bit) < EXPERTS_MAX_EXPERTS; ++bit) {
+                const uint64_t set = __ballot(id >> bit & 1);
+                same &= id >> bit & 1 ? set : ~set;
+            }
+            rank = (uint32_t)__popcll(same & ((1ull << lane) - 1));
+            starts = __ballot(id >= 0 && rank % kRows == 0);
+            count = (uint32_t)__popcll(starts);
+            return;
+        }
+        for (uint32_t e = threadIdx.x; e < g.experts; e += blockDim.x) routes.many[e] = 0;
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < pairs; i += blockDim.x) {
+            const int e = id_of(i);
+            lds_ids()[i] = (int16_t)e;
+            if constexpr (BY) lds_by()[i] = g.by[i];
+            if (e >= 0) lds_add(routes.many, (uint32_t)e, 1);
+        }
+        __syncthreads();
+        if (threadIdx.x < 64) {
+            const uint32_t each = (g.experts + 63) / 64, first = lane * each;
+            uint32_t mine = 0;
+            for (uint32_t e = first; e < first + each && e < g.experts; ++e)
+                mine += (routes.many[e] + kRows - 1) / kRows;
+            const uint32_t upto = wave_inclusive_scan(mine);
+            uint32_t at = upto - mine;
+            for (uint32_t e = first; e < first + each && e < g.experts; ++e)
+                for (uint32_t q = 0; q * kRows < routes.many[e]; ++q)
+                    routes.list[at++] = e | q << 16;
+            if (lane == 63) routes.count = upto;
+        }
+        __syncthreads();
+        count = __builtin_amdgcn_readfirstlane(routes.count);
     }
-    __syncthreads();
-    if (threadIdx.x < 64) {
-        uint32_t bits = threadIdx.x < EXPERTS_MAX_EXPERTS / 32 ? routes.mask[threadIdx.x] : 0;
-        const uint32_t mine = __builtin_popcount(bits), upto = wave_inclusive_scan(mine);
-        uint32_t at = upto - mine;
-        for (; bits; bits &= bits - 1)
-            routes.list[at++] = (int16_t)(threadIdx.x * 32 + __builtin_ctz(bits));
-        if (threadIdx.x == 63) routes.count = upto;
+
+    // The expert of a slot, and its pairs to `rows` (the wave's own kRows places); returns how many.
+    __device__ __forceinline__ uint32_t find(uint32_t slot, uint16_t *rows, uint32_t &expert) const
+    {
+        const uint32_t lane = threadIdx.x % 64;
+        const uint64_t below = (1ull << lane) - 1;
+        uint32_t seen = 0;
+        if (pairs <= 64) {
+            const bool here = starts >> lane & 1 && (uint32_t)__popcll(starts & below) == slot;
+            const int at = __builtin_ctzll(__ballot(here));
+            expert = __builtin_amdgcn_readlane(id, at);
+            const uint32_t first = __builtin_amdgcn_readlane(rank, at);
+            const bool mine = id == (int)expert && rank - first < kRows;
+            if (mine) rows[rank - first] = (uint16_t)lane;
+            seen = (uint32_t)__popcll(__ballot(mine));
+        } else {
+            const uint32_t what = __builtin_amdgcn_readfirstlane(routes.list[slot]);
+            const uint32_t skip = (what >> 16) * kRows;
+            expert = what & 0xffff;
+            for (uint32_t i = 0; i < pairs && seen < skip + kRows; i += 64) {
+                const bool here = i + lane < pairs && lds_ids()[i + lane] == (int)expert;
+                const uint64_t mask = __ballot(here);
+                const uint32_t at = seen + (uint32_t)__popcll(mask & below) - skip;
+                if (here && at < kRows) rows[at] = (uint16_t)(i + lane);
+                seen += (uint32_t)__popcll(mask);
+            }
+            seen -= skip;
+            seen = seen < kRows ? seen : kRows;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        return seen;
     }
-    __syncthreads();
-}
+
+    // The weight of a pair; of lanes that are all active.
+    __device__ __forceinline__ float weight(uint32_t pair) const
+    {
+        if (pairs <= 64) return __shfl(by, pair, 64);
+        return lds_by()[pair];
+    }
+};
 
 // ---------------------------------------------------------------------------
-// What one step of a wave multiplies: 64 bytes of each of 16 FB rows of a weight, and what goes with
-// them of 16 RM rows of tokens. At a row's ragged end the 16 bytes that end with it are loaded, and
-// shifted only when they are multiplied, so that no load is waited for before its turn.
+// Memory that a kernel reads through a descriptor: at a lane's place, plus the wave's. Of a lane whose own
+// place lies past the end nothing is loaded, and it gets zeros. kNowhere plus any place in a row is past
+// every end.
+struct Window {
+    __amdgpu_buffer_rsrc_t rsrc;
+    static constexpr uint32_t kNowhere = 1u << 31, kMost = kNowhere - 1;
+    __device__ __forceinline__ Window(const char *base, uint32_t bytes = kMost)
+        : rsrc(__builtin_amdgcn_make_buffer_rsrc((void *)base, 0, bytes, 0x00027000))
+    {
+    }
+    __device__ __forceinline__ u32x4 load16(uint32_t place, uint32_t wave) const
+    {
+        return __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)place, (int)wave, 0));
+    }
+    template <int BYTES>
+    __device__ __forceinline__ uint64_t load(uint32_t place, uint32_t wave) const
+    {
+        if constexpr (BYTES == 4)
+            return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsrc, (int)place, (int)wave, 0);
+        else
+            return __builtin_bit_cast(
+                uint64_t, __builtin_amdgcn_raw_buffer_load_b64(rsrc, (int)place, (int)wave, 0));
+    }
+};
+
+// What one step of a wave multiplies: kHalves times 64 bytes of each of 16 FB rows of a weight, and
+// what goes with them of 16 RM rows of tokens. (Two halves are whole cache lines; with one, each line is
+// asked for twice.)
+//
+// Neighbouring lanes hold neighbouring rows, so every lane is an access of its own to the CU's cache,
+// which takes one a cycle: the 64 for each KB of weights leave room for 40 more at 5.5 TB/s. So lanes of
+// rows without a token load nothing (with their rows loaded like others, 4-bit weights, four loads of tokens
+// for one of theirs, were read at 3.0 TB/s), and 16 lanes load a step's powers of two for all.
+//
+// No load of a weight leaves its row: at the row's end a lane's 16 bytes are the last ones of the row,
+// to be shifted (mend) before they are multiplied. The code is kept short: a pass over other experts' weights
+// leaves none of it in the caches, and kernels of 50 KB took 8 us for next to no work.
 template <class T, class W, int RM, int FB>
 struct Piece {
     typedef Widen<T, W> By;
     static constexpr int C = By::C;
-    static constexpr uint32_t kValues = kTurn / 16 * C * 8;  // of a row
+    static constexpr int kHalves = RM * C > 4 ? 1 : 2;  // (as registers allow)
+    static constexpr uint32_t kBytes = kHalf * kHalves, kValues = kBytes / 16 * C * 8;  // of a row
     static constexpr bool kPowers = std::is_same<W, Mx4>::value;
-    u32x4 b[FB], a[RM][C];
-    uint32_t power[kPowers ? FB : 1];
-    uint32_t step;
+    static constexpr uint32_t kStepPowers = kBytes / 16;
+    u32x4 b[FB][kHalves], a[RM][kHalves][C];
+    uint64_t power[kPowers ? FB : 1];  // of a step's blocks, in lanes below 16
 
-    static __device__ __forceinline__ u32x4 one(const char *p, int left, uint32_t row)
+    static __device__ __host__ __forceinline__ uint32_t steps(uint32_t k)
     {
-        if (row < 16) return load16<uint8_t>(p, left, false);
-        return load_any<u32x4>(p + (left < 16 ? left : 16) - 16);
+        return (row_bytes<W>(k) + kBytes - 1) / kBytes;
     }
-    static __device__ __forceinline__ int left_b(uint32_t step, uint32_t k)
+    // Whether the rows end within their last step.
+    static __device__ __forceinline__ bool ragged(uint32_t k) { return k % kValues != 0; }
+    // The places in a row of this lane's 16 bytes of b, and of its values c of a.
+    static __device__ __forceinline__ uint32_t place_b(uint32_t step, int h)
     {
-        return (int)row_bytes<W>(k) - (int)(step * kTurn + threadIdx.x % 64 / 16 * 16);
+        return step * kBytes + h * kHalf + threadIdx.x % 64 / 16 * 16;
     }
-    static __device__ __forceinline__ int left_a(uint32_t step, uint32_t k, int c)
+    static __device__ __forceinline__ uint32_t place_a(uint32_t step, int h, int c)
     {
-        return ((int)k - (int)(step * kValues + threadIdx.x % 64 / 16 * C * 8 + c * 8)) * 2;
+        return (step * kValues + (h * 4 + threadIdx.x % 64 / 16) * C * 8 + c * 8) * 2;
+    }
+    // The place of a step's powers; those of the last step end with the row.
+    static __device__ __forceinline__ uint32_t place_p(uint32_t step, uint32_t blocks)
+    {
+        const uint32_t most = blocks < kStepPowers ? 0 : blocks - kStepPowers;
+        return step * kStepPowers < most ? step * kStepPowers : most;
     }
 
-    // from_a, from_b: this lane's rows, at the 8 C values and the 16 bytes that are its own in the
-    // first step; powers: its row's first one. k: values of a row.
-    __device__ __forceinline__ void fetch(const char *const (&from_a)[RM],
-                                          const char *const (&from_b)[FB],
-                                          const char *const (&powers)[FB], uint32_t which, uint32_t k)
-    {
-        step = which;
-        const int in_b = left_b(step, k);
-#pragma unroll
-        for (int j = 0; j < FB; ++j) {
-            b[j] = one(from_b[j] + step * kTurn, in_b, row_bytes<W>(k));
-            if constexpr (kPowers) {  // (past the row's end: that of the last block, of zeros)
-                const uint32_t block = step * 4 + threadIdx.x % 64 / 16;
-                power[j] = (uint8_t)powers[j][block * 16 < row_bytes<W>(k) ? block : 0];
-            }
+    // What the pieces of a wave are loaded from: windows, and this lane's places in them.
+    struct Source {
+        const Window &tokens, &first, &second;  // b's fragments below FB / 2 (or 1) lie in the first
+        const Window &powers;
+        uint32_t a[RM], b[FB], p[FB];  // of rows; kNowhere: none
+        __device__ __forceinline__ const Window &of(int j) const
+        {
+            return j < (FB + 1) / 2 ? first : second;
         }
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int in_a = left_a(step, k, c);
-#pragma unroll
-            for (int i = 0; i < RM; ++i)
-                a[i][c] = one(from_a[i] + step * kValues * 2 + c * 16, in_a, k * 2);
-        }
-    }
+    };
 
-    __device__ __forceinline__ void multiply(f32x4 (&acc)[RM][FB], uint32_t k)
+    __device__ __forceinline__ void fetch(const Source &s, uint32_t step)
     {
-        if (step * kTurn + kTurn > row_bytes<W>(k) || step * kValues + kValues > k) {
-            const int in_b = left_b(step, k);
+        const uint32_t lane = threadIdx.x % 64 / 16;
 #pragma unroll
-            for (int j = 0; j < FB; ++j) {
-                if (row_bytes<W>(k) >= 16) b[j] = drop16(b[j], in_b);
-                if constexpr (kPowers) power[j] = in_b > 0 ? power[j] : 127;
-            }
+        for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int in_a = left_a(step, k, c);
+            for (int j = 0; j < FB; ++j)
+                b[j][h] = s.of(j).load16(s.b[j] + lane * 16 + h * kHalf, step * kBytes);
+        if constexpr (kPowers)
+#pragma unroll
+            for (int j = 0; j < FB; ++j)
+                power[j] = s.powers.template load<kStepPowers>(s.p[j], step * kStepPowers);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int i = 0; i < RM; ++i)
-                    if (k * 2 >= 16) a[i][c] = drop16(a[i][c], in_a);
+                    a[i][h][c] = s.tokens.load16(s.a[i] + lane * C * 16 + (h * 4 * C + c) * 16,
+                                                 step * kValues * 2);
+    }
+    // The last step, of rows of k values, a's of `room` bytes.
+    __device__ __forceinline__ void fetch_last(const Source &s, uint32_t step, uint32_t k,
+                                               uint32_t room)
+    {
+        const uint32_t bytes = row_bytes<W>(k);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+            const uint32_t at = place_b(step, h), in = at < bytes - 16 ? at : bytes - 16;
+#pragma unroll
+            for (int j = 0; j < FB; ++j) b[j][h] = s.of(j).load16(s.b[j] + in, 0);
+        }
+        if constexpr (kPowers)
+#pragma unroll
+            for (int j = 0; j < FB; ++j)
+                power[j] = s.powers.template load<kStepPowers>(s.p[j] + place_p(step, bytes / 16), 0);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const uint32_t at = place_a(step, h, c), in = at < room - 16 ? at : room - 16;
+#pragma unroll
+                for (int i = 0; i < RM; ++i) a[i][h][c] = s.tokens.load16(s.a[i] + in, 0);
+            }
+    }
+
+    // Puts zeros for what lies past the rows' ends; step: the last one.
+    __device__ __forceinline__ void mend_b(uint32_t step, uint32_t k, const char *powers,
+                                           const uint32_t (&from_p)[FB])
+    {
+        const uint32_t bytes = row_bytes<W>(k), blocks = bytes / 16;
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+            const int left = (int)bytes - (int)place_b(step, h);
+#pragma unroll
+            for (int j = 0; j < FB; ++j) {
+                if constexpr (kPowers) b[j][h] = left > 0 ? b[j][h] : u32x4{};  // whole blocks
+                else b[j][h] = drop16(b[j][h], left);
             }
         }
+        if constexpr (kPowers)
+#pragma unroll
+            for (int j = 0; j < FB; ++j) {
+                if (blocks >= kStepPowers) {
+                    power[j] >>= (step * kStepPowers - place_p(step, blocks)) * 8;
+                } else if (from_p[j] != Window::kNowhere) {  // a row of fewer than a step's
+                    power[j] = 0;
+#pragma unroll 1
+                    for (uint32_t q = step * kStepPowers; q < blocks; ++q)
+                        power[j] |= (uint64_t)(uint8_t)powers[from_p[j] + q]
+                                    << (q - step * kStepPowers) * 8;
+                }
+            }
+    }
+    __device__ __forceinline__ void mend_a(uint32_t step, uint32_t room)
+    {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int left = (int)room - (int)place_a(step, h, c);
+#pragma unroll
+                for (int i = 0; i < RM; ++i) a[i][h][c] = drop16(a[i][h][c], left);
+            }
+    }
+
+    __device__ __forceinline__ void multiply(f32x4 (&acc)[RM][FB]) const
+    {
+        const uint32_t lane = threadIdx.x % 64;
 #pragma unroll
         for (int j = 0; j < FB; ++j)
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const auto w = By::frag(b[j], c, power[kPowers ? j : 0]);
+            for (int h = 0; h < kHalves; ++h) {
+                uint32_t own = 0;
+                if constexpr (kPowers)
+                    own = __shfl((uint32_t)(power[j] >> h * 32), lane % 16, 64) >> lane / 16 * 8 & 0xff;
 #pragma unroll
-                for (int i = 0; i < RM; ++i) By::add(w, a[i][c], acc[i][j]);
+                for (int c = 0; c < C; ++c) {
+                    const auto w = By::frag(b[j][h], c, own);
+#pragma unroll
+                    for (int i = 0; i < RM; ++i) By::add(w, a[i][h][c], acc[i][j]);
+                }
             }
     }
 };
 
 // `mine` pieces (one or more), DEEP of them on their way while the ones before are multiplied. fetch
 // stays at the last piece when it is asked for more: loads that come from the cache, in place of
-// branches around loads, at which the compiler would wait for all of them.
-template <int DEEP, class P, class F, class M>
-__device__ __forceinline__ void pipeline(uint32_t mine, P (&p)[DEEP], F fetch, M multiply)
+// branches around loads, at which the compiler would wait for all of them. first fetches the
+// first piece, and start is called for it when it is multiplied.
+template <int DEEP, class P, class O, class F, class S, class M>
+__device__ __forceinline__ void pipeline(uint32_t mine, P (&p)[DEEP], O first, F fetch, S start,
+                                         M multiply)
 {
+    first(p[0]);
 #pragma unroll
-    for (int d = 0; d < DEEP; ++d) fetch(p[d]);
+    for (int d = 1; d < DEEP; ++d) fetch(p[d]);
+    start(p[0]);
     uint32_t left = mine;
     for (; left > DEEP; left -= DEEP)
 #pragma unroll
@@ -261,15 +457,17 @@ __device__ __forceinline__ void pipeline(uint32_t mine, P (&p)[DEEP], F fetch, M
         if ((uint32_t)d < left) multiply(p[d]);
 }
 
-// Pieces with numbers first, first + turn, ... below count.
-__device__ __forceinline__ uint32_t pieces(uint32_t count, uint32_t first, uint32_t turn)
+// Of `count` steps in a row, share number `at` of `of` begins here.
+__device__ __forceinline__ uint32_t share(uint32_t count, uint32_t at, uint32_t of)
 {
-    return count > first ? (count - first + turn - 1) / turn : 0;
+    return (uint32_t)((uint64_t)count * at / of);
 }
 
 // ---------------------------------------------------------------------------
 // Columns of h for one expert, 16 FN of them with a gate (FN fragments of its rows, then FN of the
-// others) and 32 FN without, its tokens 16 RM at a time; the four waves divide the reduction.
+// others) and 32 FN without, its tokens 16 RM at a time. The four waves divide the reduction, they take
+// the steps in turn (a wave for each 16 FN columns alone: 35 us instead of 33 for one token in 16 bits, 54
+// instead of 49 for four in 8).
 template <class T, class W, int RM, int FN, int DEEP>
 __device__ __forceinline__ void up_rows(const FewArgs &g, uint32_t e, uint32_t n0,
                                         const uint16_t *rows, uint32_t count, f32x4 *sums)
@@ -278,35 +476,48 @@ __device__ __forceinline__ void up_rows(const FewArgs &g, uint32_t e, uint32_t n
     typedef Piece<T, W, RM, FB> P;
     const uint32_t lane = threadIdx.x % 64, at = lane / 16;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const char *a[RM], *b[FB], *powers[FB];
+    const char *const base = g.up.data + (int64_t)e * g.up.stride + (int64_t)n0 * g.up.ld;
+    const char *const scales = g.up.scales + (int64_t)e * g.up.scales_stride;
+    const Window tokens(g.x, (g.tokens - 1) * (uint32_t)g.ldx + g.width * 2), powers(scales, g.up.window);
+    const Window first(base), second(base + (g.gated ? (int64_t)g.hidden * g.up.ld : 0));
+    typename P::Source from = {tokens, first, second, powers};
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
         const uint32_t r = i * 16 + lane % 16;
-        const uint32_t token = rows[r < count ? r : count - 1] / g.top_k;
-        a[i] = g.x + (int64_t)token * g.ldx + at * P::C * 16;
+        from.a[i] = r < count ? rows[r] / g.top_k * (uint32_t)g.ldx : Window::kNowhere;
     }
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
         uint32_t c = n0 + (g.gated ? j % FN : j) * 16 + lane % 16;
-        c = (c < g.hidden ? c : g.hidden - 1) + (g.gated ? j / FN * g.hidden : 0);
-        b[j] = g.up.data + (int64_t)e * g.up.stride + (int64_t)c * g.up.ld + at * 16;
-        powers[j] = nullptr;
-        if constexpr (P::kPowers)
-            powers[j] = g.up.scales + (int64_t)e * g.up.scales_stride + (int64_t)c * g.up.ld_scales;
+        c = c < g.hidden ? c : g.hidden - 1;
+        from.b[j] = (c - n0) * (uint32_t)g.up.ld;
+        c += g.gated ? j / FN * g.hidden : 0;
+        from.p[j] = lane < 16 ? c * (uint32_t)g.up.ld_scales : Window::kNowhere;
     }
     f32x4 acc[RM][FB] = {};
-    const uint32_t steps = (row_bytes<W>(g.width) + kTurn - 1) / kTurn;
-    const uint32_t mine = pieces(steps, wave, 4);
-    if (mine) {
+    // the last step first: it may be ragged
+    const uint32_t steps = P::steps(g.width);
+    if (steps > wave) {
         P p[DEEP];
-        uint32_t next = wave;
-        const uint32_t end = wave + (mine - 1) * 4;
-        pipeline(mine, p,
+        const bool ragged = wave == 0 && P::ragged(g.width);
+        uint32_t next = steps - 1 - wave;
+        auto fetch = [&](P &q) {
+            q.fetch(from, next);
+            next = next < 4 ? next : next - 4;
+        };
+        pipeline((steps - wave + 3) / 4, p,
                  [&](P &q) {
-                     q.fetch(a, b, powers, next, g.width);
-                     next = next < end ? next + 4 : end;
+                     if (!ragged) return fetch(q);
+                     q.fetch_last(from, next, g.width, g.width * 2);
+                     next = next < 4 ? next : next - 4;
                  },
-                 [&](P &q) { q.multiply(acc, g.width); });
+                 fetch,
+                 [&](P &q) {
+                     if (!ragged) return;
+                     q.mend_a(steps - 1, g.width * 2);
+                     q.mend_b(steps - 1, g.width, scales, from.p);
+                 },
+                 [&](P &q) { q.multiply(acc); });
     }
 #pragma unroll
     for (int i = 0; i < RM; ++i)
@@ -348,163 +559,150 @@ __device__ __forceinline__ void up_rows(const FewArgs &g, uint32_t e, uint32_t n
     }
 }
 
-// RM: the most rows of 16 that the tokens fill. Most experts have no more than 16 of 64 tokens, so
-// larger tiles have the smallest one beside theirs.
+// The second kernel reads whole steps of h: what its rows have beyond the last column is 0.
+template <class T>
+__device__ __forceinline__ void clear_ends(const FewArgs &g, const uint16_t *rows, uint32_t count)
+{
+    const uint32_t wide = (uint32_t)(g.ldh / 2) - g.hidden;
+    for (uint32_t i = threadIdx.x; i < count * wide; i += 256)
+        ((T *)(g.h + rows[i / wide] * g.ldh))[g.hidden + i % wide] = (T)0.f;
+}
+
+// 16 RM pairs at a time; where there are more than 16 tokens, few experts have that many of them, so the
+// smallest tile stands beside the larger one.
 template <class T, class W, int RM, int FN, int DEEP>
 __global__ void __launch_bounds__(256) k_few_up(FewArgs g)
 {
     __shared__ Routes routes;
-    __shared__ uint16_t rows[kMostFew];
+    __shared__ uint16_t rows[4][16 * RM];
     __shared__ __align__(16) f32x4 sums[4 * RM * 2 * FN * 64];
     if (blockIdx.x == 0)
         for (uint32_t i = threadIdx.x; i < g.tiles; i += 256) g.arrived[i] = 0;
-    find_routes<false>(g, routes);
-    const uint32_t each = g.gated ? 16 * FN : 32 * FN;
-    const uint32_t tiles = (g.hidden + each - 1) / each;
+    const Router<16 * RM, false> router(g, routes);
+    const uint32_t each = g.gated ? 16 * FN : 32 * FN, tiles = (g.hidden + each - 1) / each;
     const uint32_t slot = blockIdx.x / tiles, n0 = blockIdx.x % tiles * each;
-    if (slot >= __builtin_amdgcn_readfirstlane(routes.count)) return;
-    const uint32_t e = __builtin_amdgcn_readfirstlane((uint32_t)routes.list[slot]);
-    // the pairs of the expert's tokens: of a token that has it twice, the first
-    const uint32_t lane = threadIdx.x % 64;
-    int pair = -1;
-    if (lane < g.tokens)
-        for (uint32_t j = g.top_k; j-- > 0;)
-            if (lds_ids()[lane * g.top_k + j] == (int)e) pair = (int)(lane * g.top_k + j);
-    const uint64_t mask = __ballot(pair >= 0);
-    if (threadIdx.x < 64 && pair >= 0)
-        rows[__popcll(mask & ((1ull << lane) - 1))] = (uint16_t)pair;
-    __syncthreads();
-    const uint32_t count = (uint32_t)__popcll(mask);
-    if (RM == 1 || count <= 16) up_rows<T, W, 1, FN, DEEP>(g, e, n0, rows, count, sums);
-    else up_rows<T, W, RM, FN, DEEP / 2>(g, e, n0, rows, count, sums);
+    if (slot >= router.count) return;
+    uint16_t *const mine = rows[__builtin_amdgcn_readfirstlane(threadIdx.x / 64)];
+    uint32_t e;
+    const uint32_t count = router.find(slot, mine, e);
+    if (n0 == 0 && (uint32_t)(g.ldh / 2) > g.hidden) clear_ends<T>(g, mine, count);
+    if (RM == 1 || count <= 16) up_rows<T, W, 1, FN, DEEP>(g, e, n0, mine, count, sums);
+    else up_rows<T, W, RM, FN, DEEP>(g, e, n0, mine, count, sums);
 }
 
 // ---------------------------------------------------------------------------
-// 16 FN columns of the result. The steps of all experts, one expert's after another's, go to the waves
-// of `splits` workgroups in turn; each adds up its own, a step's product times the token's weight for
-// the expert (and the column's scale), the workgroup's last one to arrive adds the workgroups' sums in
-// their order.
-// Lane l holds the scale of column l % 16; a result's column is at * 4 + c.
+// 16 FN columns of the result. The steps of all experts, one expert's after another's, are shared out
+// among the waves of `splits` workgroups, a run of them each, so that a wave meets few experts. When it
+// leaves one, it adds the rows' products times their weights (and the columns' scales) to its
+// own sums of the tokens in LDS. The workgroup that arrives last adds the workgroups' sums in their
+// order.
+
+// Lane l holds the scale of column l % 16; a result's column is 4 (l / 16) + c.
 __device__ __forceinline__ float column_scale(float scale, int c)
 {
     return __shfl(scale, threadIdx.x % 64 / 16 * 4 + c, 64);
 }
 
-template <class T, class W, int RM, int FN, int DEEP>
-__global__ void __launch_bounds__(256) k_few_down(FewArgs g)
+template <class T, class W, int RM, int FN, int DEEP, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64) k_few_down(FewArgs g)
 {
     constexpr bool kScales = std::is_same<W, int8_t>::value;
-    typedef Piece<T, W, RM, FN> Loads;
-    struct P : Loads {
-        float by[RM];
-        uint32_t has;  // bit i: the token of row i has the expert
-        float scale[kScales ? FN : 1];  // of column lane % 16
-    };
+    typedef Piece<T, W, RM, FN> P;
     __shared__ Routes routes;
-    __shared__ __align__(16) f32x4 sums[4 * RM * FN * 64];
+    __shared__ uint16_t rows[WAVES][16 * RM];
     __shared__ uint32_t last;
-    find_routes<true>(g, routes);
+    const Router<16 * RM, true> router(g, routes);
     const uint32_t lane = threadIdx.x % 64, at = lane / 16;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t tile = blockIdx.x % g.tiles, split = blockIdx.x / g.tiles;
     const uint32_t n0 = tile * 16 * FN, pairs = g.tokens * g.top_k;
-    const uint32_t steps = (row_bytes<W>(g.hidden) + kTurn - 1) / kTurn;
-    const uint32_t turn = g.splits * 4;
-    const uint32_t mine = pieces(__builtin_amdgcn_readfirstlane(routes.count) * steps,
-                                 split * 4 + wave, turn);
+    const uint32_t steps = P::steps(g.hidden);
+    const uint32_t all = router.count * steps;
+    const uint32_t first = share(all, split * WAVES + wave, g.splits * WAVES);
+    const uint32_t mine = share(all, split * WAVES + wave + 1, g.splits * WAVES) - first;
+    // the sums of each wave: [tokens, in 16s][FN][16], a row's four columns of a lane together
+    const uint32_t high = (g.tokens + 15) / 16;
+    f32x4 *const sums = (f32x4 *)(few_lds + ids_bytes(pairs) + by_bytes(pairs));
+    f32x4 *const total = sums + wave * high * FN * 64;
+    for (uint32_t i = lane; i < high * FN * 64; i += 64) total[i] = f32x4{};
 
-    // where the next piece is fetched from
-    uint32_t slot = 0, step = split * 4 + wave;
-    const char *a[RM], *b[FN], *powers[FN];
-    const char *scales = nullptr;
-    uint32_t columns[FN];
-    float by[RM];
-    uint32_t has = 0;
-    auto enter = [&] {
-        const uint32_t e = __builtin_amdgcn_readfirstlane((uint32_t)routes.list[slot]);
+    const Window tokens(g.h, pairs * (uint32_t)g.ldh);
+    for (uint32_t done = 0, some; done < mine; done += some) {
+        // some steps of one expert, the last one first: it may be ragged
+        const uint32_t slot = (first + done) / steps, from = (first + done) % steps;
+        some = steps - from < mine - done ? steps - from : mine - done;
+        uint32_t e;
+        const uint32_t count = router.find(slot, rows[wave], e);
+        const char *const scales = g.down.scales + (int64_t)e * g.down.scales_stride;
+        const Window powers(scales, g.down.window);
+        const Window columns(g.down.data + (int64_t)e * g.down.stride + (int64_t)n0 * g.down.ld);
+        typename P::Source source = {tokens, columns, columns, powers};
+        int pair[RM];  // of this lane's rows, -1: none
+#pragma unroll
+        for (int i = 0; i < RM; ++i) {
+            const uint32_t r = i * 16 + lane % 16;
+            pair[i] = r < count ? (int)rows[wave][r] : -1;
+            source.a[i] = r < count ? (uint32_t)pair[i] * (uint32_t)g.ldh : Window::kNowhere;
+        }
+        float scale[kScales ? FN : 1];  // of column lane % 16
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             uint32_t c = n0 + j * 16 + lane % 16;
             c = c < g.n ? c : g.n - 1;
-            b[j] = g.down.data + (int64_t)e * g.down.stride + (int64_t)c * g.down.ld + at * 16;
-            powers[j] = nullptr;
-            if constexpr (P::kPowers)
-                powers[j] = g.down.scales + (int64_t)e * g.down.scales_stride +
-                            (int64_t)c * g.down.ld_scales;
-            columns[j] = c * 4;
+            source.b[j] = (c - n0) * (uint32_t)g.down.ld;
+            source.p[j] = lane < 16 ? c * (uint32_t)g.down.ld_scales : Window::kNowhere;
+            if constexpr (kScales) scale[j] = ((const float *)scales)[c];
         }
-        if constexpr (kScales) scales = g.down.scales + (int64_t)e * g.down.scales_stride;
-        int pair[RM], any = 0;
-        has = 0;
+        f32x4 acc[RM][FN] = {};
+        P p[DEEP];
+        const bool ragged = P::ragged(g.hidden) && from + some == steps;
+        uint32_t next = from + some - 1;
+        auto fetch = [&](P &q) {
+            q.fetch(source, next);
+            next = next > from ? next - 1 : from;
+        };
+        pipeline(some, p,
+                 [&](P &q) {
+                     if (!ragged) return fetch(q);
+                     q.fetch_last(source, next, g.hidden, (uint32_t)g.ldh);
+                     next = next > from ? next - 1 : from;
+                 },
+                 fetch,
+                 [&](P &q) {
+                     if (ragged) q.mend_b(steps - 1, g.hidden, scales, source.p);
+                 },
+                 [&](P &q) { q.multiply(acc); });
 #pragma unroll
         for (int i = 0; i < RM; ++i) {
-            const uint32_t t = i * 16 + lane % 16;
-            pair[i] = -1;
-            by[i] = 0.f;
-            if (t < g.tokens)
-                for (uint32_t j = 0; j < g.top_k; ++j)
-                    if (lds_ids()[t * g.top_k + j] == (int)e) {
-                        pair[i] = pair[i] < 0 ? (int)(t * g.top_k + j) : pair[i];
-                        by[i] += lds_by(pairs)[t * g.top_k + j];
-                    }
-            const uint64_t found = __ballot(pair[i] >= 0);
-            if (found) any = __builtin_amdgcn_readlane(pair[i], __builtin_ctzll(found));
-            has |= pair[i] >= 0 ? 1u << i : 0;
+            const uint32_t p = pair[i] < 0 ? 0 : pair[i], token = p / g.top_k;
+            const float by = router.weight(p);
+            f32x4 v[FN];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                v[j] = acc[i][j] * by;
+                if constexpr (kScales)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[j][c] *= column_scale(scale[j], c);
+            }
+            f32x4 *const to = total + (token / 16 * FN * 4 + at) * 16 + token % 16;
+            auto add = [&] {
+#pragma unroll
+                for (int j = 0; j < FN; ++j) to[j * 64] += v[j];
+            };
+            // a token that has the expert twice is in two rows: these go one after another
+            const uint32_t before = (uint32_t)__shfl_up((int)token, 1, 64);
+            const bool twice = lane % 16 != 0 && pair[i] >= 0 && before == token;
+            if (__ballot(twice) == 0) {
+                if (pair[i] >= 0) add();
+            } else {
+                for (uint32_t r = 0; r < 16; ++r) {
+                    if (lane % 16 == r && pair[i] >= 0) add();
+                    __builtin_amdgcn_wave_barrier();
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
         }
-        // a token without the expert reads the row of one that has it, and leaves the product out
-#pragma unroll
-        for (int i = 0; i < RM; ++i)
-            a[i] = g.h + (int64_t)(pair[i] >= 0 ? pair[i] : any) * g.ldh + at * Loads::C * 16;
-    };
-    auto find = [&] {  // the step's expert
-        if (step < steps) return;
-        do {
-            step -= steps;
-            ++slot;
-        } while (step >= steps);
-        enter();
-    };
-    f32x4 total[RM][FN] = {};
-    if (mine) {
-        P p[DEEP];
-        uint32_t left = mine;
-        enter();
-        find();
-        pipeline(mine, p,
-                 [&](P &q) {
-                     q.fetch(a, b, powers, step, g.hidden);
-#pragma unroll
-                     for (int i = 0; i < RM; ++i) q.by[i] = by[i];
-                     q.has = has;
-                     if constexpr (kScales)
-#pragma unroll
-                         for (int j = 0; j < FN; ++j)
-                             q.scale[j] = *(const float *)(scales + columns[j]);
-                     if (left > 1) {
-                         --left;
-                         step += turn;
-                         find();
-                     }
-                 },
-                 [&](P &q) {
-                     f32x4 acc[RM][FN] = {};
-                     q.multiply(acc, g.hidden);
-#pragma unroll
-                     for (int i = 0; i < RM; ++i)
-#pragma unroll
-                         for (int j = 0; j < FN; ++j)
-#pragma unroll
-                             for (int c = 0; c < 4; ++c) {
-                                 float v = acc[i][j][c] * q.by[i];
-                                 if constexpr (kScales) v *= column_scale(q.scale[j], c);
-                                 total[i][j][c] += q.has >> i & 1 ? v : 0.f;
-                             }
-                 });
     }
-#pragma unroll
-    for (int i = 0; i < RM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) sums[(wave * RM * FN + i * FN + j) * 64 + lane] = total[i][j];
     __syncthreads();
     auto store = [&](uint32_t f, f32x4 v) {
         const uint32_t t = f / FN * 16 + lane % 16, c = n0 + f % FN * 16 + at * 4;
@@ -520,16 +718,16 @@ __global__ void __launch_bounds__(256) k_few_down(FewArgs g)
                 if (c + q < g.n) to[q] = o[q];
         }
     };
-    uint32_t *const parts = g.partial + (uint64_t)tile * g.splits * (RM * FN * 256);
-    for (uint32_t f = wave; f < RM * FN; f += 4) {
+    uint32_t *const parts = g.partial + (uint64_t)tile * g.splits * (high * FN * 256);
+    for (uint32_t f = wave; f < high * FN; f += WAVES) {
         f32x4 v = sums[f * 64 + lane];
 #pragma unroll
-        for (int w = 1; w < 4; ++w) v += sums[(w * RM * FN + f) * 64 + lane];
+        for (int w = 1; w < WAVES; ++w) v += sums[(w * high * FN + f) * 64 + lane];
         if (g.splits == 1) {
             store(f, v);
         } else {
             // written through to where every XCD sees it
-            uint32_t *to = parts + (split * RM * FN + f) * 256 + lane;
+            uint32_t *to = parts + (split * high * FN + f) * 256 + lane;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 __hip_atomic_store(to + q * 64, __float_as_uint(v[q]), __ATOMIC_RELAXED,
@@ -544,29 +742,61 @@ __global__ void __launch_bounds__(256) k_few_down(FewArgs g)
                                       __HIP_MEMORY_SCOPE_AGENT) == g.splits - 1;
     __syncthreads();
     if (!last) return;
-    for (uint32_t f = wave; f < RM * FN; f += 4) {
-        f32x4 v = {};
-        for (uint32_t s = 0; s < g.splits; ++s) {
-            const uint32_t *from = parts + (s * RM * FN + f) * 256 + lane;
+    // eight workgroups' sums on their way at one time
+    for (uint32_t i = threadIdx.x; i < high * FN * 256; i += WAVES * 64) {
+        float v = 0.f;
+        for (uint32_t s = 0; s < g.splits; s += 8) {
+            uint32_t part[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                v[q] += __uint_as_float(__hip_atomic_load(from + q * 64, __ATOMIC_RELAXED,
-                                                          __HIP_MEMORY_SCOPE_AGENT));
+            for (uint32_t q = 0; q < 8; ++q)
+                part[q] = __hip_atomic_load(
+                    parts + (uint64_t)(s + q < g.splits ? s + q : s) * high * FN * 256 + i,
+                    __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+            for (uint32_t q = 0; q < 8; ++q)
+                if (s + q < g.splits) v += __uint_as_float(part[q]);
         }
-        store(f, v);
+        ((float *)sums)[(i / 256 * 64 + i % 64) * 4 + i / 64 % 4] = v;
     }
+    __syncthreads();
+    for (uint32_t f = wave; f < high * FN; f += WAVES) store(f, sums[f * 64 + lane]);
 }
 
 // ---------------------------------------------------------------------------
-// Fragments of columns of a workgroup (FN): two where the weights are narrower than the tokens, whose
-// rows then count for more of what is loaded, if there are no more than 16 of them.
-template <class W, int RM> constexpr int few_columns() { return sizeof(W) == 2 || RM > 1 ? 1 : 2; }
+// Steps that a wave has on their way (four: 34.7 us instead of 33.1 for one token in 16 bits).
+constexpr int kDeep = 2;
+constexpr int kDownWaves = 8;  // of a workgroup of the second kernel
+
+// Fragments of columns of a workgroup (FN): two for 4-bit weights, whose tokens' rows count for more of what
+// is loaded, if there are no more than 16 of them (67 us instead of 70 for 16 tokens; 53 instead of 49 for
+// four tokens in 8 bits).
+template <class W, int RM> constexpr int few_columns()
+{
+    return std::is_same<W, Mx4>::value && RM == 1 ? 2 : 1;
+}
 inline uint32_t columns_of(int32_t kind, uint32_t rows)
 {
-    return kind == EXPERTS_WEIGHT_16 || rows > 1 ? 1 : 2;
+    return kind == EXPERTS_WEIGHT_MX4 && rows == 1 ? 2 : 1;
 }
 
-inline uint32_t rows_of_16(uint64_t tokens) { return tokens <= 16 ? 1 : tokens <= 32 ? 2 : 4; }
+// 16 pairs of an expert at a time for up to 16 tokens, 32 for more.
+inline uint32_t rows_of_16(uint64_t tokens) { return tokens <= 16 ? 1 : 2; }
+
+// Entries of the list that there can be.
+inline uint64_t most_slots(uint64_t pairs, uint32_t experts, uint32_t rows)
+{
+    const uint64_t some = pairs < experts ? pairs : experts;
+    return some + (pairs - some) / (16 * rows);
+}
+
+// Bytes of a row of h: whole steps of the second kernel.
+inline int64_t h_bytes(uint32_t hidden, int32_t down_kind)
+{
+    const uint32_t values = down_kind == EXPERTS_WEIGHT_16     ? Piece<__bf16, __bf16, 1, 1>::kValues
+                            : down_kind == EXPERTS_WEIGHT_INT8 ? Piece<__bf16, int8_t, 1, 1>::kValues
+                                                               : Piece<__bf16, Mx4, 1, 1>::kValues;
+    return ((int64_t)hidden + values - 1) / values * values * 2;
+}
 
 struct FewPlan {
     uint32_t rows, tiles, splits;  // of the result
@@ -580,70 +810,76 @@ inline FewPlan few_plan(uint64_t tokens, uint32_t top_k, uint32_t experts, uint3
     p.rows = rows_of_16(tokens);
     const uint32_t fn = columns_of(down_kind, p.rows);
     p.tiles = (n + 16 * fn - 1) / (16 * fn);
-    const uint64_t pairs = tokens * top_k, slots = pairs < experts ? pairs : experts;
+    const uint64_t pairs = tokens * top_k, slots = most_slots(pairs, experts, p.rows);
     const uint32_t bytes = down_kind == EXPERTS_WEIGHT_16     ? hidden * 2
                            : down_kind == EXPERTS_WEIGHT_INT8 ? hidden
                                                               : (hidden + 31) / 32 * 16;
-    // workgroups for 4 on each CU, if there are steps for them: 4 for each wave
-    const uint64_t steps = slots * ((bytes + kTurn - 1) / kTurn);
-    uint64_t splits = (1024 + p.tiles - 1) / p.tiles;
-    if (splits > steps / 16) splits = steps / 16;
-    p.splits = (uint32_t)(splits < 1 ? 1 : splits > 64 ? 64 : splits);
+    // The busiest of 256 CUs has ceil(tiles splits / 256) workgroups, each of 1 / splits of a tile's work, and
+    // a split costs some hundredth of it (128 tiles: two splits 33 us, four 34; 129 tiles: two splits 160 us,
+    // eight 123). Two steps of 128 bytes for each wave are the least.
+    const uint64_t steps = slots * ((bytes + 127) / 128) / (2 * kDownWaves);
+    const uint64_t most = p.tiles < 32 ? 256 / p.tiles : 8;
+    uint64_t best = UINT64_MAX;
+    p.splits = 1;
+    for (uint64_t s = 1; s <= (most < 64 ? most : 64) && (s == 1 || s <= steps); ++s) {
+        const uint64_t cost = (p.tiles * s + 255) / 256 * 100000 / s + 1000 * s;
+        if (cost < best) best = cost, p.splits = (uint32_t)s;
+    }
     auto up = [](uint64_t b) { return (b + 255) / 256 * 256; };
     p.h = 0;
-    p.arrived = up(pairs * ((hidden + 7) / 8 * 16));
+    p.arrived = up(pairs * h_bytes(hidden, down_kind));
     p.partial = p.arrived + up((uint64_t)p.tiles * 4);
-    p.bytes = p.partial + (p.splits > 1 ? (uint64_t)p.tiles * p.splits * p.rows * fn * 1024 : 0);
+    p.bytes = p.partial +
+              (p.splits > 1 ? (uint64_t)p.tiles * p.splits * ((tokens + 15) / 16) * fn * 1024 : 0);
     return p;
 }
 
 template <class T, class W, int RM>
 hist_status_t launch_up(const FewArgs &g, uint64_t slots, hipStream_t stream)
 {
-    constexpr int FN = few_columns<W, RM>(), DEEP = sizeof(W) == 2 ? 8 : 4;
+    constexpr int FN = few_columns<W, RM>();
     const uint32_t each = g.gated ? 16 * FN : 32 * FN;
-    return launch(k_few_up<T, W, RM, FN, DEEP>, slots * ((g.hidden + each - 1) / each), 256,
-                  (g.tokens * g.top_k * 2 + 15) / 16 * 16, stream, g);
+    return launch(k_few_up<T, W, RM, FN, kDeep>, slots * ((g.hidden + each - 1) / each), 256,
+                  ids_bytes(g.tokens * g.top_k), stream, g);
 }
 
 template <class T, class W>
 hist_status_t launch_up_any(const FewArgs &g, uint64_t slots, hipStream_t stream)
 {
     return g.tokens <= 16 ? launch_up<T, W, 1>(g, slots, stream)
-                          : launch_up<T, W, 4>(g, slots, stream);
+                          : launch_up<T, W, 2>(g, slots, stream);
 }
 
-template <class T, class W, int RM>
+template <class T, class W, int RM, int WAVES>
 hist_status_t launch_down(const FewArgs &g, hipStream_t stream)
 {
-    constexpr int FN = few_columns<W, RM>(), DEEP = (sizeof(W) == 2 ? 8 : 4) / (RM == 1 ? 1 : 2);
+    constexpr int FN = few_columns<W, RM>();
     const uint32_t pairs = g.tokens * g.top_k;
-    return launch(k_few_down<T, W, RM, FN, DEEP>, (uint64_t)g.tiles * g.splits, 256,
-                  (pairs * 2 + 15) / 16 * 16 + pairs * 4, stream, g);
+    return launch(k_few_down<T, W, RM, FN, kDeep, WAVES>, (uint64_t)g.tiles * g.splits, WAVES * 64,
+                  ids_bytes(pairs) + by_bytes(pairs) + WAVES * ((g.tokens + 15) / 16) * FN * 1024,
+                  stream, g);
 }
 
 template <class T, class W>
-hist_status_t launch_down_any(const FewArgs &g, uint32_t rows, hipStream_t stream)
+hist_status_t launch_down_any(const FewArgs &g, hipStream_t stream)
 {
-    return rows == 1   ? launch_down<T, W, 1>(g, stream)
-           : rows == 2 ? launch_down<T, W, 2>(g, stream)
-                       : launch_down<T, W, 4>(g, stream);
+    return g.tokens <= 16 ? launch_down<T, W, 1, kDownWaves>(g, stream)
+                          : launch_down<T, W, 2, kDownWaves>(g, stream);
 }
 
 template <class T>
 hist_status_t launch_few(const FewArgs &g, const FewPlan &p, int32_t up_kind, int32_t down_kind,
                          hipStream_t stream)
 {
-    const uint64_t pairs = (uint64_t)g.tokens * g.top_k;
-    const uint64_t slots = pairs < g.experts ? pairs : g.experts;
+    const uint64_t slots = most_slots((uint64_t)g.tokens * g.top_k, g.experts, p.rows);
     const hist_status_t st =
         up_kind == EXPERTS_WEIGHT_16     ? launch_up_any<T, T>(g, slots, stream)
         : up_kind == EXPERTS_WEIGHT_INT8 ? launch_up_any<T, int8_t>(g, slots, stream)
                                          : launch_up_any<T, Mx4>(g, slots, stream);
     if (st != HIST_OK) return st;
-    return down_kind == EXPERTS_WEIGHT_16     ? launch_down_any<T, T>(g, p.rows, stream)
-           : down_kind == EXPERTS_WEIGHT_INT8 ? launch_down_any<T, int8_t>(g, p.rows, stream)
-                                              : launch_down_any<T, Mx4>(g, p.rows, stream);
+    return down_kind == EXPERTS_WEIGHT_16     ? launch_down_any<T, T>(g, stream)
+           : down_kind == EXPERTS_WEIGHT_INT8 ? launch_down_any<T, int8_t>(g, stream)
+                                              : launch_down_any<T, Mx4>(g, stream);
 }
 
 // Defined in a source of their own each, so that they compile at one time.

@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import mx4_reference
-from partitioned_chip_accumulation_amd import experts
+from partitioned_chip_accumulation_amd import experts, hist
 from test_experts_gpu import normal, route
 
 pytestmark = pytest.mark.gpu
@@ -84,7 +84,7 @@ def case(seed, tokens, top_k, num, width, hidden, n, kind, dtype, gated, routing
 
 
 # tokens, top_k, experts, width, hidden, columns of the result
-SIZES = [(1, 1, 1, 1, 1, 1), (1, 8, 64, 128, 64, 128), (3, 2, 5, 7, 9, 11), (4, 2, 3, 33, 31, 70),
+SIZES = [(1, 1, 1, 16, 16, 1), (1, 8, 64, 128, 64, 128), (3, 2, 5, 17, 19, 11), (4, 2, 3, 33, 31, 70),
          (16, 4, 8, 256, 96, 200), (17, 2, 4, 130, 70, 90), (33, 3, 6, 512, 257, 300),
          (64, 8, 16, 264, 136, 520), (64, 2, 2, 100, 60, 40), (5, 2, 1024, 64, 32, 48),
          (64, 64, 64, 40, 24, 33), (2, 2, 3, 2050, 1337, 700), (1, 2, 4, 4096, 2048, 2048),
@@ -100,6 +100,21 @@ def test_layer(size, kind, dtype):
             args, values = case(sum(size), *size, kind, dtype, gated, routing)
             check(experts.few_tokens(*args, gated=gated),
                   *layer(*values, gated, 2 if kind == "mx4" and dtype == torch.float16 else 1))
+
+
+@pytest.mark.parametrize("kind", ["16", "mx4"])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_the_narrowest_layers(kind, dtype):
+    """16 bytes of a token's row and of h's are the least."""
+    for width, hidden in ((8, 8), (9, 15), (15, 9)):
+        args, values = case(12, 5, 2, 3, width, hidden, 7, kind, dtype, True)
+        check(experts.few_tokens(*args), *layer(*values, True, 2))
+    args, _ = case(12, 5, 2, 3, 7, 8, 7, kind, dtype, True)
+    with pytest.raises(hist.HistError):
+        experts.few_tokens(*args)
+    args, _ = case(12, 5, 2, 3, 15, 16, 7, "int8", dtype, True)
+    with pytest.raises(hist.HistError):
+        experts.few_tokens(*args)
 
 
 @pytest.mark.parametrize("up,down", [("16", "int8"), ("int8", "mx4"), ("mx4", "16")])
