@@ -86,7 +86,7 @@ extern "C" hist_status_t experts_product_preview(int32_t product, uint64_t rows,
         g.pa = g.pb = (const uint8_t *)at;
         g.ldpa = g.ldpb = (blocks + 15) / 16 * 16;
         g.pb_stride = g.ldpb * n;
-        return with_rows_kernel<false, true>(rows_kernel<false>(g), DescribeKernel{kernel});
+        return with_rows_kernel<false, true>(rows_kernel<false, true>(g), DescribeKernel{kernel});
     }
     return dx ? with_rows_kernel<true>(rows_kernel<true>(g), DescribeKernel{kernel})
               : with_rows_kernel<false>(rows_kernel<false>(g), DescribeKernel{kernel});

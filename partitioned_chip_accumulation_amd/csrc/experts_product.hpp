@@ -468,7 +468,8 @@ struct RowsParts {
     // again in what the waves' last loads have left.
     static constexpr bool kPowers = std::is_same<T, Mx4>::value;
     static constexpr int kWaves = S::THREADS / 64;
-    static constexpr uint32_t kPowerRows = (S::BM + 63) / 64 * 64;  // of A
+    static constexpr uint32_t kPowerRows = S::BM;  // of A
+    static_assert(!kPowers || (S::BM % 64 == 0 && S::BN % 64 == 0), "groups of 64 rows");
     static constexpr int kPowerLoads =
         kPowers ? ((kPowerRows + S::BN) / 32 + kWaves - 1) / kWaves : 0;
     static constexpr uint32_t kPowersAt = A::kBytes + B::kBytes;
@@ -916,24 +917,8 @@ __global__ void __launch_bounds__(256) k_rows_thin(RowsArgs g)
             b[j] = g.b + (int64_t)t.group * g.b_stride +
                    (int64_t)(n0 + (c < wide ? c : wide - 1)) * g.ldb + at;
         }
-        constexpr bool kPowers = std::is_same<T, Mx4>::value;
-        const uint8_t *pa[RM], *pb[FN];  // a row's eight powers of two go with a piece
-        if constexpr (kPowers) {
-#pragma unroll
-            for (int i = 0; i < RM; ++i) {
-                const uint32_t r = i * 16 + lane % 16;
-                pa[i] = g.pa + (int64_t)source_row(g, m0 + (r < high ? r : high - 1)) * g.ldpa;
-            }
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const uint32_t c = j * 16 + lane % 16;
-                pb[j] = g.pb + (int64_t)t.group * g.pb_stride +
-                        (int64_t)(n0 + (c < wide ? c : wide - 1)) * g.ldpb;
-            }
-        }
         struct Piece {
             u32x4 a[RM][2], b[FN][2];
-            uint32_t pa[kPowers ? RM : 1][2], pb[kPowers ? FN : 1][2];
         };
         // whole: the piece's 128 bytes lie in the rows
         auto fetch = [&](Piece &p, uint32_t from, auto whole) {
@@ -949,18 +934,6 @@ __global__ void __launch_bounds__(256) k_rows_thin(RowsArgs g)
                 for (int j = 0; j < FN; ++j) p.b[j][h] = one(b[j] + f);
 #pragma unroll
                 for (int i = 0; i < RM; ++i) p.a[i][h] = one(a[i] + f);
-                if constexpr (kPowers) {
-                    // this lane's block is number lane / 16 of four
-                    const uint32_t block = f / 16 + lane / 16;
-                    auto power = [&](const uint8_t *q) -> uint32_t {
-                        if constexpr (decltype(whole)::value) return q[block];
-                        else return left > 0 ? q[block] : 0;
-                    };
-#pragma unroll
-                    for (int j = 0; j < FN; ++j) p.pb[j][h] = power(pb[j]);
-#pragma unroll
-                    for (int i = 0; i < RM; ++i) p.pa[i][h] = power(pa[i]);
-                }
             }
         };
         auto multiply = [&](const Piece &p) {
@@ -970,14 +943,8 @@ __global__ void __launch_bounds__(256) k_rows_thin(RowsArgs g)
                 for (int i = 0; i < RM; ++i)
 #pragma unroll
                     for (int j = 0; j < FN; ++j)
-                        if constexpr (kPowers)
-                            acc[i][j] = Mma<T>::run(__builtin_bit_cast(Frag, p.b[j][h]),
-                                                    __builtin_bit_cast(Frag, p.a[i][h]),
-                                                    acc[i][j], p.pb[j][h], p.pa[i][h]);
-                        else
-                            acc[i][j] = Mma<T>::run(__builtin_bit_cast(Frag, p.b[j][h]),
-                                                    __builtin_bit_cast(Frag, p.a[i][h]),
-                                                    acc[i][j]);
+                        acc[i][j] = Mma<T>::run(__builtin_bit_cast(Frag, p.b[j][h]),
+                                                __builtin_bit_cast(Frag, p.a[i][h]), acc[i][j]);
         };
         constexpr uint32_t kTurn = 4 * kStepBytes;
         uint32_t from = wave * kStepBytes;
@@ -1123,7 +1090,23 @@ enum class RowsKernel {
     kVia256x128, kVia128x128, kVia64x64, kVia32x128                             // through registers
 };
 
-template <bool ACROSS>
+// 4-bit operands (POWERS), us for a product and its quantising where that is more than the calls' 20, else
+// of the product alone; 32 experts of 2560 x 2048, then a dense weight of 8192 x 4096 and 16 experts of
+// 4096 x 4096:
+//                     thin32  32x128  64x64  64x128  128x128  128x256  256x256
+//   rows   2 (alone)    23.2    14.0   15.3    14.1
+//   rows   8 (alone)    30.0    20.4   19.8    19.7
+//   rows  32            54.2    26.5   25.4    28.1     33.3     34.8     40.2
+//   rows  64            86.1    37.6   33.1    31.9     37.2     37.6     43.0
+//   rows 128             148    60.0   51.1    46.9     42.3     40.4     48.6
+//   dense, 1 (alone)    11.8    11.8    8.1    13.0
+//   dense, 64 (alone)   14.1    12.4    8.1    11.7
+//   dense, 1024          175    52.1   44.3    39.4     32.1     30.4     34.5
+//   16 experts, 128      208    90.4   75.9    64.2     69.2     66.1     51.7
+//   16 experts, 512      739     258    213     181      135      139      121
+// So 64 x 64 for few rows (the reduction is half as long as in 8 bits, and a wave that has it alone spends
+// more on powers than on codes), and one round of the largest tiles sooner.
+template <bool ACROSS, bool POWERS = false>
 RowsKernel rows_kernel(const RowsArgs &g)
 {
     typedef RowsKernel K;
@@ -1135,7 +1118,7 @@ RowsKernel rows_kernel(const RowsArgs &g)
     };
     // The thin kernels divide the reduction among waves, the others do not, so the choice between
     // them does not depend on alignment: a product's bits are the same at every address.
-    if (!ACROSS) {
+    if (!ACROSS && !POWERS) {
         if (each <= 6) return K::kThin16;
         if (tiles(64, 64) < (each <= 64 ? 256 : 128)) return K::kThin32;
     }
@@ -1148,6 +1131,9 @@ RowsKernel rows_kernel(const RowsArgs &g)
         // a short reduction has no use for stages, but for workgroups beside it (16384 rows, 8 experts,
         // 256 -> 2048: 31 us in 128 x 128, 37 in 256 x 256; 1024 -> 2048: 78 and 80)
         const bool brief = g.bytes <= 8 * kStepBytes;
+        if (POWERS && each <= 48) return K::k64x64;
+        if (POWERS && !brief && each >= 80 && tiles(256, 256) >= 160 && tiles(256, 256) <= 256)
+            return K::k256x256;
         if (!brief && each >= 224 && g.cols > 128 && tiles(256, 256) >= 256) return K::k256x256;
         if (!brief && each >= 80 && g.cols > 128 && tiles(128, 256) >= 384) return K::k128x256;
         // a workgroup on each CU at most: stages instead of a second one (8 bits, 8192 x 4096, 512
@@ -1163,7 +1149,7 @@ RowsKernel rows_kernel(const RowsArgs &g)
             return K::k256x256;
         if (each >= 80 && small >= 256) return K::k128x128;
         if (each > 40 && (ACROSS || tiles(64, 128) >= 256)) return K::k64x128;
-        if (ACROSS || (each <= 40 && tiles(32, 128) >= 256))
+        if (ACROSS || (!POWERS && each <= 40 && tiles(32, 128) >= 256))
             return brief ? K::k32x128Short : K::k32x128;
         return K::k64x64;
     }
@@ -1180,7 +1166,7 @@ template <class S, bool DIRECT> struct Tiles {};
 template <int RM, int FN, int DEEP> struct Thin {};
 
 // Calls f with what the kernel is made for.
-// POWERS: 4-bit operands, whose powers of two take another tenth of a stage.
+// POWERS: 4-bit operands.
 template <bool ACROSS, bool POWERS = false, class F>
 hist_status_t with_rows_kernel(RowsKernel kernel, const F &f)
 {
@@ -1189,36 +1175,36 @@ hist_status_t with_rows_kernel(RowsKernel kernel, const F &f)
     // the rows has a stage, or a workgroup, less (32 experts, 2560 -> 2048: 2 to 32 rows an expert
     // 62-64 us, 5.2-5.4 TB/s of weights, 40 rows 78; a fourth stage, which leaves one workgroup on
     // a CU, 62-66 and 82; 1344 -> 2048: 33-34 and 34-36. 64 rows, 64 x 128: 67 us).
-    typedef typename std::conditional<
-        ACROSS, Shape<32, 128, 2, 2, 2, 3>,
-        typename std::conditional<POWERS, Shape<32, 128, 1, 4, 2, 3>,
-                                  Shape<32, 128, 1, 4, 2, 4>>::type>::type Lowest;
+    typedef typename std::conditional<ACROSS, Shape<32, 128, 2, 2, 2, 3>,
+                                      Shape<32, 128, 1, 4, 2, 4>>::type Lowest;
     // (through registers, with 4-bit operands, larger tiles or fewer waves do not fit the registers)
     typedef typename std::conditional<POWERS, Shape<128, 128, 4, 2, 1>,
                                       Shape<128, 128, 2, 2, 2>>::type Via128;
     typedef typename std::conditional<POWERS, Via128, Shape<256, 128, 4, 2, 1>>::type Via256;
-    typedef typename std::conditional<
-        ACROSS, Shape<32, 128, 2, 2, 3>,
-        typename std::conditional<POWERS, Shape<32, 128, 1, 4, 3>,
-                                  Shape<32, 128, 1, 4, 4>>::type>::type LowestShort;
+    typedef typename std::conditional<ACROSS, Shape<32, 128, 2, 2, 3>,
+                                      Shape<32, 128, 1, 4, 4>>::type LowestShort;
     switch (kernel) {
     case K::k256x256: return f(Tiles<Shape<256, 256, 2, 4, 1>, true>());
     case K::k128x256: return f(Tiles<Shape<128, 256, 2, 4, 1, 3>, true>());
     case K::k128x128Alone: return f(Tiles<Shape<128, 128, 4, 2, 1, 4>, true>());
     case K::k128x128: return f(Tiles<Shape<128, 128, 2, 2, 2>, true>());
     case K::k64x128: return f(Tiles<Shape<64, 128, 2, 2, 2, 3>, true>());
-    case K::k32x128: return f(Tiles<Lowest, true>());
-    case K::k32x128Short: return f(Tiles<LowestShort, true>());
     case K::kVia256x128: return f(Tiles<Via256, false>());
     case K::kVia128x128: return f(Tiles<Via128, false>());
     default: break;
     }
+    if constexpr (!POWERS) {
+        if (kernel == K::k32x128) return f(Tiles<Lowest, true>());
+        if (kernel == K::k32x128Short) return f(Tiles<LowestShort, true>());
+    }
     if constexpr (ACROSS) {
         return f(Tiles<Shape<32, 128, 2, 2, 3>, false>());
     } else {
+        if constexpr (!POWERS) {
+            if (kernel == K::kThin16) return f(Thin<1, 1, 4>());
+            if (kernel == K::kThin32) return f(Thin<2, 4, 2>());
+        }
         switch (kernel) {
-        case K::kThin16: return f(Thin<1, 1, 4>());
-        case K::kThin32: return f(Thin<2, 4, 2>());
         case K::k64x64: return f(Tiles<Shape<64, 64, 2, 2, 3, 3>, true>());
         default: return f(Tiles<Shape<64, 64, 2, 2, 3>, false>());
         }
@@ -1244,8 +1230,9 @@ struct LaunchRows {
 template <class T, class O, bool ACROSS>
 hist_status_t launch_rows(const RowsArgs &g, hipStream_t stream)
 {
-    return with_rows_kernel<ACROSS, std::is_same<T, Mx4>::value>(
-        rows_kernel<ACROSS>(g), LaunchRows<T, O, ACROSS>{g, stream});
+    constexpr bool kPowers = std::is_same<T, Mx4>::value;
+    return with_rows_kernel<ACROSS, kPowers>(rows_kernel<ACROSS, kPowers>(g),
+                                             LaunchRows<T, O, ACROSS>{g, stream});
 }
 
 template <class T, bool DIRECT, class S>

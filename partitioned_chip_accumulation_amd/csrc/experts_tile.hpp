@@ -77,17 +77,8 @@ struct Mx4 {
 template <> struct Mma<Mx4> {
     typedef s32x4 Frag;
     typedef f32x4 Acc;
-    typedef int s32x8 __attribute__((ext_vector_type(8)));
-    // The lowest bytes of pa and pb: the exponents plus 127 (255: NaN) of the lane's blocks.
-    static __device__ __forceinline__ Acc run(Frag a, Frag b, Acc c, uint32_t pa, uint32_t pb)
-    {
-        const s32x8 x = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
-        const s32x8 y = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
-        // (4: four bits, of one sign, two exponent and one fraction bit)
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, (int)pa, 0,
-                                                                (int)pb);
-    }
-    // The same with byte A of pa and byte B of pb.
+    // Byte A of pa and byte B of pb: the exponents plus 127 (255: NaN) of the lane's blocks.
+    // (4: four bits, of one sign, two exponent and one fraction bit)
     template <int A, int B>
     static __device__ __forceinline__ void add(Frag a, Frag b, Acc &c, uint32_t pa, uint32_t pb)
     {
@@ -217,15 +208,13 @@ struct Powers {
         return load / 2 * 64 + lane % 4 * 16 + load % 2 * 8 + lane / 8;
     }
     static __device__ __forceinline__ uint32_t half_of() { return threadIdx.x / 4 % 2; }
-    // Byte i: the power of this lane's block of fragment i, N of them (1, 2 or 4) from row first on.
+    // Byte i: the power of this lane's block of fragment i, N of them (2 or 4) from row first on.
     template <int N>
     static __device__ __forceinline__ uint32_t read(const char *lds, uint32_t first, int kk)
     {
         const uint32_t lane = threadIdx.x % 64, at = lane / 16;
         const char *p = lds + first / 64 * 512 + lane % 16 * 32 + kk * 16 + first / 16 % 4 * 4;
-        if constexpr (N == 1) {
-            return *(const uint32_t *)p >> at * 8;
-        } else if constexpr (N == 2) {
+        if constexpr (N == 2) {
             typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
             const u32x2 v = *(const u32x2 *)p;
             return __builtin_amdgcn_perm(v[1], v[0], at | (at + 4) << 8);

@@ -2,15 +2,19 @@
 against values worked out by hand."""
 from __future__ import annotations
 
+import os
+import subprocess
+
 import numpy as np
 import pytest
 import torch
 
 import mx4_reference
-from partitioned_chip_accumulation_amd import experts
+from partitioned_chip_accumulation_amd import build, experts
 from test_experts_cpu import UNSUPPORTED, P, calls
 from test_experts_kernels_cpu import shape
 from test_experts_kernels_gpu import ROWS
+from test_experts_mfma_cpu import kernels, touched_too_early
 from test_experts_mx4_gpu import VIA, expected
 
 
@@ -50,8 +54,34 @@ def test_choice_of_kernels(name, size, want, _):
     assert shape(kernel) == expected(want)
 
 
+def test_every_kernel_has_a_size():
+    """As far as any of many sizes finds one."""
+    found = set()
+    for num in (1, 2, 8, 16, 64, 300):
+        for each in (1, 6, 20, 60, 100, 175, 500, 2000):
+            for n in (1, 40, 136, 500, 1344, 2600, 4104, 8200):
+                for k in (33, 320, 2080, 4160, 8192, 16448):
+                    for alignment in (2, 16):
+                        found.add(shape(experts.preview("mx4_matmul", each * num, num, n, k,
+                                                        alignment=alignment)))
+    assert found == {expected(c[2]) for c in ROWS + VIA}
+
+
+def test_sums_of_inline_matrix_instructions_are_left_alone(tmp_path):
+    """As in test_experts_mfma_cpu, which has the reason."""
+    if not os.path.exists(build.hipcc()):
+        pytest.skip("ROCm compiler not available")
+    out = tmp_path / "device.s"
+    subprocess.run([build.hipcc(), *build.HIPCC_FLAGS, "--cuda-device-only", "-S", "-I",
+                    build.INCLUDE, "-I", build.CSRC, os.path.join(build.CSRC, "experts_mx4.hip"),
+                    "-o", str(out)], check=True, capture_output=True)
+    results = {name: touched_too_early(code) for name, code in kernels(out.read_text()).items()}
+    assert sum(bool(count) for _, count in results.values()) == 16  # 8 kernels, two types
+    assert not {name: found[:5] for name, (found, _) in results.items() if found}
+
+
 def test_preview_of_the_dense_product():
-    assert shape(experts.preview("mx4_matmul", 1, 0, 8192, 4096)) == (16, 16, 0, 0)
+    assert shape(experts.preview("mx4_matmul", 1, 0, 8192, 4096)) == (64, 64, 3, 1)
     assert shape(experts.preview("mx4_matmul", 8192, 0, 8192, 4096)) == (256, 256, 2, 1)
 
 

@@ -23,8 +23,8 @@ VIA = [
 
 
 def expected(kernel):
-    """The kernel of the 4-bit product where the others take this one."""
-    return (32, 128, 3, 1) if kernel == (32, 128, 4, 1) else kernel
+    """The kernel of the 4-bit product where the others take this one: few rows of an expert have one."""
+    return (64, 64, 3, 1) if kernel[0] <= 32 else kernel
 
 
 def check_quantized(x):

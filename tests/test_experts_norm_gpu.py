@@ -95,7 +95,7 @@ def check_gradients(dy, h, weight, dh, eps=1e-5):
     want, size, want_w, size_w = gradients(dy, h, weight, dh, eps)
     # (r enters dx as its third power at most, and along has a sum of its own)
     assert_within(dx, want, half_step(want, dy.dtype) * 1.01 + size * ((2.5 * chain(n) + 20) * U))
-    # at most 4096 groups add rows / groups terms each; then 64 lanes add groups / 64 and 6 more
+    # the groups add rows / groups terms each; then 32 lanes add groups / 32 and 5 more
     terms = rows + 64 + 6
     assert_within(dweight, want_w, half_step(want_w, dy.dtype) * 1.01 +
                   size_w * ((chain(n) / 2 + 10 + terms) * U))
