@@ -251,9 +251,16 @@ struct Router {
 struct Window {
     __amdgpu_buffer_rsrc_t rsrc;
     static constexpr uint32_t kNowhere = 1u << 31, kMost = kNowhere - 1;
-    __device__ __forceinline__ Window(const char *base, uint32_t bytes = kMost)
+    __device__ __forceinline__ Window(const char *base, uint32_t bytes)
         : rsrc(__builtin_amdgcn_make_buffer_rsrc((void *)base, 0, bytes, 0x00027000))
     {
+    }
+    // The rows of a matrix from one on: `rows` of them, `bytes` each.
+    static __device__ __forceinline__ Window rows(const char *base, int64_t ld, uint32_t rows,
+                                                  uint32_t bytes)
+    {
+        const int64_t all = (int64_t)(rows - 1) * ld + bytes;
+        return Window(base, all < kMost ? (uint32_t)all : kMost);
     }
     __device__ __forceinline__ u32x4 load16(uint32_t place, uint32_t wave) const
     {
@@ -433,10 +440,10 @@ struct Piece {
     }
 };
 
-// `mine` pieces (one or more), DEEP of them on their way while the ones before are multiplied. fetch
-// stays at the last piece when it is asked for more: loads that come from the cache, in place of
-// branches around loads, at which the compiler would wait for all of them. first fetches the
-// first piece, and start is called for it when it is multiplied.
+// `mine` pieces (one or more), DEEP of them on their way while the ones before are multiplied. first
+// fetches the first piece, and start is called for it when it is multiplied. fetch stays at the last one when
+// it is asked for more: loads that come from the cache (or, of a ragged step, end with the window), in place
+// of branches around loads, at which the compiler would wait for all of them.
 template <int DEEP, class P, class O, class F, class S, class M>
 __device__ __forceinline__ void pipeline(uint32_t mine, P (&p)[DEEP], O first, F fetch, S start,
                                          M multiply)
@@ -479,7 +486,11 @@ __device__ __forceinline__ void up_rows(const FewArgs &g, uint32_t e, uint32_t n
     const char *const base = g.up.data + (int64_t)e * g.up.stride + (int64_t)n0 * g.up.ld;
     const char *const scales = g.up.scales + (int64_t)e * g.up.scales_stride;
     const Window tokens(g.x, (g.tokens - 1) * (uint32_t)g.ldx + g.width * 2), powers(scales, g.up.window);
-    const Window first(base), second(base + (g.gated ? (int64_t)g.hidden * g.up.ld : 0));
+    // (a gate's rows, and those of the other half)
+    const uint32_t others = g.gated ? g.hidden : 0, bytes = row_bytes<W>(g.width);
+    const Window first = Window::rows(base, g.up.ld, g.hidden + others - n0, bytes);
+    const Window second =
+        Window::rows(base + (int64_t)others * g.up.ld, g.up.ld, g.hidden - n0, bytes);
     typename P::Source from = {tokens, first, second, powers};
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
@@ -635,7 +646,9 @@ __global__ void __launch_bounds__(WAVES * 64) k_few_down(FewArgs g)
         const uint32_t count = router.find(slot, rows[wave], e);
         const char *const scales = g.down.scales + (int64_t)e * g.down.scales_stride;
         const Window powers(scales, g.down.window);
-        const Window columns(g.down.data + (int64_t)e * g.down.stride + (int64_t)n0 * g.down.ld);
+        const Window columns =
+            Window::rows(g.down.data + (int64_t)e * g.down.stride + (int64_t)n0 * g.down.ld, g.down.ld,
+                         g.n - n0, row_bytes<W>(g.hidden));
         typename P::Source source = {tokens, columns, columns, powers};
         int pair[RM];  // of this lane's rows, -1: none
 #pragma unroll
