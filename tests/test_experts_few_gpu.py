@@ -293,3 +293,13 @@ def test_a_decode_step_of_all_of_them(dtype):
     info = torch.finfo(dtype)
     assert ((product.double() - want).abs() <= want.abs() * (info.eps / 2 + 4 * 2.0**-24) +
             info.smallest_normal).all()
+
+
+def test_the_example_serves_by_every_road():
+    """Few tokens at once and a batch, in 8 and in 4 bits: by the size of a value's step (half of 1/127
+    of its row's largest one, about 4 of its standard deviations, in 8 bits: 1% of the norm; in 4
+    bits, with steps of a sixth at the least, some 12%), for one operand or two, twice."""
+    from test_experts_example_gpu import example
+    got = example().main(steps=2)
+    assert got["error"] < 0.05 and got["batch"] < 0.05
+    assert got["mx4"] < 0.3 and got["mx4_batch"] < 0.4
