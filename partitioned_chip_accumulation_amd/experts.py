@@ -27,6 +27,7 @@ library hist.HistError; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -119,6 +120,17 @@ def _call(name: str, device: torch.device, *args):
             status = _functions[name](*args, _raw_stream(index))
     if status:
         raise hist.HistError(status, name)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace(name: str, *sizes) -> int:
+    """Bytes of workspace for a call of these sizes."""
+    need = _u64()
+    _library()
+    status = _functions[name](*sizes, ctypes.byref(need))
+    if status:
+        raise hist.HistError(status, name)
+    return need.value
 
 
 class Groups(NamedTuple):
@@ -406,26 +418,29 @@ def mx4_matmul(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.T
     return y
 
 
-def _norm_inputs(x: torch.Tensor, weight: torch.Tensor, other: torch.Tensor | None, name: str,
-                 eps: float) -> tuple[int, int]:
-    """Checks what the norm takes; the leading dimensions of x and of a second matrix like it."""
-    ldx = _matrix(x, "x" if name == "residual" else "dy")
+def _like(t: torch.Tensor, name: str, x: torch.Tensor) -> int:
+    """Checks a matrix of x's shape and type and returns its leading dimension."""
+    ld = _matrix(t, name, (x.dtype,))
+    if t.shape != x.shape or t.device != x.device:
+        raise ValueError(f"{name} must have the shape {tuple(x.shape)} and be on {x.device}")
+    return ld
+
+
+def _norm_inputs(x: torch.Tensor, name: str, weight: torch.Tensor, eps: float) -> int:
+    """Checks what the norm takes and returns x's leading dimension."""
+    ldx = _matrix(x, name)
     _vector(weight, "weight", x.dtype, x.shape[1:], x.device)
     if not 1e-30 <= eps < float("inf"):
         raise ValueError("eps must be 1e-30 or more, and finite")
-    if other is None:
-        return ldx, 0
-    ld = _matrix(other, name, (x.dtype,))
-    if other.shape != x.shape or other.device != x.device:
-        raise ValueError(f"{name} must have the shape {tuple(x.shape)} and be on {x.device}")
-    return ldx, ld
+    return ldx
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
              eps: float = 1e-6) -> tuple[torch.Tensor, torch.Tensor]:
     """(y, h): h = x + residual in x's type (x itself without a residual), y = h / sqrt(mean h^2 + eps)
     times weight, row by row. weight is [n], of x's type."""
-    ldx, ldr = _norm_inputs(x, weight, residual, "residual", eps)
+    ldx = _norm_inputs(x, "x", weight, eps)
+    ldr = 0 if residual is None else _like(residual, "residual", x)
     rows, n = x.shape
     y = torch.empty(rows, n, dtype=x.dtype, device=x.device)
     h = x if residual is None else torch.empty(rows, n, dtype=x.dtype, device=x.device)
@@ -439,7 +454,8 @@ def rms_norm_int8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
                   eps: float = 1e-6) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(xq, sx, h): ``rms_norm`` with y in 8 bits and float32 scales of its rows, as ``int8_matmul``
     takes them. y is not rounded to x's type before."""
-    ldx, ldr = _norm_inputs(x, weight, residual, "residual", eps)
+    ldx = _norm_inputs(x, "x", weight, eps)
+    ldr = 0 if residual is None else _like(residual, "residual", x)
     rows, n = x.shape
     ldq = (n + 15) // 16 * 16
     xq = torch.empty(rows, ldq, dtype=torch.int8, device=x.device)
@@ -456,20 +472,17 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
                       eps: float = 1e-6) -> tuple[torch.Tensor, torch.Tensor]:
     """``rms_norm``'s gradients from dy, its h and the gradient dh that h gets from elsewhere:
     (dx, dweight). dx is the gradient of x and of the residual alike."""
-    lddy, ldh = _norm_inputs(dy, weight, h, "h", eps)
-    lddh = 0 if dh is None else _norm_inputs(dy, weight, dh, "dh", eps)[1]
+    lddy = _norm_inputs(dy, "dy", weight, eps)
+    ldh = _like(h, "h", dy)
+    lddh = 0 if dh is None else _like(dh, "dh", dy)
     rows, n = dy.shape
-    need = _u64()
-    _library()
-    status = _functions["experts_rms_norm_backward_workspace_size"](rows, n, ctypes.byref(need))
-    if status:
-        raise hist.HistError(status, "experts_rms_norm_backward_workspace_size")
+    need = _workspace("experts_rms_norm_backward_workspace_size", rows, n)
     dx = torch.empty(rows, n, dtype=dy.dtype, device=dy.device)
     dweight = torch.empty(n, dtype=dy.dtype, device=dy.device)
-    work = torch.empty(need.value, dtype=torch.uint8, device=dy.device)
+    work = torch.empty(need, dtype=torch.uint8, device=dy.device)
     _call("experts_rms_norm_backward", dy.device, dx.data_ptr(), n, dweight.data_ptr(),
           dy.data_ptr(), lddy, h.data_ptr(), ldh, None if dh is None else dh.data_ptr(), lddh,
-          weight.data_ptr(), rows, n, eps, _DTYPES[dy.dtype], work.data_ptr(), need.value)
+          weight.data_ptr(), rows, n, eps, _DTYPES[dy.dtype], work.data_ptr(), need)
     return dx, dweight
 
 
@@ -528,18 +541,13 @@ def few_tokens(x: torch.Tensor, up, down, ids: torch.Tensor, weights: torch.Tens
     hidden = rows // 2 if gated else rows
     second, (others, n, _) = _stack(down, "down", hidden, x)
     _same(experts, others, "the numbers of up's and down's experts")
-    need = _u64()
-    _library()
-    status = _functions["experts_few_tokens_workspace_size"](tokens, top_k, experts, hidden, n,
-                                                             second.kind, ctypes.byref(need))
-    if status:
-        raise hist.HistError(status, "experts_few_tokens_workspace_size")
+    need = _workspace("experts_few_tokens_workspace_size", tokens, top_k, experts, hidden, n,
+                      second.kind)
     out = torch.empty(tokens, n, dtype=x.dtype, device=device)
-    work = torch.empty(need.value, dtype=torch.uint8, device=device)
+    work = torch.empty(need, dtype=torch.uint8, device=device)
     _call("experts_few_tokens", device, out.data_ptr(), n, x.data_ptr(), ldx, ctypes.addressof(first),
           ctypes.addressof(second), ids.data_ptr(), ids.element_size() * 8, weights.data_ptr(), tokens,
-          top_k, experts, width, hidden, n, bool(gated), _DTYPES[x.dtype], work.data_ptr(),
-          need.value)
+          top_k, experts, width, hidden, n, bool(gated), _DTYPES[x.dtype], work.data_ptr(), need)
     return out
 
 
