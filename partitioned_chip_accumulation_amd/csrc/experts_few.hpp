@@ -21,6 +21,7 @@ namespace pca_experts {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr uint32_t kHalf = 64;  // bytes of a row that one load of a wave takes
+constexpr uint32_t kStep = 2 * kHalf;  // what the second kernel's waves share out
 
 struct FewWeight {
     const char *data;
@@ -32,21 +33,23 @@ struct FewWeight {
 struct FewArgs {
     char *out;
     const char *x;
-    char *h;            // [pairs][ldh]
+    char *h;            // (see Rows)
     uint32_t *arrived;  // [tiles of the result]
     uint32_t *partial;
     FewWeight up, down;
     const void *ids;
     const float *by;
     int64_t ldo, ldx, ldh;  // bytes
-    uint32_t ids64, gated, tokens, top_k, experts, width, hidden, n;
+    uint32_t ids64, gated, h_fp16, h_shift, tokens, top_k, experts, width, hidden, n;
     uint32_t tiles, splits;  // of the result
 };
 
-// How weights of type W go with tokens of type T: C fragments of a lane's 16 bytes.
+// How weights of type W go with tokens of type T, and with the parts of h, of type H: C fragments of a
+// lane's 16 bytes.
 template <class T, class W> struct Widen;
 template <class T> struct Widen<T, T> {
     static constexpr int C = 1;
+    typedef T H;
     typedef typename Vec8<T>::type Frag;
     static __device__ __forceinline__ Frag frag(u32x4 v, int, uint32_t)
     {
@@ -59,6 +62,7 @@ template <class T> struct Widen<T, T> {
 };
 template <class T> struct Widen<T, int8_t> {
     static constexpr int C = 2;
+    typedef T H;
     typedef typename Vec8<T>::type Frag;
     static __device__ __forceinline__ Frag frag(u32x4 v, int c, uint32_t)
     {
@@ -76,6 +80,7 @@ template <class T> struct Widen<T, int8_t> {
 // A block's values as bfloat16, whose exponents reach as far as the powers of two.
 template <class T> struct Widen<T, Mx4> {
     static constexpr int C = 4;
+    typedef __bf16 H;
     typedef bf16x8 Frag;
     static __device__ __forceinline__ Frag frag(u32x4 v, int c, uint32_t power)
     {
@@ -124,7 +129,7 @@ __device__ __host__ __forceinline__ uint32_t row_bytes(uint32_t k)
 // in the order of the experts' first pairs. More pairs go through LDS, where the slots come in the order of
 // the experts' numbers.
 struct Routes {
-    uint32_t many[EXPERTS_MAX_EXPERTS];  // pairs of each expert
+    uint32_t many[EXPERTS_MAX_EXPERTS];  // pairs of each expert; then of those before it
     uint32_t count;
     // expert, and which kRows of its pairs << 16 (there are as many as experts, and one more for each 16 of
     // the other pairs)
@@ -189,22 +194,29 @@ struct Router {
         __syncthreads();
         if (threadIdx.x < 64) {
             const uint32_t each = (g.experts + 63) / 64, first = lane * each;
-            uint32_t mine = 0;
-            for (uint32_t e = first; e < first + each && e < g.experts; ++e)
+            uint32_t mine = 0, of = 0;
+            for (uint32_t e = first; e < first + each && e < g.experts; ++e) {
                 mine += (routes.many[e] + kRows - 1) / kRows;
+                of += routes.many[e];
+            }
             const uint32_t upto = wave_inclusive_scan(mine);
-            uint32_t at = upto - mine;
-            for (uint32_t e = first; e < first + each && e < g.experts; ++e)
-                for (uint32_t q = 0; q * kRows < routes.many[e]; ++q)
-                    routes.list[at++] = e | q << 16;
+            uint32_t at = upto - mine, before = wave_inclusive_scan(of) - of;
+            for (uint32_t e = first; e < first + each && e < g.experts; ++e) {
+                const uint32_t many = routes.many[e];
+                for (uint32_t q = 0; q * kRows < many; ++q) routes.list[at++] = e | q << 16;
+                routes.many[e] = before;
+                before += many;
+            }
             if (lane == 63) routes.count = upto;
         }
         __syncthreads();
         count = __builtin_amdgcn_readfirstlane(routes.count);
     }
 
-    // The expert of a slot, and its pairs to `rows` (the wave's own kRows places); returns how many.
-    __device__ __forceinline__ uint32_t find(uint32_t slot, uint16_t *rows, uint32_t &expert) const
+    // The expert of a slot, its pairs to `rows` (the wave's own kRows places) and how many pairs the experts
+    // and slots before it have; returns how many it has.
+    __device__ __forceinline__ uint32_t find(uint32_t slot, uint16_t *rows, uint32_t &expert,
+                                             uint32_t &before) const
     {
         const uint32_t lane = threadIdx.x % 64;
         const uint64_t below = (1ull << lane) - 1;
@@ -217,10 +229,15 @@ struct Router {
             const bool mine = id == (int)expert && rank - first < kRows;
             if (mine) rows[rank - first] = (uint16_t)lane;
             seen = (uint32_t)__popcll(__ballot(mine));
+            // (the experts' order is that of their first pairs)
+            const int own = __builtin_ctzll(same | 1ull << 63);
+            before = first + (uint32_t)__popcll(
+                                 __ballot(id >= 0 && own < __builtin_amdgcn_readlane(own, at)));
         } else {
             const uint32_t what = __builtin_amdgcn_readfirstlane(routes.list[slot]);
             const uint32_t skip = (what >> 16) * kRows;
             expert = what & 0xffff;
+            before = __builtin_amdgcn_readfirstlane(routes.many[expert]) + skip;
             for (uint32_t i = 0; i < pairs && seen < skip + kRows; i += 64) {
                 const bool here = i + lane < pairs && lds_ids()[i + lane] == (int)expert;
                 const uint64_t mask = __ballot(here);
@@ -290,7 +307,9 @@ struct Window {
 // No load of a weight leaves its row: at the row's end a lane's 16 bytes are the last ones of the row,
 // to be shifted (mend) before they are multiplied. The code is kept short: a pass over other experts' weights
 // leaves none of it in the caches, and kernels of 50 KB took 8 us for next to no work.
-template <class T, class W, int RM, int FB>
+//
+// OF_H: the tokens' rows are those of h, which lie as Rows has them.
+template <class T, class W, int RM, int FB, bool OF_H = false>
 struct Piece {
     typedef Widen<T, W> By;
     static constexpr int C = By::C;
@@ -328,6 +347,7 @@ struct Piece {
         const Window &tokens, &first, &second;  // b's fragments below FB / 2 (or 1) lie in the first
         const Window &powers;
         uint32_t a[RM], b[FB], p[FB];  // of rows; kNowhere: none
+        uint32_t unit;                 // of h: bytes of what goes with one fragment
         __device__ __forceinline__ const Window &of(int j) const
         {
             return j < (FB + 1) / 2 ? first : second;
@@ -346,6 +366,7 @@ struct Piece {
 #pragma unroll
             for (int j = 0; j < FB; ++j)
                 power[j] = s.powers.template load<kStepPowers>(s.p[j], step * kStepPowers);
+        if constexpr (OF_H) return fetch_h(s, step);
 #pragma unroll
         for (int h = 0; h < kHalves; ++h)
 #pragma unroll
@@ -353,11 +374,20 @@ struct Piece {
 #pragma unroll
                 for (int i = 0; i < RM; ++i)
                     a[i][h][c] = s.tokens.load16(s.a[i] + lane * C * 16 + (h * 4 * C + c) * 16,
-                                                 step * kValues * 2);
+                                                    step * kValues * 2);
     }
-    // The last step, of rows of k values, a's of `room` bytes.
-    __device__ __forceinline__ void fetch_last(const Source &s, uint32_t step, uint32_t k,
-                                               uint32_t room)
+    __device__ __forceinline__ void fetch_h(const Source &s, uint32_t step)
+    {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int i = 0; i < RM; ++i)
+                    a[i][h][c] = s.tokens.load16(s.a[i], ((step * kHalves + h) * C + c) * s.unit);
+    }
+    // The last step, of rows of k values.
+    __device__ __forceinline__ void fetch_last(const Source &s, uint32_t step, uint32_t k)
     {
         const uint32_t bytes = row_bytes<W>(k);
 #pragma unroll
@@ -370,6 +400,8 @@ struct Piece {
 #pragma unroll
             for (int j = 0; j < FB; ++j)
                 power[j] = s.powers.template load<kStepPowers>(s.p[j] + place_p(step, bytes / 16), 0);
+        if constexpr (OF_H) return fetch_h(s, step);
+        const uint32_t room = k * 2;
 #pragma unroll
         for (int h = 0; h < kHalves; ++h)
 #pragma unroll
@@ -434,7 +466,15 @@ struct Piece {
                 for (int c = 0; c < C; ++c) {
                     const auto w = By::frag(b[j][h], c, own);
 #pragma unroll
-                    for (int i = 0; i < RM; ++i) By::add(w, a[i][h][c], acc[i][j]);
+                    for (int i = 0; i < RM; ++i) {
+                        if constexpr (OF_H) {
+                            typedef typename By::H H;
+                            acc[i][j] = Mma<H>::run(
+                                w, __builtin_bit_cast(typename Vec8<H>::type, a[i][h][c]), acc[i][j]);
+                        } else {
+                            By::add(w, a[i][h][c], acc[i][j]);
+                        }
+                    }
                 }
             }
     }
@@ -470,6 +510,66 @@ __device__ __forceinline__ uint32_t share(uint32_t count, uint32_t at, uint32_t 
     return (uint32_t)((uint64_t)count * at / of);
 }
 
+// h of a slot, in two parts of 16 bits, what 16 bits hold of it and of the rest: two rows for a pair, first all
+// pairs' first parts, then their second ones. (Rounded to one part, h added as much to the result's error as
+// the result's own rounding. A slot of up to 8 pairs, the usual one, still has no more than the 16 rows
+// that the matrix instructions take.) They lie in the order in which the second kernel's lanes
+// take them: for each 64 bytes of a weight's row (32 columns, or 64 and 128 of narrower weights) and each 8
+// columns that a lane's 16 bytes of them go with, the 16 bytes of every row for lanes 0 to 15, those
+// for lanes 16 to 31, and so on: 16 rows are 1 KB in one piece, 16 accesses instead of 64.
+struct Rows {
+    char *const base;
+    const uint32_t count, shift;  // 2^shift fragments of columns go with 16 bytes of a weight
+    __device__ __forceinline__ Rows(const FewArgs &g, uint32_t before, uint32_t count)
+        : base(g.h + (int64_t)before * 2 * g.ldh), count(count), shift(g.h_shift)
+    {
+    }
+    __device__ __forceinline__ uint32_t unit() const { return count * 128; }
+    __device__ __forceinline__ uint32_t part() const { return count * 16; }
+    // The place of a column of a pair, of its first part.
+    __device__ __forceinline__ char *at(uint32_t row, uint32_t c) const
+    {
+        const uint32_t units = (c >> (5 + shift) << shift) + (c >> 3 & ((1u << shift) - 1));
+        const uint32_t lanes = c >> (3 + shift) & 3;
+        return base + units * unit() + (lanes * 2 * count + row) * 16 + c % 8 * 2;
+    }
+    // Four columns, of which `left` exist.
+    template <class H>
+    __device__ __forceinline__ void store(uint32_t row, uint32_t c, f32x4 v, uint32_t left) const
+    {
+        typedef H H4 __attribute__((ext_vector_type(4)));
+        H4 high, low;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            high[q] = (H)v[q];
+            const float first = (float)high[q];
+            low[q] = (H)(__builtin_isfinite(first) ? v[q] - first : 0.f);  // (no NaN of an infinity)
+        }
+        char *const to = at(row, c);
+        if (left >= 4) {
+            *(H4 *)to = high;
+            *(H4 *)(to + part()) = low;
+        } else {
+#pragma unroll
+            for (uint32_t q = 0; q < 3; ++q)
+                if (q < left) {
+                    ((H *)to)[q] = high[q];
+                    ((H *)(to + part()))[q] = low[q];
+                }
+        }
+    }
+    // The second kernel reads whole steps: what the rows have from column `hidden` to `end` is 0.
+    __device__ __forceinline__ void clear(uint32_t hidden, uint32_t end) const
+    {
+        const uint32_t wide = end - hidden;
+        for (uint32_t i = threadIdx.x; i < count * wide; i += blockDim.x) {
+            char *const to = at(i / wide, hidden + i % wide);
+            *(uint16_t *)to = 0;
+            *(uint16_t *)(to + part()) = 0;
+        }
+    }
+};
+
 // ---------------------------------------------------------------------------
 // Columns of h for one expert, 16 FN of them with a gate (FN fragments of its rows, then FN of the
 // others) and 32 FN without, its tokens 16 RM at a time. The four waves divide the reduction, they take
@@ -477,10 +577,11 @@ __device__ __forceinline__ uint32_t share(uint32_t count, uint32_t at, uint32_t 
 // instead of 49 for four in 8).
 template <class T, class W, int RM, int FN, int DEEP>
 __device__ __forceinline__ void up_rows(const FewArgs &g, uint32_t e, uint32_t n0,
-                                        const uint16_t *rows, uint32_t count, f32x4 *sums)
+                                        const uint16_t *rows, const Rows &h, f32x4 *sums)
 {
     constexpr int FB = 2 * FN;
     typedef Piece<T, W, RM, FB> P;
+    const uint32_t count = h.count;
     const uint32_t lane = threadIdx.x % 64, at = lane / 16;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const char *const base = g.up.data + (int64_t)e * g.up.stride + (int64_t)n0 * g.up.ld;
@@ -491,7 +592,7 @@ __device__ __forceinline__ void up_rows(const FewArgs &g, uint32_t e, uint32_t n
     const Window first = Window::rows(base, g.up.ld, g.hidden + others - n0, bytes);
     const Window second =
         Window::rows(base + (int64_t)others * g.up.ld, g.up.ld, g.hidden - n0, bytes);
-    typename P::Source from = {tokens, first, second, powers};
+    typename P::Source from = {tokens, first, second, powers, {}, {}, {}, 0};
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
         const uint32_t r = i * 16 + lane % 16;
@@ -519,7 +620,7 @@ __device__ __forceinline__ void up_rows(const FewArgs &g, uint32_t e, uint32_t n
         pipeline((steps - wave + 3) / 4, p,
                  [&](P &q) {
                      if (!ragged) return fetch(q);
-                     q.fetch_last(from, next, g.width, g.width * 2);
+                     q.fetch_last(from, next, g.width);
                      next = next < 4 ? next : next - 4;
                  },
                  fetch,
@@ -556,27 +657,9 @@ __device__ __forceinline__ void up_rows(const FewArgs &g, uint32_t e, uint32_t n
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = v[q] / (1.f + expf(-v[q]));
         if (g.gated) v *= sum(FN + j, g.hidden + c);
-        // h is rounded to the tokens' type here, as the rows between two separate products are.
-        T *to = (T *)(g.h + rows[r] * g.ldh) + c;
-        typedef T T4 __attribute__((ext_vector_type(4)));
-        const T4 o = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
-        if (c + 4 <= g.hidden) {
-            store_any(to, o);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 3; ++q)
-                if (c + q < g.hidden) to[q] = o[q];
-        }
+        if (std::is_same<T, _Float16>::value && g.h_fp16) h.template store<_Float16>(r, c, v, g.hidden - c);
+        else h.template store<__bf16>(r, c, v, g.hidden - c);
     }
-}
-
-// The second kernel reads whole steps of h: what its rows have beyond the last column is 0.
-template <class T>
-__device__ __forceinline__ void clear_ends(const FewArgs &g, const uint16_t *rows, uint32_t count)
-{
-    const uint32_t wide = (uint32_t)(g.ldh / 2) - g.hidden;
-    for (uint32_t i = threadIdx.x; i < count * wide; i += 256)
-        ((T *)(g.h + rows[i / wide] * g.ldh))[g.hidden + i % wide] = (T)0.f;
 }
 
 // 16 RM pairs at a time; where there are more than 16 tokens, few experts have that many of them, so the
@@ -594,11 +677,12 @@ __global__ void __launch_bounds__(256) k_few_up(FewArgs g)
     const uint32_t slot = blockIdx.x / tiles, n0 = blockIdx.x % tiles * each;
     if (slot >= router.count) return;
     uint16_t *const mine = rows[__builtin_amdgcn_readfirstlane(threadIdx.x / 64)];
-    uint32_t e;
-    const uint32_t count = router.find(slot, mine, e);
-    if (n0 == 0 && (uint32_t)(g.ldh / 2) > g.hidden) clear_ends<T>(g, mine, count);
-    if (RM == 1 || count <= 16) up_rows<T, W, 1, FN, DEEP>(g, e, n0, mine, count, sums);
-    else up_rows<T, W, RM, FN, DEEP>(g, e, n0, mine, count, sums);
+    uint32_t e, before;
+    const uint32_t count = router.find(slot, mine, e, before);
+    const Rows h(g, before, count);
+    if (n0 == 0 && (uint32_t)(g.ldh / 2) > g.hidden) h.clear(g.hidden, (uint32_t)(g.ldh / 2));
+    if (RM == 1 || count <= 16) up_rows<T, W, 1, FN, DEEP>(g, e, n0, mine, h, sums);
+    else up_rows<T, W, RM, FN, DEEP>(g, e, n0, mine, h, sums);
 }
 
 // ---------------------------------------------------------------------------
@@ -614,11 +698,107 @@ __device__ __forceinline__ float column_scale(float scale, int c)
     return __shfl(scale, threadIdx.x % 64 / 16 * 4 + c, 64);
 }
 
+// Some steps of one slot, the last one first: it may be ragged. R fragments hold the rows of h, two for a pair.
+template <class T, class W, int R, int FN, int DEEP, class O>
+__device__ __forceinline__ void down_rows(const FewArgs &g, const O &router, uint32_t e, uint32_t n0,
+                                          uint32_t from, uint32_t some, const uint16_t *rows,
+                                          const Rows &h, f32x4 *total)
+{
+    constexpr bool kScales = std::is_same<W, int8_t>::value;
+    typedef Piece<T, W, R, FN, true> P;
+    // (the steps that are shared out are two of a piece of one half)
+    const uint32_t steps = P::steps(g.hidden);
+    if constexpr (P::kHalves == 1) {
+        from *= 2;
+        some = 2 * some < steps - from ? 2 * some : steps - from;
+    }
+    const uint32_t lane = threadIdx.x % 64, at = lane / 16, count = h.count;
+    const Window tokens(h.base, count * 2 * (uint32_t)g.ldh);
+    const char *const scales = g.down.scales + (int64_t)e * g.down.scales_stride;
+    const Window powers(scales, g.down.window);
+    const Window columns =
+        Window::rows(g.down.data + (int64_t)e * g.down.stride + (int64_t)n0 * g.down.ld, g.down.ld,
+                     g.n - n0, row_bytes<W>(g.hidden));
+    typename P::Source source = {tokens, columns, columns, powers, {}, {}, {}, h.unit()};
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const uint32_t r = i * 16 + lane % 16;
+        source.a[i] = r < 2 * count ? (at * 2 * count + r) * 16 : Window::kNowhere;
+    }
+    float scale[kScales ? FN : 1];  // of column lane % 16
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        uint32_t c = n0 + j * 16 + lane % 16;
+        c = c < g.n ? c : g.n - 1;
+        source.b[j] = (c - n0) * (uint32_t)g.down.ld;
+        source.p[j] = lane < 16 ? c * (uint32_t)g.down.ld_scales : Window::kNowhere;
+        if constexpr (kScales) scale[j] = ((const float *)scales)[c];
+    }
+    f32x4 acc[R][FN] = {};
+    P p[DEEP];
+    const bool ragged = P::ragged(g.hidden) && from + some == steps;
+    uint32_t next = from + some - 1;
+    auto fetch = [&](P &q) {
+        q.fetch(source, next);
+        next = next > from ? next - 1 : from;
+    };
+    pipeline(some, p,
+             [&](P &q) {
+                 if (!ragged) return fetch(q);
+                 q.fetch_last(source, next, g.hidden);
+                 next = next > from ? next - 1 : from;
+             },
+             fetch,
+             [&](P &q) {
+                 if (ragged) q.mend_b(steps - 1, g.hidden, scales, source.p);
+             },
+             [&](P &q) { q.multiply(acc); });
+#pragma unroll
+    for (int i = 0; i < (R + 1) / 2; ++i) {
+        const uint32_t r = i * 16 + lane % 16, pair = r < count ? rows[r] : 0, token = pair / g.top_k;
+        const float by = router.weight(pair);
+        f32x4 v[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                // the second part's row is in this fragment or a later one
+                float rest = 0.f;
+#pragma unroll
+                for (int q = i; q < R; ++q) {
+                    const float other =
+                        __shfl(acc[q][j][c], (int)(lane / 16 * 16 + (lane + count) % 16), 64);
+                    if ((r + count) / 16 == (uint32_t)q) rest = other;
+                }
+                // (of an infinite weight times a pair's two parts the first one counts)
+                v[j][c] = acc[i][j][c];
+                if (__builtin_isfinite(v[j][c])) v[j][c] += rest;
+                v[j][c] *= by;
+                if constexpr (kScales) v[j][c] *= column_scale(scale[j], c);
+            }
+        f32x4 *const to = total + (token / 16 * FN * 4 + at) * 16 + token % 16;
+        auto add = [&] {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) to[j * 64] += v[j];
+        };
+        // a token that has the expert twice is in two rows: these go one after another
+        const uint32_t before = (uint32_t)__shfl_up((int)token, 1, 64);
+        const bool twice = lane % 16 != 0 && r < count && before == token;
+        if (__ballot(twice) == 0) {
+            if (r < count) add();
+        } else {
+            for (uint32_t q = 0; q < 16; ++q) {
+                if (lane % 16 == q && r < count) add();
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 template <class T, class W, int RM, int FN, int DEEP, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64) k_few_down(FewArgs g)
 {
-    constexpr bool kScales = std::is_same<W, int8_t>::value;
-    typedef Piece<T, W, RM, FN> P;
     __shared__ Routes routes;
     __shared__ uint16_t rows[WAVES][16 * RM];
     __shared__ uint32_t last;
@@ -627,7 +807,7 @@ __global__ void __launch_bounds__(WAVES * 64) k_few_down(FewArgs g)
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t tile = blockIdx.x % g.tiles, split = blockIdx.x / g.tiles;
     const uint32_t n0 = tile * 16 * FN, pairs = g.tokens * g.top_k;
-    const uint32_t steps = P::steps(g.hidden);
+    const uint32_t steps = (row_bytes<W>(g.hidden) + kStep - 1) / kStep;
     const uint32_t all = router.count * steps;
     const uint32_t first = share(all, split * WAVES + wave, g.splits * WAVES);
     const uint32_t mine = share(all, split * WAVES + wave + 1, g.splits * WAVES) - first;
@@ -637,84 +817,17 @@ __global__ void __launch_bounds__(WAVES * 64) k_few_down(FewArgs g)
     f32x4 *const total = sums + wave * high * FN * 64;
     for (uint32_t i = lane; i < high * FN * 64; i += 64) total[i] = f32x4{};
 
-    const Window tokens(g.h, pairs * (uint32_t)g.ldh);
     for (uint32_t done = 0, some; done < mine; done += some) {
         // some steps of one expert, the last one first: it may be ragged
         const uint32_t slot = (first + done) / steps, from = (first + done) % steps;
         some = steps - from < mine - done ? steps - from : mine - done;
-        uint32_t e;
-        const uint32_t count = router.find(slot, rows[wave], e);
-        const char *const scales = g.down.scales + (int64_t)e * g.down.scales_stride;
-        const Window powers(scales, g.down.window);
-        const Window columns =
-            Window::rows(g.down.data + (int64_t)e * g.down.stride + (int64_t)n0 * g.down.ld, g.down.ld,
-                         g.n - n0, row_bytes<W>(g.hidden));
-        typename P::Source source = {tokens, columns, columns, powers};
-        int pair[RM];  // of this lane's rows, -1: none
-#pragma unroll
-        for (int i = 0; i < RM; ++i) {
-            const uint32_t r = i * 16 + lane % 16;
-            pair[i] = r < count ? (int)rows[wave][r] : -1;
-            source.a[i] = r < count ? (uint32_t)pair[i] * (uint32_t)g.ldh : Window::kNowhere;
-        }
-        float scale[kScales ? FN : 1];  // of column lane % 16
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            uint32_t c = n0 + j * 16 + lane % 16;
-            c = c < g.n ? c : g.n - 1;
-            source.b[j] = (c - n0) * (uint32_t)g.down.ld;
-            source.p[j] = lane < 16 ? c * (uint32_t)g.down.ld_scales : Window::kNowhere;
-            if constexpr (kScales) scale[j] = ((const float *)scales)[c];
-        }
-        f32x4 acc[RM][FN] = {};
-        P p[DEEP];
-        const bool ragged = P::ragged(g.hidden) && from + some == steps;
-        uint32_t next = from + some - 1;
-        auto fetch = [&](P &q) {
-            q.fetch(source, next);
-            next = next > from ? next - 1 : from;
-        };
-        pipeline(some, p,
-                 [&](P &q) {
-                     if (!ragged) return fetch(q);
-                     q.fetch_last(source, next, g.hidden, (uint32_t)g.ldh);
-                     next = next > from ? next - 1 : from;
-                 },
-                 fetch,
-                 [&](P &q) {
-                     if (ragged) q.mend_b(steps - 1, g.hidden, scales, source.p);
-                 },
-                 [&](P &q) { q.multiply(acc); });
-#pragma unroll
-        for (int i = 0; i < RM; ++i) {
-            const uint32_t p = pair[i] < 0 ? 0 : pair[i], token = p / g.top_k;
-            const float by = router.weight(p);
-            f32x4 v[FN];
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                v[j] = acc[i][j] * by;
-                if constexpr (kScales)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) v[j][c] *= column_scale(scale[j], c);
-            }
-            f32x4 *const to = total + (token / 16 * FN * 4 + at) * 16 + token % 16;
-            auto add = [&] {
-#pragma unroll
-                for (int j = 0; j < FN; ++j) to[j * 64] += v[j];
-            };
-            // a token that has the expert twice is in two rows: these go one after another
-            const uint32_t before = (uint32_t)__shfl_up((int)token, 1, 64);
-            const bool twice = lane % 16 != 0 && pair[i] >= 0 && before == token;
-            if (__ballot(twice) == 0) {
-                if (pair[i] >= 0) add();
-            } else {
-                for (uint32_t r = 0; r < 16; ++r) {
-                    if (lane % 16 == r && pair[i] >= 0) add();
-                    __builtin_amdgcn_wave_barrier();
-                }
-            }
-            __builtin_amdgcn_wave_barrier();
-        }
+        uint32_t e, before;
+        const uint32_t count = router.find(slot, rows[wave], e, before);
+        const Rows h(g, before, count);
+        if (count <= 8) down_rows<T, W, 1, FN, DEEP>(g, router, e, n0, from, some, rows[wave], h, total);
+        else if (RM == 1 || count <= 16)
+            down_rows<T, W, 2, FN, DEEP>(g, router, e, n0, from, some, rows[wave], h, total);
+        else down_rows<T, W, 2 * RM, FN, DEEP>(g, router, e, n0, from, some, rows[wave], h, total);
     }
     __syncthreads();
     auto store = [&](uint32_t f, f32x4 v) {
@@ -805,9 +918,7 @@ inline uint64_t most_slots(uint64_t pairs, uint32_t experts, uint32_t rows)
 // Bytes of a row of h: whole steps of the second kernel.
 inline int64_t h_bytes(uint32_t hidden, int32_t down_kind)
 {
-    const uint32_t values = down_kind == EXPERTS_WEIGHT_16     ? Piece<__bf16, __bf16, 1, 1>::kValues
-                            : down_kind == EXPERTS_WEIGHT_INT8 ? Piece<__bf16, int8_t, 1, 1>::kValues
-                                                               : Piece<__bf16, Mx4, 1, 1>::kValues;
+    const uint32_t values = kStep / 2 << down_kind;  // (16, 8 and 4 bits)
     return ((int64_t)hidden + values - 1) / values * values * 2;
 }
 
@@ -840,7 +951,7 @@ inline FewPlan few_plan(uint64_t tokens, uint32_t top_k, uint32_t experts, uint3
     }
     auto up = [](uint64_t b) { return (b + 255) / 256 * 256; };
     p.h = 0;
-    p.arrived = up(pairs * h_bytes(hidden, down_kind));
+    p.arrived = up(pairs * 2 * h_bytes(hidden, down_kind));
     p.partial = p.arrived + up((uint64_t)p.tiles * 4);
     p.bytes = p.partial +
               (p.splits > 1 ? (uint64_t)p.tiles * p.splits * ((tokens + 15) / 16) * fn * 1024 : 0);

@@ -53,7 +53,8 @@ def test_workspace_size():
     good = (10, 2, 4, 64, 96, 0)
     assert size(*good, ctypes.byref(n)) == OK and n.value >= 20 * 64 * 2
     assert size(0, *good[1:], ctypes.byref(n)) == OK and n.value == 0
-    assert size(64, 64, 1024, 2**17, 2**17, 0, ctypes.byref(n)) == OK and 2**30 <= n.value < 2**31
+    # (64 x 64 rows of 2^17 columns in two parts of two bytes: 2^31)
+    assert size(64, 64, 1024, 2**17, 2**17, 0, ctypes.byref(n)) == OK and 2**31 <= n.value < 2**32
     assert size(*good, None) == BAD
     for at, value in ((1, 0), (2, 0), (3, 0), (4, 0), (5, 3), (5, -1)):
         assert size(*good[:at], value, *good[at + 1:], ctypes.byref(n)) == BAD

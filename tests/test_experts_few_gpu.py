@@ -190,6 +190,40 @@ def test_an_expert_with_infinities_keeps_them(kind):
     assert torch.isfinite(experts.few_tokens(x, up, down, without, by)).all()
 
 
+@pytest.mark.parametrize("tokens", [3, 40])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_an_infinite_weight_of_the_second_product_keeps_its_sign(dtype, tokens):
+    """Whatever the type leaves of h, and of whichever sign that is."""
+    x = normal(11, tokens, 64, dtype=dtype)
+    up, down = (normal(s, 2, 64, 64, dtype=dtype, scale=0.125) for s in (12, 13))
+    down[1, 5, 7] = float("inf")
+    ids = torch.ones(tokens, 1, dtype=torch.int32, device="cuda")
+    out = experts.few_tokens(x, up, down, ids, torch.ones(tokens, 1, device="cuda"), gated=False)
+    a = x.double() @ up[1].double().t().contiguous()
+    h = a[:, 7] * torch.sigmoid(a[:, 7])
+    assert (h.abs() > 1e-3).all()  # (signs that rounding cannot change)
+    assert torch.equal(out[:, 5].double(), torch.sign(h) * float("inf"))
+    assert torch.isfinite(out[:, [c for c in range(64) if c != 5]]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_column_that_the_type_rounds_to_infinity_is_one(dtype):
+    """h is finite in 32 bits and past the type's last value: what is left of it adds no NaN."""
+    width = hidden = 16
+    x = torch.zeros(3, width, dtype=dtype, device="cuda")
+    up = torch.zeros(1, hidden, width, dtype=dtype, device="cuda")
+    if dtype == torch.float16:
+        x[1, 0] = up[0, 0, 0] = 300.0  # 90,000 > 65,520
+    else:
+        # 2^127 (255 / 128 + 1.5 / 256): past 2^127 (2 - 1 / 256), below 2^128
+        x[1, 0], up[0, 0, 0] = 2.0**64 * 255 / 128, 2.0**63
+        x[1, 1], up[0, 0, 1] = 2.0**55 * 1.5, 2.0**64
+    down = torch.ones(1, 8, hidden, dtype=dtype, device="cuda")
+    ids = torch.zeros(3, 1, dtype=torch.int32, device="cuda")
+    out = experts.few_tokens(x, up, down, ids, torch.ones(3, 1, device="cuda"), gated=False)
+    assert torch.isposinf(out[1]).all() and (out[0] == 0).all() and (out[2] == 0).all()
+
+
 def test_infinities_and_nan_of_a_token_stay_in_its_row():
     for kind in KINDS:
         for dtype in DTYPES:
