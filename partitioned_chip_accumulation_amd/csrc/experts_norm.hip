@@ -5,7 +5,9 @@
 //   dn = dy weight, u = h r:  dx = r (dn - u mean(dn u)) + dh, dweight = sum over rows of dy u
 //
 // All are bound by memory: each row is read once and kept in registers between its sums and its
-// results.
+// results. 16384 rows of 4096 in bf16, with the residual and h: 93-98 us, 5.5-5.8 TB/s (a large copy runs at
+// 5.1); 8192 of them to 8 bits: 45 us, 5.3 TB/s; the gradients of 8191 rows of 2048: 27-29 us, 4.6-5.0 TB/s,
+// and 4 for the groups' sums; 32 rows of 4096: 5.3 us, the launch and a row's latency.
 #include "experts_common.hpp"
 
 namespace pca_experts {
@@ -470,8 +472,8 @@ inline uint32_t backward_threads(uint32_t n)
 }
 
 // Groups of rows, each with its own sums for the weight's gradient, which are written and read again. us
-// for 8191 x 2048, 16384 x 4096, 16384 x 1024, 4096 x 8192 and 2048 x 16384 with as many waves as 2048,
-// 3072 and 4096: 35.9, 32.7, 34.9; 106, 111, 115; 35.8, 40.8, 44.5; 62.2, 61.3, 64.5; 83.8, 71.1, 68.7.
+// with 8, 12 and 16 waves a CU: 8191 x 2048 35.9, 32.7, 34.9; 16384 x 4096 106, 111, 115; 16384 x 1024 35.8,
+// 40.8, 44.5; 4096 x 8192 62.2, 61.3, 64.5; 2048 x 16384 83.8, 71.1, 68.7.
 inline uint32_t backward_groups(uint64_t rows, uint32_t n)
 {
     const uint64_t most = n > kWidest ? 64

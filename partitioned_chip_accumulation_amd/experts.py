@@ -8,6 +8,12 @@ to their tokens (``combine_backward``: its gradients). ``linear`` and
 ``merge`` are the product and the sum for torch's autograd, with gradients of the
 first order (a gradient of a gradient raises RuntimeError).
 
+Around them: ``rms_norm`` before a layer, with the residual's addition, and
+``rms_norm_backward`` (``norm``: both for autograd; ``rms_norm_int8``: its result in 8 bits); the
+product of rows and weights in 4 bits with a power of two for each 32 values,
+``quantize_mx4`` and ``mx4_matmul``; and the layer for up to MAX_FEW tokens in one call, with
+weights in 16, 8 or 4 bits, ``few_tokens``.
+
 ::
 
     g = experts.group_rows(ids, num_experts)              # ids: [tokens, top_k]
@@ -15,13 +21,17 @@ first order (a gradient of a gradient raises RuntimeError).
     y = experts.linear(torch.nn.functional.silu(h), w_down, g)
     out = experts.merge(y, g, weights)                    # [tokens, k]
 
+    y, h = experts.norm(x, norm_weight, residual)         # h = x + residual goes on to the next one
+    out = experts.few_tokens(y, w_up, w_down, ids, weights, gated=False)   # 64 tokens at most
+
 A pair whose id lies outside [0, experts) is dropped: place -1, no row, nothing
 added. Rows of the sorted arrays past the last kept pair are zero.
 
 Tensors are bfloat16 or float16, rows of unit stride (the stride between rows
 is free). Every call queues kernels on the current stream of the tensors'
 device, allocates its results there, and never synchronises, so it can be
-captured into a graph. A bad argument raises ValueError, a status of the
+captured into a graph (torch ends the process if a backward pass is captured while an
+eager graph of the same leaves lives). A bad argument raises ValueError, a status of the
 library hist.HistError; there is no fallback.
 """
 from __future__ import annotations
@@ -398,17 +408,17 @@ def mx4_matmul(xq: torch.Tensor, xs: torch.Tensor, wq: torch.Tensor, ws: torch.T
     if g is None:
         if gather:
             raise ValueError("gather needs the groups")
-        ldw, stride, ws_stride = _matrix(wq, "wq", (torch.uint8,)), 0, 0
+        ldw, stride = _matrix(wq, "wq", (torch.uint8,)), 0
         if wq.device != device or wq.shape[0] == 0:
             raise ValueError(f"wq must have rows and be on {device}")
         experts, pairs, top_k, offsets, order = 1, x_rows, 1, None, None
     else:
         experts, pairs, top_k = _groups(g, device)
         ldw, stride = _weights(wq, experts, device, torch.uint8)
-        ws_stride = ws.stride(0) if experts > 1 and ws.dim() == 3 else 0
         _rows(xq, g, pairs, gather, "xq")
         offsets, order = g.offsets.data_ptr(), g.order.data_ptr() if gather else None
     ldws = _powers(ws, wq, "ws")
+    ws_stride = ws.stride(0) if experts > 1 else 0
     n = wq.shape[-2]
     _same(xq.shape[1], wq.shape[-1], "the last dimensions of xq and wq")
     y = torch.empty(pairs, n, dtype=out_dtype, device=device)
@@ -493,6 +503,8 @@ def _stack(w, name: str, k: int, x: torch.Tensor) -> tuple[_Weight, tuple]:
         ld = _matrix(data, name, (x.dtype,), 3)
         kind, width, ld_scales, scales_stride = 0, k, 0, 0
     else:
+        if not isinstance(w, (tuple, list)) or len(w) != 2:
+            raise ValueError(f"{name} must be a tensor, or a pair of one and its scales")
         data, scales = w
         mx4 = isinstance(data, torch.Tensor) and data.dtype == torch.uint8
         ld = _matrix(data, name, (torch.uint8 if mx4 else torch.int8,), 3)

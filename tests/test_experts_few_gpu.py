@@ -272,6 +272,16 @@ def test_refused():
             experts.few_tokens(*bad)
 
 
+@pytest.mark.parametrize("other", [None, 3, (), (None,), (None, None)])
+def test_weights_that_are_none(other):
+    x, up, down, ids, by = case(1, 2, 2, 3, 32, 32, 32, "int8", torch.bfloat16, False)[0]
+    for args in ((x, other, down, ids, by), (x, up, other, ids, by)):
+        with pytest.raises(ValueError):
+            experts.few_tokens(*args, gated=False)
+    with pytest.raises(ValueError):
+        experts.few_tokens(x, (up[0], other), down, ids, by, gated=False)
+
+
 def test_captured_twice_and_on_another_stream():
     """Two graphs of one layer, replayed in turn, with eager calls on another stream between: every
     result the same bits."""

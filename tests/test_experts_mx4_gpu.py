@@ -209,6 +209,18 @@ def test_empty_and_refused():
             bad()
 
 
+def test_powers_that_are_none():
+    q, p = experts.quantize_mx4(torch.ones(4, 64, dtype=torch.bfloat16, device="cuda"))
+    g = experts.group_rows(torch.zeros(4, 1, dtype=torch.int32, device="cuda"), 2)
+    w, powers = torch.stack([q, q]), torch.stack([p, p])
+    assert torch.isfinite(experts.mx4_matmul(q, p, w, powers, g)).all()
+    for bad in (None, 3, p, powers[:1], powers.float()):
+        with pytest.raises(ValueError):
+            experts.mx4_matmul(q, p, w, bad, g)
+        with pytest.raises(ValueError):
+            experts.mx4_matmul(q, None if bad is p else bad, w, powers, g)
+
+
 def test_captured_twice():
     """Two captured graphs of one product, replayed in turn with eager calls between."""
     g = pairs_of(1000, 8)
