@@ -113,7 +113,8 @@ extern "C" hist_status_t experts_few_tokens(void *out, int64_t ldo, const void *
     g.hidden = hidden;
     g.n = n;
     g.tiles = p.tiles;
-    g.splits = p.splits;
+    g.groups = p.groups;
+    g.parts = p.parts;
     g.gated = (uint32_t)gated;
     g.h_shift = (uint32_t)down->kind;  // (of 16, 8 and 4 bits: 0, 1, 2)
     g.h_fp16 = dtype == EXPERTS_FP16 && down->kind != EXPERTS_WEIGHT_MX4;

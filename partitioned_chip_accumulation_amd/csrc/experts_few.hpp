@@ -41,7 +41,7 @@ struct FewArgs {
     const float *by;
     int64_t ldo, ldx, ldh;  // bytes
     uint32_t ids64, gated, h_fp16, h_shift, tokens, top_k, experts, width, hidden, n;
-    uint32_t tiles, splits;  // of the result
+    uint32_t tiles, groups, parts;  // of the result; workgroups, and the most of them that share a tile
 };
 
 // How weights of type W go with tokens of type T, and with the parts of h, of type H: C fragments of a
@@ -504,10 +504,10 @@ __device__ __forceinline__ void pipeline(uint32_t mine, P (&p)[DEEP], O first, F
         if ((uint32_t)d < left) multiply(p[d]);
 }
 
-// Of `count` steps in a row, share number `at` of `of` begins here.
+// Of `count` steps in a row, share number `at` of `of` (2^16 at most) begins here.
 __device__ __forceinline__ uint32_t share(uint32_t count, uint32_t at, uint32_t of)
 {
-    return (uint32_t)((uint64_t)count * at / of);
+    return count / of * at + count % of * at / of;
 }
 
 // h of a slot, in two parts of 16 bits, what 16 bits hold of it and of the rest: two rows for a pair, first all
@@ -686,11 +686,11 @@ __global__ void __launch_bounds__(256) k_few_up(FewArgs g)
 }
 
 // ---------------------------------------------------------------------------
-// 16 FN columns of the result. The steps of all experts, one expert's after another's, are shared out
-// among the waves of `splits` workgroups, a run of them each, so that a wave meets few experts. When it
-// leaves one, it adds the rows' products times their weights (and the columns' scales) to its
-// own sums of the tokens in LDS. The workgroup that arrives last adds the workgroups' sums in their
-// order.
+// Tiles of 16 FN columns of the result. The workgroups take equal shares of all tiles, so that one
+// has a part of a tile, or of several. A part is of the steps of all experts, one expert's after another's; the
+// waves have a run of them each, so that a wave meets few experts. When it leaves one, it
+// adds the rows' products times their weights (and the columns' scales) to its own sums of the tokens in
+// LDS. The workgroup that arrives last at a tile adds the workgroups' sums in their order.
 
 // Lane l holds the scale of column l % 16; a result's column is 4 (l / 16) + c.
 __device__ __forceinline__ float column_scale(float scale, int c)
@@ -805,87 +805,100 @@ __global__ void __launch_bounds__(WAVES * 64) k_few_down(FewArgs g)
     const Router<16 * RM, true> router(g, routes);
     const uint32_t lane = threadIdx.x % 64, at = lane / 16;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const uint32_t tile = blockIdx.x % g.tiles, split = blockIdx.x / g.tiles;
-    const uint32_t n0 = tile * 16 * FN, pairs = g.tokens * g.top_k;
+    const uint32_t pairs = g.tokens * g.top_k;
     const uint32_t steps = (row_bytes<W>(g.hidden) + kStep - 1) / kStep;
     const uint32_t all = router.count * steps;
-    const uint32_t first = share(all, split * WAVES + wave, g.splits * WAVES);
-    const uint32_t mine = share(all, split * WAVES + wave + 1, g.splits * WAVES) - first;
     // the sums of each wave: [tokens, in 16s][FN][16], a row's four columns of a lane together
     const uint32_t high = (g.tokens + 15) / 16;
     f32x4 *const sums = (f32x4 *)(few_lds + ids_bytes(pairs) + by_bytes(pairs));
     f32x4 *const total = sums + wave * high * FN * 64;
-    for (uint32_t i = lane; i < high * FN * 64; i += 64) total[i] = f32x4{};
 
-    for (uint32_t done = 0, some; done < mine; done += some) {
-        // some steps of one expert, the last one first: it may be ragged
-        const uint32_t slot = (first + done) / steps, from = (first + done) % steps;
-        some = steps - from < mine - done ? steps - from : mine - done;
-        uint32_t e, before;
-        const uint32_t count = router.find(slot, rows[wave], e, before);
-        const Rows h(g, before, count);
-        if (count <= 8) down_rows<T, W, 1, FN, DEEP>(g, router, e, n0, from, some, rows[wave], h, total);
-        else if (RM == 1 || count <= 16)
-            down_rows<T, W, 2, FN, DEEP>(g, router, e, n0, from, some, rows[wave], h, total);
-        else down_rows<T, W, 2 * RM, FN, DEEP>(g, router, e, n0, from, some, rows[wave], h, total);
-    }
-    __syncthreads();
-    auto store = [&](uint32_t f, f32x4 v) {
-        const uint32_t t = f / FN * 16 + lane % 16, c = n0 + f % FN * 16 + at * 4;
-        if (t >= g.tokens || c >= g.n) return;
-        typedef T T4 __attribute__((ext_vector_type(4)));
-        T *to = (T *)(g.out + t * g.ldo) + c;
-        const T4 o = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
-        if (c + 4 <= g.n) {
-            store_any(to, o);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 3; ++q)
-                if (c + q < g.n) to[q] = o[q];
+    // (in units of 1 / groups of a tile)
+    uint32_t until;
+    for (uint32_t from_tile = blockIdx.x * g.tiles; from_tile < (blockIdx.x + 1) * g.tiles;
+         from_tile = until) {
+        const uint32_t tile = from_tile / g.groups, n0 = tile * 16 * FN;
+        until = (tile + 1) * g.groups;
+        if (until > (blockIdx.x + 1) * g.tiles) until = (blockIdx.x + 1) * g.tiles;
+        const uint32_t begin = (from_tile - tile * g.groups) * WAVES + wave * (until - from_tile);
+        const uint32_t first = share(all, begin, g.groups * WAVES);
+        const uint32_t mine = share(all, begin + until - from_tile, g.groups * WAVES) - first;
+        const uint32_t leader = tile * g.groups / g.tiles;  // the first workgroup that has a part of it
+        const uint32_t sharing = ((tile + 1) * g.groups - 1) / g.tiles - leader + 1;
+        const uint32_t own = blockIdx.x - leader;
+        if (from_tile != blockIdx.x * g.tiles) __syncthreads();  // the sums before these have been read
+        for (uint32_t i = lane; i < high * FN * 64; i += 64) total[i] = f32x4{};
+
+        for (uint32_t done = 0, some; done < mine; done += some) {
+            // some steps of one expert, the last one first: it may be ragged
+            const uint32_t slot = (first + done) / steps, from = (first + done) % steps;
+            some = steps - from < mine - done ? steps - from : mine - done;
+            uint32_t e, before;
+            const uint32_t count = router.find(slot, rows[wave], e, before);
+            const Rows h(g, before, count);
+            if (count <= 8) down_rows<T, W, 1, FN, DEEP>(g, router, e, n0, from, some, rows[wave], h, total);
+            else if (RM == 1 || count <= 16)
+                down_rows<T, W, 2, FN, DEEP>(g, router, e, n0, from, some, rows[wave], h, total);
+            else down_rows<T, W, 2 * RM, FN, DEEP>(g, router, e, n0, from, some, rows[wave], h, total);
         }
-    };
-    uint32_t *const parts = g.partial + (uint64_t)tile * g.splits * (high * FN * 256);
-    for (uint32_t f = wave; f < high * FN; f += WAVES) {
-        f32x4 v = sums[f * 64 + lane];
+        __syncthreads();
+        auto store = [&](uint32_t f, f32x4 v) {
+            const uint32_t t = f / FN * 16 + lane % 16, c = n0 + f % FN * 16 + at * 4;
+            if (t >= g.tokens || c >= g.n) return;
+            typedef T T4 __attribute__((ext_vector_type(4)));
+            T *to = (T *)(g.out + t * g.ldo) + c;
+            const T4 o = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+            if (c + 4 <= g.n) {
+                store_any(to, o);
+            } else {
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) v += sums[(w * high * FN + f) * 64 + lane];
-        if (g.splits == 1) {
-            store(f, v);
-        } else {
-            // written through to where every XCD sees it
-            uint32_t *to = parts + (split * high * FN + f) * 256 + lane;
+                for (int q = 0; q < 3; ++q)
+                    if (c + q < g.n) to[q] = o[q];
+            }
+        };
+        uint32_t *const parts = g.partial + (uint64_t)tile * g.parts * (high * FN * 256);
+        for (uint32_t f = wave; f < high * FN; f += WAVES) {
+            f32x4 v = sums[f * 64 + lane];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                __hip_atomic_store(to + q * 64, __float_as_uint(v[q]), __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_AGENT);
+            for (int w = 1; w < WAVES; ++w) v += sums[(w * high * FN + f) * 64 + lane];
+            if (sharing == 1) {
+                store(f, v);
+            } else {
+                // written through to where every XCD sees it
+                uint32_t *to = parts + (own * high * FN + f) * 256 + lane;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    __hip_atomic_store(to + q * 64, __float_as_uint(v[q]), __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+            }
         }
-    }
-    if (g.splits == 1) return;
-    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // this wave's sums are there
-    __syncthreads();
-    if (threadIdx.x == 0)
-        last = __hip_atomic_fetch_add(g.arrived + tile, 1u, __ATOMIC_RELAXED,
-                                      __HIP_MEMORY_SCOPE_AGENT) == g.splits - 1;
-    __syncthreads();
-    if (!last) return;
-    // eight workgroups' sums on their way at one time
-    for (uint32_t i = threadIdx.x; i < high * FN * 256; i += WAVES * 64) {
-        float v = 0.f;
-        for (uint32_t s = 0; s < g.splits; s += 8) {
-            uint32_t part[8];
+        if (sharing == 1) continue;
+        asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // this wave's sums are there
+        __syncthreads();
+        if (threadIdx.x == 0)
+            last = __hip_atomic_fetch_add(g.arrived + tile, 1u, __ATOMIC_RELAXED,
+                                          __HIP_MEMORY_SCOPE_AGENT) == sharing - 1;
+        __syncthreads();
+        if (!last) continue;
+        // eight workgroups' sums on their way at one time
+        for (uint32_t i = threadIdx.x; i < high * FN * 256; i += WAVES * 64) {
+            float v = 0.f;
+            for (uint32_t s = 0; s < sharing; s += 8) {
+                uint32_t part[8];
 #pragma unroll
-            for (uint32_t q = 0; q < 8; ++q)
-                part[q] = __hip_atomic_load(
-                    parts + (uint64_t)(s + q < g.splits ? s + q : s) * high * FN * 256 + i,
-                    __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                for (uint32_t q = 0; q < 8; ++q)
+                    part[q] = __hip_atomic_load(
+                        parts + (uint64_t)(s + q < sharing ? s + q : s) * high * FN * 256 + i,
+                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-            for (uint32_t q = 0; q < 8; ++q)
-                if (s + q < g.splits) v += __uint_as_float(part[q]);
+                for (uint32_t q = 0; q < 8; ++q)
+                    if (s + q < sharing) v += __uint_as_float(part[q]);
+            }
+            ((float *)sums)[(i / 256 * 64 + i % 64) * 4 + i / 64 % 4] = v;
         }
-        ((float *)sums)[(i / 256 * 64 + i % 64) * 4 + i / 64 % 4] = v;
+        __syncthreads();
+        for (uint32_t f = wave; f < high * FN; f += WAVES) store(f, sums[f * 64 + lane]);
     }
-    __syncthreads();
-    for (uint32_t f = wave; f < high * FN; f += WAVES) store(f, sums[f * 64 + lane]);
 }
 
 // ---------------------------------------------------------------------------
@@ -923,7 +936,7 @@ inline int64_t h_bytes(uint32_t hidden, int32_t down_kind)
 }
 
 struct FewPlan {
-    uint32_t rows, tiles, splits;  // of the result
+    uint32_t rows, tiles, groups, parts;  // of the result (see FewArgs)
     uint64_t h, arrived, partial, bytes;  // offsets in the workspace, and its size
 };
 
@@ -938,23 +951,28 @@ inline FewPlan few_plan(uint64_t tokens, uint32_t top_k, uint32_t experts, uint3
     const uint32_t bytes = down_kind == EXPERTS_WEIGHT_16     ? hidden * 2
                            : down_kind == EXPERTS_WEIGHT_INT8 ? hidden
                                                               : (hidden + 31) / 32 * 16;
-    // The busiest of 256 CUs has ceil(tiles splits / 256) workgroups, each of 1 / splits of a tile's work, and
-    // a split costs some hundredth of it (128 tiles: two splits 33 us, four 34; 129 tiles: two splits 160 us,
-    // eight 123). Two steps of 128 bytes for each wave are the least.
-    const uint64_t steps = slots * ((bytes + 127) / 128) / (2 * kDownWaves);
-    const uint64_t most = p.tiles < 32 ? 256 / p.tiles : 8;
+    // Either a tile for `sharing` whole workgroups, or 256 workgroups with equal shares of all tiles. What
+    // a workgroup does once a part costs it as much as reading 64 KB or so. us with whole ones (seven or eight a
+    // tile; four of 320) and with equal shares: 129 tiles of 1.4 MB 70 and 61, 224 of 0.7 MB 106 and 85, 320 of 0.7 MB
+    // 131 and 118; 65 of 0.3 MB 26 and 30; 1024 of 0.1 MB 70 (one a tile) and 74. Two steps of 128 bytes
+    // for each wave are the least.
+    constexpr uint64_t kOnce = 65536;
+    const uint64_t tile = slots * bytes * 16 * fn, steps = slots * ((bytes + 127) / 128) / (2 * kDownWaves);
+    const uint64_t most = steps < 1 ? 1 : steps < 64 ? steps : 64;
     uint64_t best = UINT64_MAX;
-    p.splits = 1;
-    for (uint64_t s = 1; s <= (most < 64 ? most : 64) && (s == 1 || s <= steps); ++s) {
-        const uint64_t cost = (p.tiles * s + 255) / 256 * 100000 / s + 1000 * s;
-        if (cost < best) best = cost, p.splits = (uint32_t)s;
+    for (uint64_t sharing = 1; sharing <= most && (sharing == 1 || p.tiles * sharing <= 4096); ++sharing) {
+        const uint64_t cost = (p.tiles * sharing + kCus - 1) / kCus * (tile / sharing + kOnce);
+        if (cost < best) best = cost, p.groups = (uint32_t)(p.tiles * sharing);
     }
+    if (p.tiles * most > kCus && p.tiles * tile / kCus + ((p.tiles + kCus - 1) / kCus + 1) * kOnce < best)
+        p.groups = kCus;
+    // (where neither is a multiple of the other, a tile's ends lie within workgroups' shares)
+    p.parts = (p.groups + p.tiles - 1) / p.tiles + (p.groups % p.tiles && p.tiles % p.groups);
     auto up = [](uint64_t b) { return (b + 255) / 256 * 256; };
     p.h = 0;
     p.arrived = up(pairs * 2 * h_bytes(hidden, down_kind));
     p.partial = p.arrived + up((uint64_t)p.tiles * 4);
-    p.bytes = p.partial +
-              (p.splits > 1 ? (uint64_t)p.tiles * p.splits * ((tokens + 15) / 16) * fn * 1024 : 0);
+    p.bytes = p.partial + (p.parts > 1 ? (uint64_t)p.tiles * p.parts * ((tokens + 15) / 16) * fn * 1024 : 0);
     return p;
 }
 
@@ -979,7 +997,7 @@ hist_status_t launch_down(const FewArgs &g, hipStream_t stream)
 {
     constexpr int FN = few_columns<W, RM>();
     const uint32_t pairs = g.tokens * g.top_k;
-    return launch(k_few_down<T, W, RM, FN, kDeep, WAVES>, (uint64_t)g.tiles * g.splits, WAVES * 64,
+    return launch(k_few_down<T, W, RM, FN, kDeep, WAVES>, g.groups, WAVES * 64,
                   ids_bytes(pairs) + by_bytes(pairs) + WAVES * ((g.tokens + 15) / 16) * FN * 1024,
                   stream, g);
 }

@@ -8,7 +8,6 @@
 
 namespace pca_experts {
 
-constexpr uint32_t kCus = 256;           // of the device
 constexpr uint32_t kLdsOfCu = 160 << 10;  // bytes
 
 struct RowsArgs {

@@ -25,6 +25,8 @@
 
 namespace pca_experts {
 
+constexpr uint32_t kCus = 256;  // of the device
+
 constexpr uint32_t kStepBytes = 128;
 constexpr uint32_t kStepPowers = kStepBytes / 16;  // bytes of powers of two that go with them
 
