@@ -115,6 +115,11 @@ extern "C" hist_status_t experts_few_tokens(void *out, int64_t ldo, const void *
     g.tiles = p.tiles;
     g.groups = p.groups;
     g.parts = p.parts;
+    g.by_top_k = Divide::by(top_k);
+    g.by_tiles = Divide::by(p.tiles);
+    g.by_groups = Divide::by(p.groups);
+    g.by_waves = Divide::by(p.groups * kDownWaves);
+    g.by_steps = Divide::by((uint32_t)(g.ldh / 2 / (kStep / 2 << down->kind)));
     g.gated = (uint32_t)gated;
     g.h_shift = (uint32_t)down->kind;  // (of 16, 8 and 4 bits: 0, 1, 2)
     g.h_fp16 = dtype == EXPERTS_FP16 && down->kind != EXPERTS_WEIGHT_MX4;

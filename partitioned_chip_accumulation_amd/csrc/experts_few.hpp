@@ -42,6 +42,8 @@ struct FewArgs {
     int64_t ldo, ldx, ldh;  // bytes
     uint32_t ids64, gated, h_fp16, h_shift, tokens, top_k, experts, width, hidden, n;
     uint32_t tiles, groups, parts;  // of the result; workgroups, and the most of them that share a tile
+    // (a kernel's first loads wait for its divisions)
+    Divide by_top_k, by_up_tiles, by_tiles, by_groups, by_waves, by_steps;
 };
 
 // How weights of type W go with tokens of type T, and with the parts of h, of type H: C fragments of a
@@ -504,10 +506,11 @@ __device__ __forceinline__ void pipeline(uint32_t mine, P (&p)[DEEP], O first, F
         if ((uint32_t)d < left) multiply(p[d]);
 }
 
-// Of `count` steps in a row, share number `at` of `of` (2^16 at most) begins here.
-__device__ __forceinline__ uint32_t share(uint32_t count, uint32_t at, uint32_t of)
+// Of `count` steps in a row, share number `at` of `of` (2^15 at most) begins here.
+__device__ __forceinline__ uint32_t share(uint32_t count, uint32_t at, uint32_t of, Divide by)
 {
-    return count / of * at + count % of * at / of;
+    const uint32_t whole = by(count);
+    return whole * at + by((count - whole * of) * at);
 }
 
 // h of a slot, in two parts of 16 bits, what 16 bits hold of it and of the rest: two rows for a pair, first all
@@ -596,7 +599,7 @@ __device__ __forceinline__ void up_rows(const FewArgs &g, uint32_t e, uint32_t n
 #pragma unroll
     for (int i = 0; i < RM; ++i) {
         const uint32_t r = i * 16 + lane % 16;
-        from.a[i] = r < count ? rows[r] / g.top_k * (uint32_t)g.ldx : Window::kNowhere;
+        from.a[i] = r < count ? g.by_top_k(rows[r]) * (uint32_t)g.ldx : Window::kNowhere;
     }
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
@@ -674,7 +677,7 @@ __global__ void __launch_bounds__(256) k_few_up(FewArgs g)
         for (uint32_t i = threadIdx.x; i < g.tiles; i += 256) g.arrived[i] = 0;
     const Router<16 * RM, false> router(g, routes);
     const uint32_t each = g.gated ? 16 * FN : 32 * FN, tiles = (g.hidden + each - 1) / each;
-    const uint32_t slot = blockIdx.x / tiles, n0 = blockIdx.x % tiles * each;
+    const uint32_t slot = g.by_up_tiles(blockIdx.x), n0 = (blockIdx.x - slot * tiles) * each;
     if (slot >= router.count) return;
     uint16_t *const mine = rows[__builtin_amdgcn_readfirstlane(threadIdx.x / 64)];
     uint32_t e, before;
@@ -755,7 +758,7 @@ __device__ __forceinline__ void down_rows(const FewArgs &g, const O &router, uin
              [&](P &q) { q.multiply(acc); });
 #pragma unroll
     for (int i = 0; i < (R + 1) / 2; ++i) {
-        const uint32_t r = i * 16 + lane % 16, pair = r < count ? rows[r] : 0, token = pair / g.top_k;
+        const uint32_t r = i * 16 + lane % 16, pair = r < count ? rows[r] : 0, token = g.by_top_k(pair);
         const float by = router.weight(pair);
         f32x4 v[FN];
 #pragma unroll
@@ -817,21 +820,21 @@ __global__ void __launch_bounds__(WAVES * 64) k_few_down(FewArgs g)
     uint32_t until;
     for (uint32_t from_tile = blockIdx.x * g.tiles; from_tile < (blockIdx.x + 1) * g.tiles;
          from_tile = until) {
-        const uint32_t tile = from_tile / g.groups, n0 = tile * 16 * FN;
+        const uint32_t tile = g.by_groups(from_tile), n0 = tile * 16 * FN;
         until = (tile + 1) * g.groups;
         if (until > (blockIdx.x + 1) * g.tiles) until = (blockIdx.x + 1) * g.tiles;
         const uint32_t begin = (from_tile - tile * g.groups) * WAVES + wave * (until - from_tile);
-        const uint32_t first = share(all, begin, g.groups * WAVES);
-        const uint32_t mine = share(all, begin + until - from_tile, g.groups * WAVES) - first;
-        const uint32_t leader = tile * g.groups / g.tiles;  // the first workgroup that has a part of it
-        const uint32_t sharing = ((tile + 1) * g.groups - 1) / g.tiles - leader + 1;
+        const uint32_t first = share(all, begin, g.groups * WAVES, g.by_waves);
+        const uint32_t mine = share(all, begin + until - from_tile, g.groups * WAVES, g.by_waves) - first;
+        const uint32_t leader = g.by_tiles(tile * g.groups);  // the first workgroup that has a part of it
+        const uint32_t sharing = g.by_tiles((tile + 1) * g.groups - 1) - leader + 1;
         const uint32_t own = blockIdx.x - leader;
         if (from_tile != blockIdx.x * g.tiles) __syncthreads();  // the sums before these have been read
         for (uint32_t i = lane; i < high * FN * 64; i += 64) total[i] = f32x4{};
 
         for (uint32_t done = 0, some; done < mine; done += some) {
             // some steps of one expert, the last one first: it may be ragged
-            const uint32_t slot = (first + done) / steps, from = (first + done) % steps;
+            const uint32_t slot = g.by_steps(first + done), from = first + done - slot * steps;
             some = steps - from < mine - done ? steps - from : mine - done;
             uint32_t e, before;
             const uint32_t count = router.find(slot, rows[wave], e, before);
@@ -964,6 +967,7 @@ inline FewPlan few_plan(uint64_t tokens, uint32_t top_k, uint32_t experts, uint3
         const uint64_t cost = (p.tiles * sharing + kCus - 1) / kCus * (tile / sharing + kOnce);
         if (cost < best) best = cost, p.groups = (uint32_t)(p.tiles * sharing);
     }
+    if (p.tiles > 4096) best = UINT64_MAX;  // (share() has 32 bits)
     if (p.tiles * most > kCus && p.tiles * tile / kCus + ((p.tiles + kCus - 1) / kCus + 1) * kOnce < best)
         p.groups = kCus;
     // (where neither is a multiple of the other, a tile's ends lie within workgroups' shares)
@@ -977,12 +981,13 @@ inline FewPlan few_plan(uint64_t tokens, uint32_t top_k, uint32_t experts, uint3
 }
 
 template <class T, class W, int RM>
-hist_status_t launch_up(const FewArgs &g, uint64_t slots, hipStream_t stream)
+hist_status_t launch_up(FewArgs g, uint64_t slots, hipStream_t stream)
 {
     constexpr int FN = few_columns<W, RM>();
-    const uint32_t each = g.gated ? 16 * FN : 32 * FN;
-    return launch(k_few_up<T, W, RM, FN, kDeep>, slots * ((g.hidden + each - 1) / each), 256,
-                  ids_bytes(g.tokens * g.top_k), stream, g);
+    const uint32_t each = g.gated ? 16 * FN : 32 * FN, tiles = (g.hidden + each - 1) / each;
+    g.by_up_tiles = Divide::by(tiles);
+    return launch(k_few_up<T, W, RM, FN, kDeep>, slots * tiles, 256, ids_bytes(g.tokens * g.top_k),
+                  stream, g);
 }
 
 template <class T, class W>
