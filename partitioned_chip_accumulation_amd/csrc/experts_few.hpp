@@ -3,9 +3,11 @@
 //
 //   h[t, e] = act(x[t] up[e]^T),  out[t] = sum over t's experts e of weight[t, e] h[t, e] down[e]^T
 //
-// Bound by reading the weights of the experts that have a token, once each. Two kernels: the first
-// takes an expert's 16 FN columns of h a workgroup, the second 16 FN columns of the result, with the
-// products of all experts added up in registers. Both find the experts from the ids by themselves, so
+// Bound by reading the weights of the experts that have a token, once each: one token, 8 experts of 2048 and
+// 2 x 1280 columns in bf16 (126 MB) 34 us, the kernels 20 and 12.5; four in 8 bits 50; 16 tokens, 4 of 32 experts
+// of 2048 and 2 x 2560 in 4 bits 67; 63 tokens, 2 of 32 experts of 2048 and 1344 in fp16 73 (of 2050 and 1337, rows at
+// odd addresses, 106). Two kernels: the first takes an expert's 16 FN columns of h a workgroup, the second 16 FN
+// columns of the result, with the products of all experts added up in registers. Both find the experts from the ids by themselves, so
 // nothing is sorted, counted or copied before, and the host needs to know nothing of the routing.
 //
 // The fragments of the matrix instructions come from memory to registers: a lane's 16 bytes of a

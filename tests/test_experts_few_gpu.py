@@ -123,6 +123,37 @@ def test_weights_of_two_kinds(up, down):
     check(experts.few_tokens(*args), *layer(*values, True, 2))
 
 
+def sharing(tokens, top_k, num, hidden, n, kind):
+    """The most workgroups that have a part of 16 columns (of 32, of up to 16 tokens in 4 bits) of the
+    result, from the size of their sums in the workspace."""
+    at = KINDS.index(kind)
+    wide = 32 if kind == "mx4" and tokens <= 16 else 16
+    tiles, step = -(-n // wide), 64 << at
+    rest = experts._workspace("experts_few_tokens_workspace_size", tokens, top_k, num, hidden, n, at)
+    for part in (tokens * top_k * 2 * -(-hidden // step) * step * 2, tiles * 4):
+        rest -= -(-part // 256) * 256
+    assert rest % (tiles * -(-tokens // 16) * wide * 64) == 0
+    return tiles, rest // (tiles * -(-tokens // 16) * wide * 64)
+
+
+# 256 workgroups that divide the tiles evenly: the ends of their shares lie within tiles.
+@pytest.mark.parametrize("kind,tokens,num,hidden,n,want", [
+    ("16", 40, 16, 1337, 2064, (129, 3)),
+    ("16", 9, 8, 2680, 2050, (129, 3)),
+    ("16", 40, 8, 1344, 5120, (320, 2)),
+    ("int8", 40, 16, 2677, 2064, (129, 3)),
+    ("int8", 5, 8, 2688, 2050, (129, 3)),
+    ("mx4", 40, 16, 2677, 5120, (320, 2)),
+    ("mx4", 16, 16, 2688, 4112, (129, 3)),
+    ("16", 3, 2, 64, 65552, (4097, 2)),
+])
+def test_equal_shares(kind, tokens, num, hidden, n, want):
+    assert sharing(tokens, 2, num, hidden, n, kind) == want
+    args, values = case(31, tokens, 2, num, 64, hidden, n, kind, torch.bfloat16, False, "all")
+    # (h's two parts: twice the products)
+    check(experts.few_tokens(*args, gated=False), *layer(*values, False, 2))
+
+
 @pytest.mark.parametrize("routing", ["one", "none"])
 @pytest.mark.parametrize("tokens", [1, 16, 64])
 def test_one_expert_for_all_and_none_at_all(routing, tokens):
