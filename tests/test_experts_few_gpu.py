@@ -3,8 +3,10 @@
 Tolerances, from the arithmetic alone. A 32-bit sum of m products is off by at most m steps of 2^-23 of
 the sum of their magnitudes (twice as many products where float16 tokens are split in two parts); each
 scale or weight is one more rounding of 2^-24. silu's slope is at most 1.1, and exp, the sum, the
-division and the product after it are within 8 + |a| steps of 2^-24 of their result. h and the result are
-rounded to the type once: half a step of the value, or half the smallest subnormal.
+division and the product after it are within 8 + |a| steps of 2^-24 of their result. The result is
+rounded to the type once: half a step of the value, or half the smallest subnormal. h is allowed as much;
+test_h_keeps_what_the_type_does_not holds it to two values of the type, of which the second is off by half a
+step of at most half a step.
 """
 from __future__ import annotations
 
@@ -35,10 +37,12 @@ def make(seed, kind, num, rows, k, dtype):
     return (q, powers), torch.from_numpy(values.copy()).cuda()
 
 
-def layer(x, up, down, ids, by, gated, split):
-    """The result in 64 bits and how far a result may be off before its own rounding."""
+def layer(x, up, down, ids, by, gated, split, step=None):
+    """The result in 64 bits and how far a result may be off before its own rounding; step: h's own,
+    relative to it."""
     dtype, num, hidden = x.dtype, up.shape[0], down.shape[2]
     info = torch.finfo(dtype)
+    step = info.eps / 2 if step is None else step
     out = torch.zeros(x.shape[0], down.shape[1], dtype=torch.float64, device="cuda")
     room, u = torch.zeros_like(out), 2.0**-24
     d = x.double()
@@ -56,7 +60,7 @@ def layer(x, up, down, ids, by, gated, split):
             if gated:
                 h = s * a[:, hidden:]
                 off_h = off_s * (a[:, hidden:].abs() + off[:, hidden:]) + s.abs() * off[:, hidden:]
-            off_h = off_h * (1 + info.eps) + h.abs() * (info.eps / 2) + info.smallest_normal * info.eps
+            off_h = off_h * (1 + info.eps) + h.abs() * step + info.smallest_normal * info.eps
             w, size = by[t, j].double().unsqueeze(1), down[e].abs().t().contiguous()
             out.index_add_(0, t, w * (h @ down[e].t().contiguous()))
             terms = 2 * split * hidden * ids.shape[1] + 2 * ids.shape[1] + 8
@@ -134,6 +138,15 @@ def sharing(tokens, top_k, num, hidden, n, kind):
         rest -= -(-part // 256) * 256
     assert rest % (tiles * -(-tokens // 16) * wide * 64) == 0
     return tiles, rest // (tiles * -(-tokens // 16) * wide * 64)
+
+
+@pytest.mark.parametrize("tokens,kind,dtype", [
+    (t, k, d) for t in (1, 12, 40) for k in KINDS for d in DTYPES])
+def test_h_keeps_what_the_type_does_not(tokens, kind, dtype):
+    """(4-bit weights take h in bfloat16 whatever the tokens' type.)"""
+    args, values = case(21, tokens, 2, 3, 64, 96, 40, kind, dtype, True)
+    eps = torch.finfo(torch.bfloat16 if kind == "mx4" else dtype).eps
+    check(experts.few_tokens(*args), *layer(*values, True, 2, (eps / 2)**2))
 
 
 # 256 workgroups that divide the tiles evenly: the ends of their shares lie within tiles.
