@@ -223,8 +223,8 @@ hist_status_t experts_few_tokens_workspace_size(uint64_t tokens, uint32_t top_k,
  *   h = silu(a) (gated 0), or (gated 1) silu of a's first half times its second.
  * up [experts][hidden or 2 hidden][width], down [experts][n][hidden]. ids: int32
  * or int64 (id_bits) [tokens][top_k]; an id outside [0, experts) adds nothing.
- * silu(a) = a / (1 + e^-a). Sums are held in 32 bits, h as the sum of two values of
- * 16 bits; the result is rounded once. Weights of an expert without a token are not read.
+ * silu(a) = a / (1 + e^-a). Sums and h are held in 32 bits, and the result is
+ * rounded once. Weights of an expert without a token are not read.
  * width and hidden are 8 or more, 16 for 8-bit weights; 64 of x's rows, and an
  * expert's rows of powers of two, lie within 2^31 bytes, and the weights' leading
  * dimensions are 2^25 at most (HIST_ERR_UNSUPPORTED otherwise).

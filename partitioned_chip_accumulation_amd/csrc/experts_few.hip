@@ -119,10 +119,9 @@ extern "C" hist_status_t experts_few_tokens(void *out, int64_t ldo, const void *
     g.by_tiles = Divide::by(p.tiles);
     g.by_groups = Divide::by(p.groups);
     g.by_waves = Divide::by(p.groups * kDownWaves);
-    g.by_steps = Divide::by((uint32_t)(g.ldh / 2 / (kStep / 2 << down->kind)));
+    g.by_steps = Divide::by((uint32_t)(g.ldh / 4 / (kStep / 2 << down->kind)));
     g.gated = (uint32_t)gated;
     g.h_shift = (uint32_t)down->kind;  // (of 16, 8 and 4 bits: 0, 1, 2)
-    g.h_fp16 = dtype == EXPERTS_FP16 && down->kind != EXPERTS_WEIGHT_MX4;
     return (dtype == EXPERTS_BF16 ? launch_few_bf16 : launch_few_fp16)(g, p, up->kind, down->kind,
                                                                       stream);
 }

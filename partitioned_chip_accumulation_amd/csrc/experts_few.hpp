@@ -13,7 +13,7 @@
 // The fragments of the matrix instructions come from memory to registers: a lane's 16 bytes of a
 // weight's row, 8, 16 or 32 values, are widened to the tokens' type there (exact: 8-bit whole numbers
 // and 4-bit values times a power of two have 8 bits at most), so that what is read is what the weights
-// take.
+// take. h is held in 32 bits between the two products, whatever the types, and all 24 of its bits are multiplied.
 #pragma once
 
 #include "experts_tile.hpp"
@@ -21,6 +21,7 @@
 namespace pca_experts {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kHalf = 64;  // bytes of a row that one load of a wave takes
 constexpr uint32_t kStep = 2 * kHalf;  // what the second kernel's waves share out
@@ -42,18 +43,33 @@ struct FewArgs {
     const void *ids;
     const float *by;
     int64_t ldo, ldx, ldh;  // bytes
-    uint32_t ids64, gated, h_fp16, h_shift, tokens, top_k, experts, width, hidden, n;
+    uint32_t ids64, gated, h_shift, tokens, top_k, experts, width, hidden, n;
     uint32_t tiles, groups, parts;  // of the result; workgroups, and the most of them that share a tile
     // (a kernel's first loads wait for its divisions)
     Divide by_top_k, by_up_tiles, by_tiles, by_groups, by_waves, by_steps;
 };
 
-// How weights of type W go with tokens of type T, and with the parts of h, of type H: C fragments of a
-// lane's 16 bytes.
+// The upper halves of values of 32 bits, two in a word.
+template <int N>
+__device__ __forceinline__ uint32_t __attribute__((ext_vector_type(N / 2)))
+upper(float __attribute__((ext_vector_type(N))) v)
+{
+    uint32_t __attribute__((ext_vector_type(N / 2))) two;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+        two[i] = __builtin_amdgcn_perm(__float_as_uint(v[2 * i + 1]), __float_as_uint(v[2 * i]), 0x07060302);
+    return two;
+}
+
+// How weights of type W go with tokens of type T, C fragments of a lane's 16 bytes, and with h, which is in
+// 32 bits: kParts if they are bfloat16 values exactly (part), which meet the three parts of h; float16 ones are
+// widened (wide) for the matrix instruction of 32-bit values, a sixteenth as fast. us in parts and that way: four
+// tokens in 8 bits 57 and 61, sixteen in 4 bits 74 and 94, in bf16 89 and 92. (float16 weights in two parts of
+// their own: 78 instead of 81 for 63 tokens of 2048 and 1344 columns, 111 instead of 107 of 2050 and 1337.)
 template <class T, class W> struct Widen;
 template <class T> struct Widen<T, T> {
     static constexpr int C = 1;
-    typedef T H;
+    static constexpr bool kParts = std::is_same<T, __bf16>::value;
     typedef typename Vec8<T>::type Frag;
     static __device__ __forceinline__ Frag frag(u32x4 v, int, uint32_t)
     {
@@ -63,28 +79,56 @@ template <class T> struct Widen<T, T> {
     {
         acc = Mma<T>::run(w, __builtin_bit_cast(Frag, a), acc);
     }
+    static __device__ __forceinline__ bf16x8 part(u32x4 v, int, uint32_t)
+    {
+        return __builtin_bit_cast(bf16x8, v);
+    }
+    static __device__ __forceinline__ f32x8 wide(u32x4 v, int)
+    {
+        const Frag w = __builtin_bit_cast(Frag, v);
+        f32x8 f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = (float)w[i];
+        return f;
+    }
 };
 template <class T> struct Widen<T, int8_t> {
     static constexpr int C = 2;
-    typedef T H;
+    static constexpr bool kParts = true;
     typedef typename Vec8<T>::type Frag;
     static __device__ __forceinline__ Frag frag(u32x4 v, int c, uint32_t)
     {
-        Frag f;
+        const f32x8 w = wide(v, c);
+        if constexpr (std::is_same<T, __bf16>::value) {
+            return __builtin_bit_cast(Frag, upper<8>(w));  // (8 bits: exact)
+        } else {
+            Frag f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] = (T)(float)(int8_t)(v[c * 2 + i / 4] >> i % 4 * 8);
-        return f;
+            for (int i = 0; i < 8; ++i) f[i] = (T)w[i];
+            return f;
+        }
     }
     static __device__ __forceinline__ void add(Frag w, u32x4 a, f32x4 &acc)
     {
         acc = Mma<T>::run(w, __builtin_bit_cast(Frag, a), acc);
     }
+    static __device__ __forceinline__ bf16x8 part(u32x4 v, int c, uint32_t power)
+    {
+        return Widen<__bf16, int8_t>::frag(v, c, power);
+    }
+    static __device__ __forceinline__ f32x8 wide(u32x4 v, int c)
+    {
+        f32x8 f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = (float)((int32_t)(v[c * 2 + i / 4] << (24 - i % 4 * 8)) >> 24);
+        return f;
+    }
 };
 // A block's values as bfloat16, whose exponents reach as far as the powers of two.
 template <class T> struct Widen<T, Mx4> {
     static constexpr int C = 4;
-    typedef __bf16 H;
+    static constexpr bool kParts = true;
     typedef bf16x8 Frag;
     static __device__ __forceinline__ Frag frag(u32x4 v, int c, uint32_t power)
     {
@@ -97,6 +141,10 @@ template <class T> struct Widen<T, Mx4> {
         const bf16x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[c], scale, 3);
         f = Frag{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
         return f;
+    }
+    static __device__ __forceinline__ bf16x8 part(u32x4 v, int c, uint32_t power)
+    {
+        return frag(v, c, power);
     }
     // A float16 value is the sum of two bfloat16 ones (11 bits, of 8 and 3), so two products have it
     // whole; float16 weights could not hold every power of two.
@@ -115,6 +163,24 @@ template <class T> struct Widen<T, Mx4> {
             }
             acc = Mma<__bf16>::run(w, high, acc);
             acc = Mma<__bf16>::run(w, low, acc);
+        }
+    }
+};
+
+// A value of 32 bits is the sum of three bfloat16 ones: its upper 16 bits, those of what is left, and what
+// is left then (8 of the 24 bits each). An infinity leaves NaN: its first part alone counts.
+template <int N>
+struct Parts {
+    typedef __bf16 Part __attribute__((ext_vector_type(N)));
+    Part part[3];
+    __device__ __forceinline__ Parts(float __attribute__((ext_vector_type(N))) v)
+    {
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            part[p] = __builtin_bit_cast(Part, upper<N>(v));
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                v[i] -= __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
         }
     }
 };
@@ -312,16 +378,25 @@ struct Window {
 // to be shifted (mend) before they are multiplied. The code is kept short: a pass over other experts' weights
 // leaves none of it in the caches, and kernels of 50 KB took 8 us for next to no work.
 //
-// OF_H: the tokens' rows are those of h, which lie as Rows has them.
-template <class T, class W, int RM, int FB, bool OF_H = false>
+// The tokens' rows can be those of h, which lie as Rows has them: the 32 bytes of a row that go with a fragment
+// are two words of a lane, or (kFolded) words of two lanes, so that one load has those of up to 8 pairs, the
+// second ones in the rows after the first ones. Then each matrix instruction takes all rows with half of a
+// fragment, and its sums count in the rows that this half belongs to (four tokens in 8 bits 54 us instead of 57,
+// one in 16 bits 34.6 instead of 35.5).
+enum Tokens { kOfX, kOfH, kFolded };
+template <class T, class W, int RM, int FB, Tokens OF = kOfX>
 struct Piece {
     typedef Widen<T, W> By;
     static constexpr int C = By::C;
-    static constexpr int kHalves = RM * C > 4 ? 1 : 2;  // (as registers allow)
+    static constexpr int kWords = OF == kOfH ? 2 : 1;  // 16-byte words of a lane that go with a fragment
+    static constexpr int kHalves = RM * C * kWords > 4 ? 1 : 2;  // (as registers allow)
+    // Sums of the words' products; in parts, those of the first part and then those of the others.
+    static constexpr int kOfWords = OF == kFolded ? 2 : 1;
+    static constexpr int kSums = OF != kOfX && By::kParts ? 2 * kOfWords : kOfWords;
     static constexpr uint32_t kBytes = kHalf * kHalves, kValues = kBytes / 16 * C * 8;  // of a row
     static constexpr bool kPowers = std::is_same<W, Mx4>::value;
     static constexpr uint32_t kStepPowers = kBytes / 16;
-    u32x4 b[FB][kHalves], a[RM][kHalves][C];
+    u32x4 b[FB][kHalves], a[RM][kHalves][C][kWords];
     uint64_t power[kPowers ? FB : 1];  // of a step's blocks, in lanes below 16
 
     static __device__ __host__ __forceinline__ uint32_t steps(uint32_t k)
@@ -351,7 +426,7 @@ struct Piece {
         const Window &tokens, &first, &second;  // b's fragments below FB / 2 (or 1) lie in the first
         const Window &powers;
         uint32_t a[RM], b[FB], p[FB];  // of rows; kNowhere: none
-        uint32_t unit;                 // of h: bytes of what goes with one fragment
+        uint32_t unit;                 // of h: bytes of the words of all its rows
         __device__ __forceinline__ const Window &of(int j) const
         {
             return j < (FB + 1) / 2 ? first : second;
@@ -370,15 +445,15 @@ struct Piece {
 #pragma unroll
             for (int j = 0; j < FB; ++j)
                 power[j] = s.powers.template load<kStepPowers>(s.p[j], step * kStepPowers);
-        if constexpr (OF_H) return fetch_h(s, step);
+        if constexpr (OF != kOfX) return fetch_h(s, step);
 #pragma unroll
         for (int h = 0; h < kHalves; ++h)
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int i = 0; i < RM; ++i)
-                    a[i][h][c] = s.tokens.load16(s.a[i] + lane * C * 16 + (h * 4 * C + c) * 16,
-                                                    step * kValues * 2);
+                    a[i][h][c][0] = s.tokens.load16(
+                        s.a[i] + lane * C * 16 + (h * 4 * C + c) * 16, step * kValues * 2);
     }
     __device__ __forceinline__ void fetch_h(const Source &s, uint32_t step)
     {
@@ -388,7 +463,10 @@ struct Piece {
             for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int i = 0; i < RM; ++i)
-                    a[i][h][c] = s.tokens.load16(s.a[i], ((step * kHalves + h) * C + c) * s.unit);
+#pragma unroll
+                    for (int q = 0; q < kWords; ++q)
+                        a[i][h][c][q] = s.tokens.load16(
+                            s.a[i], (((step * kHalves + h) * C + c) * kWords + q) * s.unit);
     }
     // The last step, of rows of k values.
     __device__ __forceinline__ void fetch_last(const Source &s, uint32_t step, uint32_t k)
@@ -404,7 +482,7 @@ struct Piece {
 #pragma unroll
             for (int j = 0; j < FB; ++j)
                 power[j] = s.powers.template load<kStepPowers>(s.p[j] + place_p(step, bytes / 16), 0);
-        if constexpr (OF_H) return fetch_h(s, step);
+        if constexpr (OF != kOfX) return fetch_h(s, step);
         const uint32_t room = k * 2;
 #pragma unroll
         for (int h = 0; h < kHalves; ++h)
@@ -412,7 +490,7 @@ struct Piece {
             for (int c = 0; c < C; ++c) {
                 const uint32_t at = place_a(step, h, c), in = at < room - 16 ? at : room - 16;
 #pragma unroll
-                for (int i = 0; i < RM; ++i) a[i][h][c] = s.tokens.load16(s.a[i] + in, 0);
+                for (int i = 0; i < RM; ++i) a[i][h][c][0] = s.tokens.load16(s.a[i] + in, 0);
             }
     }
 
@@ -452,35 +530,94 @@ struct Piece {
             for (int c = 0; c < C; ++c) {
                 const int left = (int)room - (int)place_a(step, h, c);
 #pragma unroll
-                for (int i = 0; i < RM; ++i) a[i][h][c] = drop16(a[i][h][c], left);
+                for (int i = 0; i < RM; ++i) a[i][h][c][0] = drop16(a[i][h][c][0], left);
             }
     }
 
-    __device__ __forceinline__ void multiply(f32x4 (&acc)[RM][FB]) const
+    // The power of this lane's block of b's fragment j.
+    __device__ __forceinline__ uint32_t own_power(int j, int h) const
     {
-        const uint32_t lane = threadIdx.x % 64;
+        if constexpr (!kPowers) return 0;
+        else {
+            const uint32_t lane = threadIdx.x % 64;
+            return __shfl((uint32_t)(power[j] >> h * 32), lane % 16, 64) >> lane / 16 * 8 & 0xff;
+        }
+    }
+    __device__ __forceinline__ void multiply(f32x4 (&acc)[kSums][RM][FB]) const
+    {
+        if constexpr (OF != kOfX) return multiply_h(acc);
 #pragma unroll
         for (int j = 0; j < FB; ++j)
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
-                uint32_t own = 0;
-                if constexpr (kPowers)
-                    own = __shfl((uint32_t)(power[j] >> h * 32), lane % 16, 64) >> lane / 16 * 8 & 0xff;
+                const uint32_t own = own_power(j, h);
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     const auto w = By::frag(b[j][h], c, own);
 #pragma unroll
-                    for (int i = 0; i < RM; ++i) {
-                        if constexpr (OF_H) {
-                            typedef typename By::H H;
-                            acc[i][j] = Mma<H>::run(
-                                w, __builtin_bit_cast(typename Vec8<H>::type, a[i][h][c]), acc[i][j]);
-                        } else {
-                            By::add(w, a[i][h][c], acc[i][j]);
+                    for (int i = 0; i < RM; ++i) By::add(w, a[i][h][c][0], acc[0][i][j]);
+                }
+            }
+    }
+    __device__ __forceinline__ void multiply_h(f32x4 (&acc)[kSums][RM][FB]) const
+    {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+            uint32_t own[FB];
+#pragma unroll
+            for (int j = 0; j < FB; ++j) own[j] = own_power(j, h);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int i = 0; i < RM; ++i) {
+                    const auto v = words(i, h, c);
+                    if constexpr (By::kParts) {
+                        const Parts<4 * kWords> parts(v);
+#pragma unroll
+                        for (int j = 0; j < FB; ++j) {
+                            const bf16x8 w = By::part(b[j][h], c, own[j]);
+#pragma unroll
+                            for (int p = 0; p < 3; ++p)
+#pragma unroll
+                                for (int q = 0; q < kOfWords; ++q) {
+                                    f32x4 &to = acc[(p ? kOfWords : 0) + q][i][j];
+                                    if constexpr (OF == kFolded)
+                                        to = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(
+                                            __builtin_bit_cast(s16x4, four(w, q)),
+                                            __builtin_bit_cast(s16x4, parts.part[p]), to, 0, 0, 0);
+                                    else
+                                        to = Mma<__bf16>::run(w, parts.part[p], to);
+                                }
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < FB; ++j) {
+                            const f32x8 w = By::wide(b[j][h], c);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                f32x4 &to = acc[q / 4 * (kOfWords - 1)][i][j];
+                                to = __builtin_amdgcn_mfma_f32_16x16x4f32(w[q], v[q % (4 * kWords)], to, 0, 0,
+                                                                          0);
+                            }
                         }
                     }
                 }
-            }
+        }
+    }
+    // What this lane has of h for a fragment.
+    typedef float Words __attribute__((ext_vector_type(4 * kWords)));
+    __device__ __forceinline__ Words words(int i, int h, int c) const
+    {
+        struct {
+            u32x4 word[kWords];
+        } v;
+#pragma unroll
+        for (int q = 0; q < kWords; ++q) v.word[q] = a[i][h][c][q];
+        return __builtin_bit_cast(Words, v);
+    }
+    static __device__ __forceinline__ bf16x4 four(bf16x8 w, int q)
+    {
+        return q ? __builtin_shufflevector(w, w, 4, 5, 6, 7) : __builtin_shufflevector(w, w, 0, 1, 2, 3);
     }
 };
 
@@ -515,63 +652,47 @@ __device__ __forceinline__ uint32_t share(uint32_t count, uint32_t at, uint32_t 
     return whole * at + by((count - whole * of) * at);
 }
 
-// h of a slot, in two parts of 16 bits, what 16 bits hold of it and of the rest: two rows for a pair, first all
-// pairs' first parts, then their second ones. (Rounded to one part, h added as much to the result's error as
-// the result's own rounding. A slot of up to 8 pairs, the usual one, still has no more than the 16 rows
-// that the matrix instructions take.) They lie in the order in which the second kernel's lanes
-// take them: for each 64 bytes of a weight's row (32 columns, or 64 and 128 of narrower weights) and each 8
-// columns that a lane's 16 bytes of them go with, the 16 bytes of every row for lanes 0 to 15, those
-// for lanes 16 to 31, and so on: 16 rows are 1 KB in one piece, 16 accesses instead of 64.
+// h of a slot, in 32 bits. It lies in the order in which the second kernel's lanes take it: for each 64 bytes of
+// a weight's row (32 columns, or 64 and 128 of narrower weights) and each 8 columns that a lane's 16 bytes of
+// them go with, first four columns of each, the 16 bytes of every row for lanes 0 to 15, those for lanes 16 to
+// 31, and so on, then the other four likewise: 16 rows are 1 KB in one piece, 16 accesses instead of 64.
 struct Rows {
     char *const base;
     const uint32_t count, shift;  // 2^shift fragments of columns go with 16 bytes of a weight
     __device__ __forceinline__ Rows(const FewArgs &g, uint32_t before, uint32_t count)
-        : base(g.h + (int64_t)before * 2 * g.ldh), count(count), shift(g.h_shift)
+        : base(g.h + (int64_t)before * g.ldh), count(count), shift(g.h_shift)
     {
     }
-    __device__ __forceinline__ uint32_t unit() const { return count * 128; }
-    __device__ __forceinline__ uint32_t part() const { return count * 16; }
-    // The place of a column of a pair, of its first part.
-    __device__ __forceinline__ char *at(uint32_t row, uint32_t c) const
+    // Few pairs are folded (see Piece): one after another, first all pairs' first four columns, then the others.
+    __device__ __forceinline__ bool folded() const { return count <= 8; }
+    __device__ __forceinline__ uint32_t unit() const { return count * (folded() ? 128 : 64); }
+    // The place of a column of a pair.
+    __device__ __forceinline__ float *at(uint32_t row, uint32_t c) const
     {
-        const uint32_t units = (c >> (5 + shift) << shift) + (c >> 3 & ((1u << shift) - 1));
+        const uint32_t fragment = (c >> (5 + shift) << shift) + (c >> 3 & ((1u << shift) - 1));
         const uint32_t lanes = c >> (3 + shift) & 3;
-        return base + units * unit() + (lanes * 2 * count + row) * 16 + c % 8 * 2;
+        const uint32_t word = c >> 2 & 1;
+        const uint32_t in = folded() ? (lanes * 2 + word) * count + row : (word * 4 + lanes) * count + row;
+        return (float *)(base + (fragment * 8 * count + in) * 16) + c % 4;
     }
     // Four columns, of which `left` exist.
-    template <class H>
     __device__ __forceinline__ void store(uint32_t row, uint32_t c, f32x4 v, uint32_t left) const
     {
-        typedef H H4 __attribute__((ext_vector_type(4)));
-        H4 high, low;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            high[q] = (H)v[q];
-            const float first = (float)high[q];
-            low[q] = (H)(__builtin_isfinite(first) ? v[q] - first : 0.f);  // (no NaN of an infinity)
-        }
-        char *const to = at(row, c);
+        float *const to = at(row, c);
         if (left >= 4) {
-            *(H4 *)to = high;
-            *(H4 *)(to + part()) = low;
+            *(f32x4 *)to = v;
         } else {
 #pragma unroll
             for (uint32_t q = 0; q < 3; ++q)
-                if (q < left) {
-                    ((H *)to)[q] = high[q];
-                    ((H *)(to + part()))[q] = low[q];
-                }
+                if (q < left) to[q] = v[q];
         }
     }
     // The second kernel reads whole steps: what the rows have from column `hidden` to `end` is 0.
     __device__ __forceinline__ void clear(uint32_t hidden, uint32_t end) const
     {
         const uint32_t wide = end - hidden;
-        for (uint32_t i = threadIdx.x; i < count * wide; i += blockDim.x) {
-            char *const to = at(i / wide, hidden + i % wide);
-            *(uint16_t *)to = 0;
-            *(uint16_t *)(to + part()) = 0;
-        }
+        for (uint32_t i = threadIdx.x; i < count * wide; i += blockDim.x)
+            *at(i / wide, hidden + i % wide) = 0.f;
     }
 };
 
@@ -611,7 +732,7 @@ __device__ __forceinline__ void up_rows(const FewArgs &g, uint32_t e, uint32_t n
         c += g.gated ? j / FN * g.hidden : 0;
         from.p[j] = lane < 16 ? c * (uint32_t)g.up.ld_scales : Window::kNowhere;
     }
-    f32x4 acc[RM][FB] = {};
+    f32x4 acc[1][RM][FB] = {};
     // the last step first: it may be ragged
     const uint32_t steps = P::steps(g.width);
     if (steps > wave) {
@@ -639,7 +760,7 @@ __device__ __forceinline__ void up_rows(const FewArgs &g, uint32_t e, uint32_t n
 #pragma unroll
     for (int i = 0; i < RM; ++i)
 #pragma unroll
-        for (int j = 0; j < FB; ++j) sums[(wave * RM * FB + i * FB + j) * 64 + lane] = acc[i][j];
+        for (int j = 0; j < FB; ++j) sums[(wave * RM * FB + i * FB + j) * 64 + lane] = acc[0][i][j];
     __syncthreads();
     const uint32_t columns = g.gated ? FN : FB;  // fragments of results
     for (uint32_t f = wave; f < RM * columns; f += 4) {
@@ -662,8 +783,7 @@ __device__ __forceinline__ void up_rows(const FewArgs &g, uint32_t e, uint32_t n
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = v[q] / (1.f + expf(-v[q]));
         if (g.gated) v *= sum(FN + j, g.hidden + c);
-        if (std::is_same<T, _Float16>::value && g.h_fp16) h.template store<_Float16>(r, c, v, g.hidden - c);
-        else h.template store<__bf16>(r, c, v, g.hidden - c);
+        h.store(r, c, v, g.hidden - c);
     }
 }
 
@@ -685,7 +805,7 @@ __global__ void __launch_bounds__(256) k_few_up(FewArgs g)
     uint32_t e, before;
     const uint32_t count = router.find(slot, mine, e, before);
     const Rows h(g, before, count);
-    if (n0 == 0 && (uint32_t)(g.ldh / 2) > g.hidden) h.clear(g.hidden, (uint32_t)(g.ldh / 2));
+    if (n0 == 0 && (uint32_t)(g.ldh / 4) > g.hidden) h.clear(g.hidden, (uint32_t)(g.ldh / 4));
     if (RM == 1 || count <= 16) up_rows<T, W, 1, FN, DEEP>(g, e, n0, mine, h, sums);
     else up_rows<T, W, RM, FN, DEEP>(g, e, n0, mine, h, sums);
 }
@@ -703,14 +823,15 @@ __device__ __forceinline__ float column_scale(float scale, int c)
     return __shfl(scale, threadIdx.x % 64 / 16 * 4 + c, 64);
 }
 
-// Some steps of one slot, the last one first: it may be ragged. R fragments hold the rows of h, two for a pair.
-template <class T, class W, int R, int FN, int DEEP, class O>
+// Some steps of one slot, the last one first: it may be ragged.
+template <class T, class W, int RM, int FN, int DEEP, Tokens OF, class O>
 __device__ __forceinline__ void down_rows(const FewArgs &g, const O &router, uint32_t e, uint32_t n0,
                                           uint32_t from, uint32_t some, const uint16_t *rows,
                                           const Rows &h, f32x4 *total)
 {
     constexpr bool kScales = std::is_same<W, int8_t>::value;
-    typedef Piece<T, W, R, FN, true> P;
+    typedef Piece<T, W, RM, FN, OF> P;
+    constexpr uint32_t kEach = P::kOfWords;  // rows of a pair
     // (the steps that are shared out are two of a piece of one half)
     const uint32_t steps = P::steps(g.hidden);
     if constexpr (P::kHalves == 1) {
@@ -718,7 +839,7 @@ __device__ __forceinline__ void down_rows(const FewArgs &g, const O &router, uin
         some = 2 * some < steps - from ? 2 * some : steps - from;
     }
     const uint32_t lane = threadIdx.x % 64, at = lane / 16, count = h.count;
-    const Window tokens(h.base, count * 2 * (uint32_t)g.ldh);
+    const Window tokens(h.base, count * (uint32_t)g.ldh);
     const char *const scales = g.down.scales + (int64_t)e * g.down.scales_stride;
     const Window powers(scales, g.down.window);
     const Window columns =
@@ -726,9 +847,9 @@ __device__ __forceinline__ void down_rows(const FewArgs &g, const O &router, uin
                      g.n - n0, row_bytes<W>(g.hidden));
     typename P::Source source = {tokens, columns, columns, powers, {}, {}, {}, h.unit()};
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
+    for (int i = 0; i < RM; ++i) {
         const uint32_t r = i * 16 + lane % 16;
-        source.a[i] = r < 2 * count ? (at * 2 * count + r) * 16 : Window::kNowhere;
+        source.a[i] = r < kEach * count ? (at * kEach * count + r) * 16 : Window::kNowhere;
     }
     float scale[kScales ? FN : 1];  // of column lane % 16
 #pragma unroll
@@ -739,7 +860,7 @@ __device__ __forceinline__ void down_rows(const FewArgs &g, const O &router, uin
         source.p[j] = lane < 16 ? c * (uint32_t)g.down.ld_scales : Window::kNowhere;
         if constexpr (kScales) scale[j] = ((const float *)scales)[c];
     }
-    f32x4 acc[R][FN] = {};
+    f32x4 acc[P::kSums][RM][FN] = {};
     P p[DEEP];
     const bool ragged = P::ragged(g.hidden) && from + some == steps;
     uint32_t next = from + some - 1;
@@ -759,7 +880,7 @@ __device__ __forceinline__ void down_rows(const FewArgs &g, const O &router, uin
              },
              [&](P &q) { q.multiply(acc); });
 #pragma unroll
-    for (int i = 0; i < (R + 1) / 2; ++i) {
+    for (int i = 0; i < RM; ++i) {
         const uint32_t r = i * 16 + lane % 16, pair = r < count ? rows[r] : 0, token = g.by_top_k(pair);
         const float by = router.weight(pair);
         f32x4 v[FN];
@@ -767,17 +888,18 @@ __device__ __forceinline__ void down_rows(const FewArgs &g, const O &router, uin
         for (int j = 0; j < FN; ++j)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                // the second part's row is in this fragment or a later one
-                float rest = 0.f;
-#pragma unroll
-                for (int q = i; q < R; ++q) {
-                    const float other =
-                        __shfl(acc[q][j][c], (int)(lane / 16 * 16 + (lane + count) % 16), 64);
-                    if ((r + count) / 16 == (uint32_t)q) rest = other;
+                // of an infinite h the first part counts; a folded pair's second word is in a row after its own
+                auto sum = [&](int s) {
+                    float v = acc[s * P::kOfWords][i][j][c];
+                    if constexpr (OF == kFolded)
+                        v += __shfl(acc[s * 2 + 1][i][j][c], (int)(lane / 16 * 16 + (lane + count) % 16), 64);
+                    return v;
+                };
+                v[j][c] = sum(0);
+                if constexpr (P::kSums > P::kOfWords) {
+                    const float rest = sum(1);
+                    if (__builtin_isfinite(v[j][c])) v[j][c] += rest;
                 }
-                // (of an infinite weight times a pair's two parts the first one counts)
-                v[j][c] = acc[i][j][c];
-                if (__builtin_isfinite(v[j][c])) v[j][c] += rest;
                 v[j][c] *= by;
                 if constexpr (kScales) v[j][c] *= column_scale(scale[j], c);
             }
@@ -841,10 +963,11 @@ __global__ void __launch_bounds__(WAVES * 64) k_few_down(FewArgs g)
             uint32_t e, before;
             const uint32_t count = router.find(slot, rows[wave], e, before);
             const Rows h(g, before, count);
-            if (count <= 8) down_rows<T, W, 1, FN, DEEP>(g, router, e, n0, from, some, rows[wave], h, total);
+            if (h.folded())
+                down_rows<T, W, 1, FN, DEEP, kFolded>(g, router, e, n0, from, some, rows[wave], h, total);
             else if (RM == 1 || count <= 16)
-                down_rows<T, W, 2, FN, DEEP>(g, router, e, n0, from, some, rows[wave], h, total);
-            else down_rows<T, W, 2 * RM, FN, DEEP>(g, router, e, n0, from, some, rows[wave], h, total);
+                down_rows<T, W, 1, FN, DEEP, kOfH>(g, router, e, n0, from, some, rows[wave], h, total);
+            else down_rows<T, W, RM, FN, DEEP, kOfH>(g, router, e, n0, from, some, rows[wave], h, total);
         }
         __syncthreads();
         auto store = [&](uint32_t f, f32x4 v) {
@@ -937,7 +1060,7 @@ inline uint64_t most_slots(uint64_t pairs, uint32_t experts, uint32_t rows)
 inline int64_t h_bytes(uint32_t hidden, int32_t down_kind)
 {
     const uint32_t values = kStep / 2 << down_kind;  // (16, 8 and 4 bits)
-    return ((int64_t)hidden + values - 1) / values * values * 2;
+    return ((int64_t)hidden + values - 1) / values * values * 4;
 }
 
 struct FewPlan {
@@ -976,7 +1099,7 @@ inline FewPlan few_plan(uint64_t tokens, uint32_t top_k, uint32_t experts, uint3
     p.parts = (p.groups + p.tiles - 1) / p.tiles + (p.groups % p.tiles && p.tiles % p.groups);
     auto up = [](uint64_t b) { return (b + 255) / 256 * 256; };
     p.h = 0;
-    p.arrived = up(pairs * 2 * h_bytes(hidden, down_kind));
+    p.arrived = up(pairs * h_bytes(hidden, down_kind));
     p.partial = p.arrived + up((uint64_t)p.tiles * 4);
     p.bytes = p.partial + (p.parts > 1 ? (uint64_t)p.tiles * p.parts * ((tokens + 15) / 16) * fn * 1024 : 0);
     return p;

@@ -533,7 +533,8 @@ def few_tokens(x: torch.Tensor, up, down, ids: torch.Tensor, weights: torch.Tens
     up is [experts, hidden (gated: 2 hidden), width] and down [experts, n, hidden]: a tensor of x's type,
     or a pair of int8 values and float32 scales [experts, rows], or a pair of 4-bit codes and powers of
     two as ``quantize_mx4`` makes them. ids (int32 or int64) and weights (float32) are [tokens, top_k]; an
-    id outside [0, experts) adds nothing. Weights of experts without a token are not read."""
+    id outside [0, experts) adds nothing. Weights of experts without a token are not read. a, h and all sums are
+    held in 32 bits, whatever the types, and the result is rounded once."""
     ldx = _matrix(x, "x")
     tokens, width = x.shape
     device = x.device

@@ -1,0 +1,162 @@
+"""What the layer for a few tokens keeps of h between its two products: the 32 bits it was computed in,
+whatever the tokens' type and the kind of weights.
+
+Tolerances, from the arithmetic alone, in units of u = 2^-24. a, a sum of `width` products (twice as many where
+float16 tokens meet 4-bit weights in two parts), is off by at most 2 (products + 2) u of the sum of their
+magnitudes. silu's slope is at most 1.1; exp, the sum, the division and the product after it are within 9 u of
+their result, and |a| more where a is negative (exp's argument is rounded, and for a > 0 e^-a is what counts less,
+by a e^-a < 0.4). h itself is allowed one u, the half step of 32 bits. Its products with `down` (up to six
+for one of them, of parts of both) and their sum are off by at most 2 (6 hidden + 8) u of the sum of their
+magnitudes. The result is rounded to the type once. No value here is so small that 32 bits lose it.
+"""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from partitioned_chip_accumulation_amd import experts
+from test_experts_few_gpu import KINDS, make
+from test_experts_gpu import normal
+
+pytestmark = pytest.mark.gpu
+DTYPES = [torch.bfloat16, torch.float16]
+U = 2.0**-24
+
+
+def definition(x, up, down, gated):
+    """One expert's layer in 64 bits, how far a result may be off before its own rounding, and h."""
+    hidden, d = down.shape[1], x.double()
+    a = d @ up.t().contiguous()
+    off = (d.abs() @ up.abs().t().contiguous()) * (2 * (2 * x.shape[1] + 2) * U)
+    gate, off_gate = a[:, :hidden], off[:, :hidden]
+    h = gate * torch.sigmoid(gate)
+    off_h = 1.1 * off_gate + h.abs() * (9 + (-gate).clamp(min=0)) * U
+    if gated:
+        other, off_other = a[:, hidden:], off[:, hidden:]
+        off_h = off_h * (other.abs() + off_other) + h.abs() * off_other
+        h = h * other
+    off_h = off_h + h.abs() * U
+    size = down.abs().t().contiguous()
+    room = off_h @ size + (h.abs() + off_h) @ size * (2 * (6 * hidden + 8) * U)
+    return h @ down.t().contiguous(), room, h
+
+
+def check(x, up, down, values, gated, room_most):
+    """room_most: the room of the results as a share of the largest of them, at most: a wrong result fails."""
+    tokens = x.shape[0]
+    ids = torch.zeros(tokens, 1, dtype=torch.int32, device="cuda")
+    got = experts.few_tokens(x, up, down, ids, torch.ones(tokens, 1, device="cuda"), gated=gated)
+    want, room, h = definition(x, values[0][0], values[1][0], gated)
+    info = torch.finfo(x.dtype)
+    assert float(room.max()) < room_most * float(want.abs().max())
+    room = room + want.abs() * (info.eps / 2) * 1.01 + info.smallest_normal * info.eps / 2
+    bad = ~((got.double() - want).abs() <= room)
+    assert not bad.any(), (int(bad.sum()), got[bad][:4], want[bad][:4], room[bad][:4])
+    return h
+
+
+def scaled(w, values, power):
+    """A weight and its values times 2^power."""
+    values = values * 2.0**power
+    if isinstance(w, torch.Tensor):
+        return (w.double() * 2.0**power).to(w.dtype), values
+    q, s = w
+    return (q, s * 2.0**power if s.dtype == torch.float32 else s + power), values
+
+
+@pytest.mark.parametrize("tokens", [1, 7, 16, 30])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_h_past_the_types_largest_value(dtype, kind, tokens):
+    """h near 100,000 (a = 300 and 300), results near 1000."""
+    width, hidden = 32, 64
+    x = torch.full((tokens, width), 300.0, dtype=dtype, device="cuda")
+    up, up_values = make(1, kind, 1, 2 * hidden, width, dtype)
+    # (rows of one non-zero value: 1 in each kind)
+    one = torch.zeros(2 * hidden, width, device="cuda", dtype=torch.float64)
+    one[:, 3] = 1.0
+    if kind == "16":
+        up = one.to(dtype).unsqueeze(0)
+    elif kind == "int8":
+        up = ((one * 64).to(torch.int8).unsqueeze(0), torch.full((1, 2 * hidden), 1 / 64, device="cuda"))
+    else:
+        up = tuple(t.unsqueeze(0) for t in experts.quantize_mx4(one.bfloat16()))
+    down, down_values = make(3, kind, 1, 48, hidden, dtype)
+    down, down_values = scaled(down, down_values, -7)
+    h = check(x, up, down, (one.unsqueeze(0), down_values), True, 1e-3)
+    assert (h > 65504 * 1.3).all()
+
+
+# (two values of float16 hold multiples of 2^-24; the weights of 16 bits stay within float16)
+@pytest.mark.parametrize("tokens", [1, 7, 16, 30])
+@pytest.mark.parametrize("kind,power,x_power", [
+    ("16", 4, 0), ("16", 8, -8), ("16", 13, -8), ("int8", 13, -8), ("int8", 30, 0), ("int8", -30, 0),
+    ("mx4", 13, -8), ("mx4", 30, 0), ("mx4", -30, 0)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_h_of_any_size(dtype, kind, power, x_power, tokens):
+    """up 2^-power times its size and down 2^power: ordinary results of an h that is small, or large. Without a
+    gate h is about a / 2 for small a, and 0 or a for large ones."""
+    width, hidden, n = 16, 16, 50
+    x = normal(5, tokens, width, dtype=dtype, scale=2.0**x_power)
+    up, up_values = scaled(*make(6, kind, 1, hidden, width, dtype), -power)
+    down, down_values = scaled(*make(8, kind, 1, n, hidden, dtype), power)
+    if kind == "16":  # (as they are rounded)
+        up_values, down_values = up.double(), down.double()
+    h = check(x, up, down, (up_values, down_values), False, 1e-3)
+    assert power < 0 or float(h.abs().max()) < 8 * 2.0**(x_power - power)
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 6, 10, 11, 16, 17, 30])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_differences_of_nearly_equal_columns(dtype, kind, tokens):
+    """Columns of h in pairs that differ by some 2^-13 of themselves, and a `down` that takes the differences:
+    values of 16 significant bits would have a tenth of them at best."""
+    width, pairs = 64, 48
+    x = torch.ones(tokens, width, dtype=dtype, device="cuda")
+    x += normal(9, tokens, width, dtype=dtype).abs()
+    x[:, 1] = 2.0**-12 * (1 + torch.arange(tokens, device="cuda") % 7).to(dtype)
+    # both of a pair have 1 for token columns 0 and 2; the second one has 0.5 for column 1 too
+    up = torch.zeros(2 * pairs, width, dtype=torch.float64, device="cuda")
+    up[:, 0], up[:, 2] = 1.0, 1.0
+    up[1::2, 1] = 0.5
+    down = torch.zeros(40, 2 * pairs, dtype=torch.float64, device="cuda")
+    at = torch.arange(40, device="cuda")
+    down[at, 2 * at], down[at, 2 * at + 1] = -1.0, 1.0
+
+    def weight(values):
+        if kind == "16":
+            return values.to(dtype).unsqueeze(0)
+        if kind == "int8":
+            return ((values * 2).to(torch.int8).unsqueeze(0),
+                    torch.full((1, values.shape[0]), 0.5, device="cuda"))
+        return tuple(t.unsqueeze(0) for t in experts.quantize_mx4(values.bfloat16()))
+
+    # (the sums here have three products that are not 0, each exact; rooms for all are too large)
+    ids = torch.zeros(tokens, 1, dtype=torch.int32, device="cuda")
+    got = experts.few_tokens(x, weight(up), weight(down), ids, torch.ones(tokens, 1, device="cuda"),
+                             gated=False)
+    a = x.double() @ up.t().contiguous()
+    h = a * torch.sigmoid(a)
+    want = h[:, 1:80:2] - h[:, 0:80:2]
+    # a > 0: two additions of 2 u each; silu's 9 u; h's own; the difference is of two such columns
+    each = 1.1 * a * 4 * U + h * 10 * U
+    room = each[:, 1:80:2] + each[:, 0:80:2] + want.abs() * (torch.finfo(dtype).eps / 2 * 1.01 + 8 * U)
+    info = torch.finfo(dtype)
+    room = room + info.smallest_normal * info.eps / 2
+    assert float((room / want.abs()).max()) < 0.25
+    bad = ~((got.double() - want).abs() <= room)
+    assert not bad.any(), (int(bad.sum()), got[bad][:4], want[bad][:4], room[bad][:4])
+
+
+@pytest.mark.parametrize("kind,up_power,down_power", [
+    ("mx4", -30, 30), ("mx4", 30, -30), ("mx4", -60, 60), ("mx4", 40, -40)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_powers_of_blocks_far_from_float16s_range(dtype, kind, up_power, down_power):
+    """4-bit weights whose powers of two float16 does not reach count in full for float16 tokens too. (h is
+    held in 32 bits, which reach as far as the powers.)"""
+    x = normal(11, 3, 64, dtype=dtype)
+    up, up_values = scaled(*make(12, kind, 1, 64, 64, dtype), up_power)
+    down, down_values = scaled(*make(14, kind, 1, 64, 64, dtype), down_power)
+    h = check(x, up, down, (up_values, down_values), False, 4e-3)
+    assert float(h.abs().max()) > 65504 if up_power > 0 else float(h.abs().max()) < 2.0**-24
