@@ -62,6 +62,62 @@ __device__ __forceinline__ void store8(T *p, typename Vec8<T>::type v, int left)
         if (i < left) p[i] = v[i];
 }
 
+typedef int8_t i8x8 __attribute__((ext_vector_type(8)));
+
+// f / scale to the nearest whole number, ties to even, for |f| up to 127 scale (scale > 0). The quotient
+// by the reciprocal is within 127 * 2^-23 = 0.000015 of the real one, so its rounding is right unless it lies
+// that near a half; only eights with such a value, and scales that have no normal reciprocal, take the way
+// that decides exactly (taken for every value, quantising was bound by its arithmetic: 8192 x 4096 in 30 us, not 28).
+struct Steps {
+    float scale, inverse;
+    bool normal;
+    explicit __device__ __forceinline__ Steps(float scale)
+        : scale(scale), normal(scale > 1e-37f && scale < 1e37f)
+    {
+        inverse = normal ? 1.0f / scale : 0.f;
+    }
+    __device__ __forceinline__ i8x8 operator()(const float (&f)[8]) const
+    {
+        float n[8], most = normal ? 0.f : 1.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float t = f[i] * inverse;
+            n[i] = rintf(t);
+            most = fmaxf(most, fabsf(t - n[i]));
+        }
+        if (most > 0.49998f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float m = rintf(f[i] / scale);
+                // What m leaves of f is exact in 32 bits: a multiple of the last bit of scale (or of f, if that
+                // is less than scale, and m 0 or 1), and no more than some half of scale. Comparing it with
+                // half the scale decides.
+                const float rest = __builtin_fmaf(-m, scale, f[i]);
+                const float twice = 2.f * fabsf(rest);
+                const bool odd = ((int)m & 1) != 0;
+                if (twice > scale || (twice == scale && odd)) m += rest > 0.f ? 1.f : -1.f;
+                n[i] = fminf(fmaxf(m, -127.f), 127.f);
+            }
+        }
+        i8x8 q;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = (int8_t)(int)n[i];
+        return q;
+    }
+};
+
+// Eight 8-bit values to p, of which `left` lie in the row.
+__device__ __forceinline__ void store8(int8_t *p, i8x8 v, int left)
+{
+    if (left >= 8) {
+        store_any(p, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) p[i] = v[i];
+}
+
 __device__ __forceinline__ void lds_add(uint32_t *lds, uint32_t slot, uint32_t v)
 {
     __hip_atomic_fetch_add(lds + slot, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);

@@ -13,7 +13,6 @@ __global__ void __launch_bounds__(256)
                const T *__restrict__ x, int64_t ldx, uint32_t rows, uint32_t k)
 {
     typedef typename Vec8<T>::type V;
-    typedef int8_t i8x8 __attribute__((ext_vector_type(8)));
     __shared__ uint32_t tops[4];
     const uint32_t r = blockIdx.x * (256 / THREADS) + threadIdx.x / THREADS;
     const uint32_t lane = threadIdx.x % THREADS;
@@ -54,48 +53,14 @@ __global__ void __launch_bounds__(256)
     const float scale = __uint_as_float(top) / 127.0f;
     const bool finite = top < 0x7f800000u && scale > 0.f;
     if (lane == 0) sx[r] = scale;
-    // The quotient by the reciprocal is within 127 * 2^-23 of the real one, so its rounding is
-    // right unless it lies next to a half; only pieces with such a value, and rows whose scale has no
-    // normal reciprocal, take the way that decides exactly (done for every value, the kernel was
-    // bound by its arithmetic: 8192 x 4096 in 30 us).
-    const bool normal = scale > 1e-37f && scale < 1e37f;
-    const float inverse = normal ? 1.0f / scale : 0.f;
+    const Steps steps(scale);
     auto quantize = [&](const V &v, uint32_t c) {
-        const int left = (int)(k - c);
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = (float)v[i];
         i8x8 q = {};
-        if (finite) {
-            float n[8];
-            bool near_half = !normal;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float t = (float)v[i] * inverse;
-                n[i] = rintf(t);
-                near_half |= fabsf(t - n[i]) > 0.4999f;
-            }
-            if (near_half) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float f = (float)v[i];
-                    float m = rintf(f / scale);
-                    // what m leaves of f is exact in 32 bits: comparing it with half the scale
-                    // decides
-                    const float rest = __builtin_fmaf(-m, scale, f);
-                    const float twice = 2.f * fabsf(rest);
-                    const bool odd = ((int)m & 1) != 0;
-                    if (twice > scale || (twice == scale && odd)) m += rest > 0.f ? 1.f : -1.f;
-                    n[i] = fminf(fmaxf(m, -127.f), 127.f);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = (int8_t)(int)n[i];
-        }
-        if (left >= 8) {
-            store_any(to + c, q);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < left) to[c + i] = q[i];
-        }
+        if (finite) q = steps(f);
+        store8(to + c, q, (int)(k - c));
     };
 #pragma unroll
     for (int s = 0; s < KEPT; ++s) {

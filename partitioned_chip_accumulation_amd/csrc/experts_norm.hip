@@ -165,7 +165,6 @@ __global__ void __launch_bounds__(THREADS > kBlock ? THREADS : kBlock) k_norm(No
         }
         for (uint32_t c = kFirst + lane * kCols; c < n; c += THREADS * kCols) put(again(c), c);
     } else {
-        typedef int8_t i8x8 __attribute__((ext_vector_type(8)));
         int8_t *y = (int8_t *)g.y + (int64_t)r * g.ldy;
         // As whole numbers, magnitudes order like floats, infinity and then NaN above all.
         uint32_t top = 0;
@@ -196,27 +195,11 @@ __global__ void __launch_bounds__(THREADS > kBlock ? THREADS : kBlock) k_norm(No
         const float scale = __uint_as_float(top) / 127.0f;
         if (lane == 0) g.sx[r] = scale;
         const bool finite = top < 0x7f800000u && scale > 0.f;
-        // y is a 32-bit result itself, so the quotient need not be exact next to a half; only a
-        // scale without a normal reciprocal (weights near 1e-36) divides.
-        const bool normal = scale > 1e-37f && scale < 1e37f;
-        const float steps = normal ? 1.0f / scale : 0.f;
+        const Steps steps(scale);
         auto put = [&](const float (&o)[8], uint32_t c) {
             i8x8 q = {};
-            if (finite) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float t = normal ? o[i] * steps : o[i] / scale;
-                    q[i] = (int8_t)(int)fminf(fmaxf(rintf(t), -127.f), 127.f);
-                }
-            }
-            const int left = (int)(n - c);
-            if (left >= 8) {
-                store_any(y + c, q);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < left) y[c + i] = q[i];
-            }
+            if (finite) q = steps(o);
+            store8(y + c, q, (int)(n - c));
         };
 #pragma unroll
         for (int s = 0; s < KEPT; ++s) {
