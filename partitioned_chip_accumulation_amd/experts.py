@@ -686,8 +686,9 @@ class _Norm(torch.autograd.Function):
 
 def norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
          eps: float = 1e-6) -> tuple[torch.Tensor, torch.Tensor]:
-    """``rms_norm`` with gradients for x, the weight and the residual. The gradient that h gets from
-    what follows is added to the norm's before the one rounding."""
+    """``rms_norm`` with gradients for x, the weight and the residual. With a residual, the gradient that h
+    gets from what follows is added to the norm's before the one rounding; without one h is x itself, and
+    autograd adds its gradient to the norm's, each of them rounded, and rounds the sum."""
     if residual is None:
         return _Norm.apply(x, weight, None, eps), x
     return _Norm.apply(x, weight, residual, eps)
