@@ -353,9 +353,10 @@ __device__ __forceinline__ void block_barrier()
     asm volatile("" : : : "memory");
 }
 
-// n / d for n < 2^30 and 1 <= d <= 64: mul = ceil(2^(31 + s) / d) with s =
-// floor(log2 d) exceeds the real quotient by less than 1, which moves n * mul by
-// less than 2^30 < 2^(31 + s) / d, so the floor is exact.
+// n / d for n < 2^30 and 1 <= d < 2^31: mul = ceil(2^(31 + s) / d) with s =
+// floor(log2 d) is at most 2^31 and exceeds the real quotient by less than 1, which
+// moves n * mul by less than 2^30 < 2^(31 + s) / d (as d < 2^(s + 1)), so the floor
+// is exact.
 struct Divide {
     uint32_t mul, shift;
     static Divide by(uint32_t d)
