@@ -1,12 +1,12 @@
 """What the layer for a few tokens keeps of h between its two products: the 32 bits it was computed in,
 whatever the tokens' type and the kind of weights.
 
-Tolerances, from the arithmetic alone, in units of u = 2^-24. a, a sum of `width` products (twice as many where
-float16 tokens meet 4-bit weights in two parts), is off by at most 2 (products + 2) u of the sum of their
-magnitudes. silu's slope is at most 1.1; exp, the sum, the division and the product after it are within 9 u of
+Tolerances, from the arithmetic alone, in units of u = 2^-24. a, a sum of m products that are not 0 (twice as many where
+float16 tokens meet 4-bit weights in two parts), is off by at most 2 (2 m + 2) u of the sum of their
+magnitudes (adding 0 rounds nothing). silu's slope is at most 1.1; exp, the sum, the division and the product after it are within 9 u of
 their result, and |a| more where a is negative (exp's argument is rounded, and for a > 0 e^-a is what counts less,
 by a e^-a < 0.4). h itself is allowed one u, the half step of 32 bits. Its products with `down` (up to six
-for one of them, of parts of both) and their sum are off by at most 2 (6 hidden + 8) u of the sum of their
+for one of them, of parts of both) and their sum are off by at most 2 (6 m + 8) u of the sum of their
 magnitudes. The result is rounded to the type once. No value here is so small that 32 bits lose it.
 """
 from __future__ import annotations
@@ -27,7 +27,8 @@ def definition(x, up, down, gated):
     """One expert's layer in 64 bits, how far a result may be off before its own rounding, and h."""
     hidden, d = down.shape[1], x.double()
     a = d @ up.t().contiguous()
-    off = (d.abs() @ up.abs().t().contiguous()) * (2 * (2 * x.shape[1] + 2) * U)
+    products = int((x != 0).sum(1).max())
+    off = (d.abs() @ up.abs().t().contiguous()) * (2 * (2 * products + 2) * U)
     gate, off_gate = a[:, :hidden], off[:, :hidden]
     h = gate * torch.sigmoid(gate)
     off_h = 1.1 * off_gate + h.abs() * (9 + (-gate).clamp(min=0)) * U
@@ -37,7 +38,8 @@ def definition(x, up, down, gated):
         h = h * other
     off_h = off_h + h.abs() * U
     size = down.abs().t().contiguous()
-    room = off_h @ size + (h.abs() + off_h) @ size * (2 * (6 * hidden + 8) * U)
+    products = int((h != 0).sum(1).max())
+    room = off_h @ size + (h.abs() + off_h) @ size * (2 * (6 * products + 8) * U)
     return h @ down.t().contiguous(), room, h
 
 
@@ -106,7 +108,8 @@ def test_h_of_any_size(dtype, kind, power, x_power, tokens):
     assert power < 0 or float(h.abs().max()) < 8 * 2.0**(x_power - power)
 
 
-@pytest.mark.parametrize("tokens", [1, 5, 6, 10, 11, 16, 17, 30])
+# (how an expert's rows lie changes after 8, 16 and 32 of them)
+@pytest.mark.parametrize("tokens", [1, 5, 8, 9, 15, 16, 17, 31, 32, 33, 64])
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_differences_of_nearly_equal_columns(dtype, kind, tokens):
@@ -160,3 +163,30 @@ def test_powers_of_blocks_far_from_float16s_range(dtype, kind, up_power, down_po
     down, down_values = scaled(*make(14, kind, 1, 64, 64, dtype), down_power)
     h = check(x, up, down, (up_values, down_values), False, 4e-3)
     assert float(h.abs().max()) > 65504 if up_power > 0 else float(h.abs().max()) < 2.0**-24
+
+
+@pytest.mark.parametrize("tokens", [2, 9, 40])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_the_widest(dtype, kind, tokens):
+    """2^17 columns of x, of h and of the result, which is all that a call takes."""
+    most = 2**17
+    for width, hidden, n in ((most, 16, 16), (16, most, 16), (16, 16, most), (most - 3, 40, 3),
+                             (40, most - 9, 3)):
+        x = normal(21, tokens, width, dtype=dtype)
+        up, up_values = make(22, kind, 1, hidden, width, dtype)
+        down, down_values = make(24, kind, 1, n, hidden, dtype)
+        # 24 columns of a wide x or h are not 0, the first and the last ones among them
+        some = torch.randperm(most, generator=torch.Generator().manual_seed(26))
+        for rows, wide in ((x, width), (up if kind == "16" else up[0], hidden)):
+            if wide < 100:
+                continue
+            keep = torch.cat([some[some < wide][:16], torch.arange(4), wide - 1 - torch.arange(4)]).cuda()
+            gone = torch.ones(wide, dtype=torch.bool, device="cuda").index_fill_(0, keep, False)
+            if rows is x:
+                x[:, gone] = 0
+            else:  # (8 bits and 4: codes of 0)
+                rows[0, gone] = 0
+                up_values[0, gone] = 0
+        h = check(x, up, down, (up_values, down_values), False, 1e-2)
+        assert (h != 0).any(1).all()
