@@ -4,11 +4,12 @@
 //   h[t, e] = act(x[t] up[e]^T),  out[t] = sum over t's experts e of weight[t, e] h[t, e] down[e]^T
 //
 // Bound by reading the weights of the experts that have a token, once each: one token, 8 experts of 2048 and
-// 2 x 1280 columns in bf16 (126 MB) 34 us, the kernels 20 and 12.5; four in 8 bits 50; 16 tokens, 4 of 32 experts
-// of 2048 and 2 x 2560 in 4 bits 67; 63 tokens, 2 of 32 experts of 2048 and 1344 in fp16 73 (of 2050 and 1337, rows at
-// odd addresses, 106). Two kernels: the first takes an expert's 16 FN columns of h a workgroup, the second 16 FN
-// columns of the result, with the products of all experts added up in registers. Both find the experts from the ids by themselves, so
-// nothing is sorted, counted or copied before, and the host needs to know nothing of the routing.
+// 2 x 1280 columns in bf16 (126 MB) 34.5 us, the kernels' medians 21.6 and 15.9 (traced); four in 8 bits 51; 16
+// tokens, 4 of 32 experts of 2048 and 2 x 2560 in 4 bits 71; 63 tokens, 2 of 32 experts of 2048 and 1344 in fp16
+// 80 (of 2050 and 1337, rows at odd addresses, 107). Two kernels: the first takes an expert's 16 FN columns of h
+// a workgroup, the second 16 FN columns of the result, with the products of all experts added up in registers.
+// Both find the experts from the ids by themselves, so nothing is sorted, counted or copied before, and the host
+// needs to know nothing of the routing.
 //
 // The fragments of the matrix instructions come from memory to registers: a lane's 16 bytes of a
 // weight's row, 8, 16 or 32 values, are widened to the tokens' type there (exact: 8-bit whole numbers
@@ -1030,12 +1031,13 @@ __global__ void __launch_bounds__(WAVES * 64) k_few_down(FewArgs g)
 }
 
 // ---------------------------------------------------------------------------
-// Steps that a wave has on their way (four: 34.7 us instead of 33.1 for one token in 16 bits).
+// Steps that a wave has on their way (four: 35.7 us instead of 34.5 for one token in 16 bits, 56.5 instead of 51
+// for four in 8).
 constexpr int kDeep = 2;
 constexpr int kDownWaves = 8;  // of a workgroup of the second kernel
 
 // Fragments of columns of a workgroup (FN): two for 4-bit weights, whose tokens' rows count for more of what
-// is loaded, if there are no more than 16 of them (67 us instead of 70 for 16 tokens; 53 instead of 49 for
+// is loaded, if there are no more than 16 of them (71 us instead of 73.5 for 16 tokens; 55 instead of 51 for
 // four tokens in 8 bits).
 template <class W, int RM> constexpr int few_columns()
 {
@@ -1080,10 +1082,9 @@ inline FewPlan few_plan(uint64_t tokens, uint32_t top_k, uint32_t experts, uint3
                            : down_kind == EXPERTS_WEIGHT_INT8 ? hidden
                                                               : (hidden + 31) / 32 * 16;
     // Either a tile for `sharing` whole workgroups, or 256 workgroups with equal shares of all tiles. What
-    // a workgroup does once a part costs it as much as reading 64 KB or so. us with whole ones (seven or eight a
-    // tile; four of 320) and with equal shares: 129 tiles of 1.4 MB 70 and 61, 224 of 0.7 MB 106 and 85, 320 of 0.7 MB
-    // 131 and 118; 65 of 0.3 MB 26 and 30; 1024 of 0.1 MB 70 (one a tile) and 74. Two steps of 128 bytes
-    // for each wave are the least.
+    // a workgroup does once a part costs it as much as reading 64 KB or so. us with whole ones and with equal
+    // shares: 129 tiles of 0.8 MB 68 and 63, 224 83 and 87, 320 155 and 121, 512 175 and 174; 65 of 0.3 MB 26
+    // and 30. Two steps of 128 bytes for each wave are the least.
     constexpr uint64_t kOnce = 65536;
     const uint64_t tile = slots * bytes * 16 * fn, steps = slots * ((bytes + 127) / 128) / (2 * kDownWaves);
     const uint64_t most = steps < 1 ? 1 : steps < 64 ? steps : 64;

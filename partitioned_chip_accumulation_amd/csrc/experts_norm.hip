@@ -7,7 +7,9 @@
 // All are bound by memory: each row is read once and kept in registers between its sums and its
 // results. 16384 rows of 4096 in bf16, with the residual and h: 93-98 us, 5.5-5.8 TB/s (a large copy runs at
 // 5.1); 8192 of them to 8 bits: 45 us, 5.3 TB/s; the gradients of 8191 rows of 2048: 27-29 us, 4.6-5.0 TB/s,
-// and 4 for the groups' sums; 32 rows of 4096: 5.3 us, the launch and a row's latency.
+// and 4 for the groups' sums; 32 rows of 4096: 5.4-6 us, the launch and a row's latency. Rows of fewer than 512
+// columns leave lanes of their wave without work: 67 MB of rows of 512, 256, 128 and 64 columns with the residual
+// and h take 42, 53, 90 and 164 us, their gradients 58, 93, 165 and 310.
 #include "experts_common.hpp"
 
 namespace pca_experts {

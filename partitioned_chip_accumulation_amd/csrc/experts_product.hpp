@@ -1104,7 +1104,10 @@ enum class RowsKernel {
 //   16 experts, 128      208    90.4   75.9    64.2     69.2     66.1     51.7
 //   16 experts, 512      739     258    213     181      135      139      121
 // So 64 x 64 for few rows (the reduction is half as long as in 8 bits, and a wave that has it alone spends
-// more on powers than on codes), and one round of the largest tiles sooner.
+// more on powers than on codes), and one round of the largest tiles sooner. Few columns and a long reduction leave
+// most CUs without a workgroup, as nothing divides the reduction: 128 to 1024 columns, one row and 16, and the
+// product in 8 bits: of 8192 10.8, 10.9; 8.8, 21 (the calls take 9 to 11), of 32768 28, 28; 20, 75, of 131072 118,
+// 123; 71, 292.
 template <bool ACROSS, bool POWERS = false>
 RowsKernel rows_kernel(const RowsArgs &g)
 {
